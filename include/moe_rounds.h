@@ -87,7 +87,9 @@ typedef enum {
   MOE_ERR_HIP = 4
 } moe_status_t;
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype_t;
+/* MOE_F16 (IEEE half precision) is an element type of the ragged expert
+ * operators at the end of this header; a layer config takes the other two. */
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 } moe_dtype_t;
 
 /* Layout of w_gate, w_up and w_down as the calls below read them:
  *   MOE_WEIGHTS_ROW_MAJOR  [E][out][in] row-major, as documented above;
@@ -495,6 +497,122 @@ moe_status_t moe_backward(const moe_config_t *cfg, const void *x,
                           float *dw_gate, float *dw_up, float *dw_down,
                           const void *ws, size_t ws_bytes, void *bws,
                           size_t bws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Ragged expert operators: the experts' products without rounds. They work
+ * on rows sorted by expert, in a buffer of any number of rows: expert e owns
+ * the rows offsets[e] <= i < offsets[e + 1]. offsets is int32 [E + 1] on the
+ * device, non-decreasing: the `offsets` of moe_plan's workspace, whose `perm`
+ * lists the assignments in that order and whose `z` rows are in it (so a
+ * product may write z for moe_combine), or a program's own. Experts may have
+ * no rows. Rows below offsets[0] and from offsets[E] on belong to nobody:
+ * they are not read, and outputs keep what they held there.
+ *
+ * Nothing here allocates, waits or keeps state: every call enqueues its
+ * launches on `stream` and can be captured into a graph. The sizes that
+ * shape a launch are on the host, the offsets only on the device; offsets
+ * are clamped to [0, rows], so wrong ones give wrong results but no access
+ * outside the buffers. Outputs must not overlap inputs. Matrices are
+ * row-major with a row stride of ld elements (0 means the width); unlike in
+ * the layer's calls, addresses only need the alignment of an element (16
+ * bytes for the 4-bit format). 16-byte aligned rows are faster.
+ *
+ * elem below is fp32, bf16 or fp16 (MOE_F32, MOE_BF16, MOE_F16). Products
+ * run on the matrix cores with fp32 accumulation and round each output once.
+ * Infinities and NaN follow the arithmetic: they reach exactly the outputs
+ * whose sums contain them. Results do not depend on how rows are grouped
+ * into tiles or calls, and repeat bit for bit. */
+
+/* rows: rows of the buffers; w: E matrices [N][K] (out x in), contiguous;
+ * x and dx: [rows][K] at ld_x; y and dy: [rows][N] at ld_y. Limits: rows <
+ * 2^31, E <= 1024, N*K < 2^29, ld_x and ld_y at most 2^20, at most 2^23
+ * output tiles of 128 x 128 (MOE_ERR_UNSUPPORTED otherwise). */
+typedef struct {
+  int64_t rows;
+  int32_t E, N, K;
+  int32_t dtype;       /* moe_dtype_t of x, w, y (and of dx, dy) */
+  int64_t ld_x, ld_y;  /* row strides in elements, 0: K and N */
+} moe_grouped_t;
+
+/* y[i] = w[e] x[i] for the rows i of every expert e. */
+moe_status_t moe_grouped_gemm(const moe_grouped_t *g, const int32_t *offsets,
+                              const void *x, const void *w, void *y,
+                              void *stream);
+
+/* The gradient with respect to x: dx[i] = w[e]^T dy[i]. */
+moe_status_t moe_grouped_gemm_dx(const moe_grouped_t *g, const int32_t *offsets,
+                                 const void *dy, const void *w, void *dx,
+                                 void *stream);
+
+/* The gradient with respect to w: dw[e] = sum over e's rows of dy[i] x[i]^T,
+ * fp32 [E][N][K], contiguous. accumulate = 0 stores dw in full (zeros for an
+ * expert without rows), 1 adds to it. ws: moe_grouped_dw_workspace_size bytes
+ * (which may be 0: then it is not used and may be NULL), 16-byte aligned; the
+ * sums of an expert with many rows are split over it and joined in a fixed
+ * order. The size is a pure function of g. Calls that may overlap in time,
+ * replays of two captured graphs among them, need a workspace each. */
+moe_status_t moe_grouped_dw_workspace_size(const moe_grouped_t *g, size_t *bytes);
+moe_status_t moe_grouped_gemm_dw(const moe_grouped_t *g, const int32_t *offsets,
+                                 const void *x, const void *dy, float *dw,
+                                 int32_t accumulate, void *ws, size_t ws_bytes,
+                                 void *stream);
+
+/* The activation between the products and its gradient. gu: elem
+ * [rows][2f], g then u; h: elem [rows][f] = silu(g) u with silu(g) = g s, s =
+ * 1 / (1 + e^-g); dgu: elem [rows][2f] = [dh u s (1 + g (1 - s)), dh g s].
+ * n_rows: NULL, or one int32 on the device: only rows below it are read and
+ * written (offsets + E for rows sorted by expert). 2f, ld <= 2^20. */
+moe_status_t moe_swiglu(int32_t dtype, int64_t rows, int64_t f, const void *gu,
+                        int64_t ld_gu, void *h, int64_t ld_h,
+                        const int32_t *n_rows, void *stream);
+moe_status_t moe_swiglu_backward(int32_t dtype, int64_t rows, int64_t f,
+                                 const void *gu, int64_t ld_gu, const void *dh,
+                                 int64_t ld_dh, void *dgu, int64_t ld_dgu,
+                                 const int32_t *n_rows, void *stream);
+
+/* Microscaled 4-bit floating point (MXFP4). A row of K values, K a multiple
+ * of MOE_MXFP4_BLOCK, is
+ *   codes   K / 2 bytes: value c in the low (c even) or high half of byte
+ *           c / 2; bit 3 the sign, bits 0-2 the magnitudes 0, 0.5, 1, 1.5,
+ *           2, 3, 4, 6
+ *   scales  one byte b per block of 32 values, which are the coded ones
+ *           times 2^(b - 127); 255 makes the block NaN. A row of scales is
+ *           moe_mxfp4_scale_stride(K) bytes (K / 32 rounded up to 4; -1 for
+ *           an invalid K); the bytes past K / 32 are written as 0 and their
+ *           content is never used.
+ * Rows of both are contiguous, the arrays 16-byte aligned. */
+#define MOE_MXFP4_BLOCK 32
+int64_t moe_mxfp4_scale_stride(int64_t K);
+
+/* elem rows to MXFP4: b = floor(log2(the block's largest magnitude)) - 2 +
+ * 127, at least 0 (0 for a block of zeros); values rounded to nearest, ties
+ * to the even code, ending at 6 times the scale. A block with an infinity or
+ * a NaN gets b = 255 and codes 0. index NULL: row i of the output is row i of
+ * x (at least `rows` rows). Otherwise it is row index[i] / index_div of x
+ * (src_rows rows; int32 on the device), zeros where index[i] is negative or
+ * names no row: with moe_plan's perm and index_div = k, tokens in expert
+ * order. Weights are E*N rows. n_rows as for moe_swiglu. */
+moe_status_t moe_mxfp4_quantize(int32_t dtype, int64_t rows, int64_t K,
+                                const void *x, int64_t ld_x, int64_t src_rows,
+                                const int32_t *index, int32_t index_div,
+                                const int32_t *n_rows, uint8_t *codes,
+                                uint8_t *scales, void *stream);
+
+/* The values, rounded to elem (bf16 and fp32 hold every one of them). */
+moe_status_t moe_mxfp4_dequantize(int32_t dtype, int64_t rows, int64_t K,
+                                  const uint8_t *codes, const uint8_t *scales,
+                                  void *y, int64_t ld_y, const int32_t *n_rows,
+                                  void *stream);
+
+/* moe_grouped_gemm on MXFP4 operands: x of `rows` rows, w of E*N rows, K
+ * values each (a multiple of 32; g->ld_x 0 or K). y has g->dtype. */
+moe_status_t moe_mxfp4_grouped_gemm(const moe_grouped_t *g,
+                                    const int32_t *offsets,
+                                    const uint8_t *x_codes,
+                                    const uint8_t *x_scales,
+                                    const uint8_t *w_codes,
+                                    const uint8_t *w_scales, void *y,
+                                    void *stream);
 
 #ifdef __cplusplus
 }

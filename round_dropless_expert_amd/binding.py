@@ -25,6 +25,7 @@ MOE_ERR_HIP = 4
 
 MOE_F32 = 0
 MOE_BF16 = 1
+MOE_F16 = 2  # ragged expert operators only
 
 MOE_WEIGHTS_ROW_MAJOR = 0
 MOE_WEIGHTS_TILED = 1
@@ -37,7 +38,11 @@ EXPORTS = ("moe_status_string", "moe_last_error", "moe_hip_runtime_version",
            "moe_expert_down", "moe_dispatch_gate_up", "moe_pack_weights", "moe_combine", "moe_forward",
            "moe_capacity_curve", "moe_capacity_for_rounds",
            "moe_backward_workspace_size", "moe_backward_layout",
-           "moe_backward", "moe_forward_static")
+           "moe_backward", "moe_forward_static",
+           "moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw",
+           "moe_grouped_dw_workspace_size", "moe_swiglu", "moe_swiglu_backward",
+           "moe_mxfp4_scale_stride", "moe_mxfp4_quantize", "moe_mxfp4_dequantize",
+           "moe_mxfp4_grouped_gemm")
 
 
 class MoeConfig(ctypes.Structure):
@@ -64,6 +69,13 @@ BWD_LAYOUT_FIELDS = ("xr", "dyr", "gu", "hw", "dgu", "dz", "ones")
 class MoeBackwardLayout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in BWD_LAYOUT_FIELDS] + \
         [("total", ctypes.c_size_t)]
+
+
+class MoeGrouped(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("E", ctypes.c_int32),
+                ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("ld_x", ctypes.c_int64),
+                ("ld_y", ctypes.c_int64)]
 
 
 class MoeError(RuntimeError):
@@ -119,7 +131,22 @@ def load() -> ctypes.CDLL:
     L.moe_backward_layout.argtypes = [cfgp, ctypes.POINTER(MoeBackwardLayout)]
     L.moe_backward.argtypes = [cfgp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                vp, sz, vp, sz, vp]
-    for n in ("moe_check_config", "moe_workspace_size", "moe_forward_workspace_size",
+    gp = ctypes.POINTER(MoeGrouped)
+    L.moe_grouped_gemm.argtypes = [gp, vp, vp, vp, vp, vp]
+    L.moe_grouped_gemm_dx.argtypes = [gp, vp, vp, vp, vp, vp]
+    L.moe_grouped_dw_workspace_size.argtypes = [gp, ctypes.POINTER(ctypes.c_size_t)]
+    L.moe_grouped_gemm_dw.argtypes = [gp, vp, vp, vp, vp, i32, vp, sz, vp]
+    L.moe_swiglu.argtypes = [i32, i64, i64, vp, i64, vp, i64, vp, vp]
+    L.moe_swiglu_backward.argtypes = [i32, i64, i64, vp, i64, vp, i64, vp, i64, vp, vp]
+    L.moe_mxfp4_scale_stride.argtypes = [i64]
+    L.moe_mxfp4_scale_stride.restype = i64
+    L.moe_mxfp4_quantize.argtypes = [i32, i64, i64, vp, i64, i64, vp, i32, vp, vp, vp, vp]
+    L.moe_mxfp4_dequantize.argtypes = [i32, i64, i64, vp, vp, vp, i64, vp, vp]
+    L.moe_mxfp4_grouped_gemm.argtypes = [gp, vp, vp, vp, vp, vp, vp, vp]
+    for n in ("moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw",
+              "moe_grouped_dw_workspace_size", "moe_swiglu", "moe_swiglu_backward",
+              "moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_grouped_gemm",
+              "moe_check_config", "moe_workspace_size", "moe_forward_workspace_size",
               "moe_workspace_layout",
               "moe_plan", "moe_launch_batches", "moe_dispatch", "moe_expert_ffn",
               "moe_expert_gate_up", "moe_expert_down", "moe_dispatch_gate_up",
@@ -444,6 +471,199 @@ def capacity_for_rounds(cfg: MoeConfig, counts, target_rounds=1,
         ctypes.byref(cfg), a.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)),
         a.shape[0], int(target_rounds), float(quantile), ctypes.byref(out)))
     return out.value
+
+
+# ---------------------------------------------------------------------------
+# Ragged expert operators (the last section of the header): rows sorted by
+# expert, expert e owning the rows offsets[e] .. offsets[e + 1] - 1.
+
+_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
+_TORCH_DTYPES = {v: k for k, v in _DTYPES.items()}
+
+
+def grouped(rows, E, N, K, dtype, ld_x=0, ld_y=0) -> MoeGrouped:
+    """Shape of a grouped product: weights [E, N, K], buffers of `rows` rows
+    with row strides ld_x and ld_y in elements (0: K and N)."""
+    if isinstance(dtype, str):
+        dtype = {"f32": MOE_F32, "bf16": MOE_BF16, "f16": MOE_F16}[dtype]
+    elif isinstance(dtype, torch.dtype):
+        dtype = _DTYPES[dtype]
+    return MoeGrouped(int(rows), int(E), int(N), int(K), int(dtype), int(ld_x),
+                      int(ld_y))
+
+
+def grouped_dw_workspace_size(g: MoeGrouped) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().moe_grouped_dw_workspace_size(ctypes.byref(g), ctypes.byref(n)))
+    return n.value
+
+
+def mxfp4_scale_stride(K: int) -> int:
+    """Bytes of a row of MXFP4 scales."""
+    n = load().moe_mxfp4_scale_stride(int(K))
+    if n < 0:
+        raise ValueError(f"K = {K} must be a positive multiple of 32")
+    return n
+
+
+def _on_device(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor or an int address")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a device (cuda) tensor, got {t.device}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _dense(t, name, dtype, numel):
+    """_arg for a tensor that must live on the current device."""
+    if t is None or isinstance(t, int):
+        return t
+    _on_device(t, name)
+    return _arg(t, name, dtype, numel)
+
+
+def _mat(t, name, dtype, rows, cols, ld):
+    """Address of a [rows, cols] matrix whose rows are ld elements apart."""
+    if t is None or isinstance(t, int):
+        return t
+    _on_device(t, name)
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected ({rows}, {cols})")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: elements of a row must be adjacent")
+    if rows > 1 and t.stride(0) != ld:
+        raise ValueError(f"{name}: row stride {t.stride(0)}, expected {ld}")
+    return t.data_ptr()
+
+
+def _rows_of(t, name):
+    """(dtype, rows, width, row stride) of a matrix argument."""
+    _on_device(t, name)
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a matrix, got {t.dim()} dimensions")
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name}: dtype {t.dtype} is not supported")
+    r, c = t.shape
+    if c > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: elements of a row must be adjacent")
+    ld = t.stride(0) if r > 1 else c
+    if ld < c:
+        raise ValueError(f"{name}: rows overlap (row stride {ld}, width {c})")
+    return t.dtype, r, c, ld
+
+
+def _offsets(offsets, E):
+    return _dense(offsets, "offsets", torch.int32, E + 1)
+
+
+def _grouped_dims(g):
+    if g.dtype not in _TORCH_DTYPES:
+        raise ValueError(f"unknown dtype {g.dtype}")
+    return _TORCH_DTYPES[g.dtype], g.ld_x or g.K, g.ld_y or g.N
+
+
+def moe_grouped_gemm(g, offsets, x, w, y, stream=None):
+    """y[i] = w[e] x[i] for the rows i of every expert e: x [rows, K], w
+    [E, N, K], y [rows, N]; rows of no expert keep what they held."""
+    el, ld_x, ld_y = _grouped_dims(g)
+    _check(load().moe_grouped_gemm(
+        ctypes.byref(g), _offsets(offsets, g.E), _mat(x, "x", el, g.rows, g.K, ld_x),
+        _dense(w, "w", el, g.E * g.N * g.K), _mat(y, "y", el, g.rows, g.N, ld_y),
+        _stream(stream)))
+
+
+def moe_grouped_gemm_dx(g, offsets, dy, w, dx, stream=None):
+    """dx[i] = w[e]^T dy[i]."""
+    el, ld_x, ld_y = _grouped_dims(g)
+    _check(load().moe_grouped_gemm_dx(
+        ctypes.byref(g), _offsets(offsets, g.E), _mat(dy, "dy", el, g.rows, g.N, ld_y),
+        _dense(w, "w", el, g.E * g.N * g.K), _mat(dx, "dx", el, g.rows, g.K, ld_x),
+        _stream(stream)))
+
+
+def moe_grouped_gemm_dw(g, offsets, x, dy, dw, ws=None, accumulate=False, stream=None):
+    """dw[e] = sum over e's rows of dy[i] x[i]^T (fp32 [E, N, K]), added to dw
+    with accumulate; ws: grouped_dw_workspace_size bytes (None if 0)."""
+    el, ld_x, ld_y = _grouped_dims(g)
+    # an empty workspace tensor has no address
+    w_ptr = None if ws is None or (isinstance(ws, torch.Tensor) and ws.numel() == 0) \
+        else _dense(ws, "ws", None, None)
+    if isinstance(ws, int):
+        raise TypeError("ws: expected a torch.Tensor (its size is checked)")
+    _check(load().moe_grouped_gemm_dw(
+        ctypes.byref(g), _offsets(offsets, g.E), _mat(x, "x", el, g.rows, g.K, ld_x),
+        _mat(dy, "dy", el, g.rows, g.N, ld_y),
+        _dense(dw, "dw", torch.float32, g.E * g.N * g.K), int(bool(accumulate)), w_ptr,
+        0 if ws is None else _nbytes(ws), _stream(stream)))
+
+
+def moe_swiglu(gu, h, n_rows=None, stream=None):
+    """h = silu(g) u for rows gu = [g, u]: gu [rows, 2f], h [rows, f]. n_rows:
+    a one-element int32 device tensor, rows from it on are left alone."""
+    dt, rows, f, ld_h = _rows_of(h, "h")
+    ld_gu = _rows_of(gu, "gu")[3]
+    _check(load().moe_swiglu(
+        _DTYPES[dt], rows, f, _mat(gu, "gu", dt, rows, 2 * f, ld_gu), ld_gu,
+        _mat(h, "h", dt, rows, f, ld_h), ld_h,
+        _dense(n_rows, "n_rows", torch.int32, 1), _stream(stream)))
+
+
+def moe_swiglu_backward(gu, dh, dgu, n_rows=None, stream=None):
+    """dgu [rows, 2f] from gu [rows, 2f] and dh [rows, f]."""
+    dt, rows, f, ld_dh = _rows_of(dh, "dh")
+    ld_gu, ld_dgu = _rows_of(gu, "gu")[3], _rows_of(dgu, "dgu")[3]
+    _check(load().moe_swiglu_backward(
+        _DTYPES[dt], rows, f, _mat(gu, "gu", dt, rows, 2 * f, ld_gu), ld_gu,
+        _mat(dh, "dh", dt, rows, f, ld_dh), ld_dh,
+        _mat(dgu, "dgu", dt, rows, 2 * f, ld_dgu), ld_dgu,
+        _dense(n_rows, "n_rows", torch.int32, 1), _stream(stream)))
+
+
+def moe_mxfp4_quantize(x, codes, scales, index=None, index_div=1, n_rows=None,
+                       stream=None):
+    """Rows of x [src_rows, K] to MXFP4: codes uint8 [..., K / 2] and scales
+    uint8 [..., mxfp4_scale_stride(K)], contiguous, of as many rows as index
+    (int32) has entries, row i from x[index[i] // index_div] (zeros where that
+    is no row); without index, of x's rows."""
+    if x.dim() > 2 and x.is_contiguous():  # weights [E, N, K]
+        x = x.view(-1, x.shape[-1])
+    dt, src, K, ld_x = _rows_of(x, "x")
+    rows = src if index is None else index.numel()
+    _check(load().moe_mxfp4_quantize(
+        _DTYPES[dt], rows, K, x.data_ptr(), ld_x, src,
+        _dense(index, "index", torch.int32, rows), int(index_div),
+        _dense(n_rows, "n_rows", torch.int32, 1),
+        _dense(codes, "codes", torch.uint8, rows * (K // 2)),
+        _dense(scales, "scales", torch.uint8, rows * mxfp4_scale_stride(K)),
+        _stream(stream)))
+
+
+def moe_mxfp4_dequantize(codes, scales, y, n_rows=None, stream=None):
+    """The values of codes and scales, y [rows, K]."""
+    dt, rows, K, ld_y = _rows_of(y, "y")
+    _check(load().moe_mxfp4_dequantize(
+        _DTYPES[dt], rows, K, _dense(codes, "codes", torch.uint8, rows * (K // 2)),
+        _dense(scales, "scales", torch.uint8, rows * mxfp4_scale_stride(K)),
+        _mat(y, "y", dt, rows, K, ld_y), ld_y,
+        _dense(n_rows, "n_rows", torch.int32, 1), _stream(stream)))
+
+
+def moe_mxfp4_grouped_gemm(g, offsets, x_codes, x_scales, w_codes, w_scales, y,
+                           stream=None):
+    """moe_grouped_gemm on MXFP4 operands; y has g's dtype."""
+    el, _, ld_y = _grouped_dims(g)
+    S, u8 = mxfp4_scale_stride(g.K), torch.uint8
+    _check(load().moe_mxfp4_grouped_gemm(
+        ctypes.byref(g), _offsets(offsets, g.E),
+        _dense(x_codes, "x_codes", u8, g.rows * (g.K // 2)),
+        _dense(x_scales, "x_scales", u8, g.rows * S),
+        _dense(w_codes, "w_codes", u8, g.E * g.N * (g.K // 2)),
+        _dense(w_scales, "w_scales", u8, g.E * g.N * S),
+        _mat(y, "y", el, g.rows, g.N, ld_y), _stream(stream)))
 
 
 def workspace_views(cfg: MoeConfig, ws: torch.Tensor) -> dict:

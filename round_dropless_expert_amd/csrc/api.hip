@@ -19,6 +19,7 @@
 #include <vector>
 
 #include "../../include/moe_rounds.h"
+#include "api_common.hpp"
 #include "launch.hpp"
 
 namespace {
@@ -509,6 +510,16 @@ moe_status_t stage_gemm(const moe_config_t* cfg, int32_t round, int32_t n_rounds
 }
 
 }  // namespace
+
+namespace moe {
+
+moe_status_t api_fail(moe_status_t s, const char* msg, const char* name) {
+  return fail(s, msg, name);
+}
+moe_status_t api_hip_fail(hipError_t e, const char* where) { return hip_fail(e, where); }
+moe_status_t api_num_cus(int* out) { return num_cus(out); }
+
+}  // namespace moe
 
 extern "C" {
 

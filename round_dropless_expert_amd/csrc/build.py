@@ -22,8 +22,10 @@ CALIB_SOURCE = "calibrate.hip"
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["route_plan.hip", "dispatch_combine.hip", "grouped_gemm.hip",
-           "wgrad.hip", "backward.hip", "api.hip"]
-HEADERS = ["device_common.hpp", "launch.hpp"]
+           "wgrad.hip", "backward.hip", "api.hip", "ragged_gemm.hip", "swiglu.hip",
+           "mxfp4.hip", "ragged_api.hip"]
+HEADERS = ["device_common.hpp", "launch.hpp", "api_common.hpp", "ragged.hpp",
+           "ragged_device.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

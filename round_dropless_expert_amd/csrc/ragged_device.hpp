@@ -1,0 +1,69 @@
+// Device helpers of the ragged expert operators.
+#pragma once
+
+#include "device_common.hpp"
+#include "ragged.hpp"
+
+namespace moe {
+
+typedef _Float16 f16;
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ float to_f32(f16 v) { return static_cast<float>(v); }
+// float -> fp16 rounds to nearest even (v_cvt_f16_f32); past 65504 + half a
+// step it is infinite.
+template <>
+__device__ __forceinline__ f16 from_f32<f16>(float v) { return static_cast<f16>(v); }
+
+// Rows of expert e: [start, start + rows), with offsets clamped to [0, n],
+// so that no offsets, however wrong, lead a kernel out of its buffers.
+__device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int n, int* start,
+                                            int* rows) {
+  int a = offsets[e], b = offsets[e + 1];
+  a = a < 0 ? 0 : (a > n ? n : a);
+  b = b < 0 ? 0 : (b > n ? n : b);
+  *start = a;
+  *rows = b > a ? b - a : 0;
+}
+
+// The expert whose units hold unit t, when expert e owns units(rows_e)
+// consecutive units: every wavefront scans 64 experts at a time. All lanes
+// return the same values; false past the last unit.
+struct ExpertUnit {
+  int e, start, rows;  // the expert and its rows
+  int first;           // its first unit
+};
+template <typename Units>
+__device__ __forceinline__ bool find_unit(const int32_t* offsets, int E, int n, int t,
+                                          Units units, ExpertUnit* out) {
+  const int lane = threadIdx.x & (kWave - 1);
+  int carry = 0;
+  for (int base = 0; base < E; base += kWave) {
+    const int e = base + lane;
+    int start = 0, rows = 0, own = 0;
+    if (e < E) {
+      expert_rows(offsets, e, n, &start, &rows);
+      own = units(rows);
+    }
+    const int incl = wave_inclusive_scan(own) + carry;
+    const int before = __builtin_popcountll(__builtin_amdgcn_ballot_w64(incl <= t));
+    if (before < kWave && base + before < E) {
+      out->e = base + before;
+      out->start = __builtin_amdgcn_readlane(start, before);
+      out->rows = __builtin_amdgcn_readlane(rows, before);
+      out->first = __builtin_amdgcn_readlane(incl - own, before);
+      return true;
+    }
+    carry = __builtin_amdgcn_readlane(incl, kWave - 1);
+  }
+  return false;
+}
+
+// Rows that an elementwise call processes.
+__device__ __forceinline__ int64_t live_rows(int64_t rows, const int32_t* n_rows) {
+  if (!n_rows) return rows;
+  const int64_t n = *n_rows;
+  return n < 0 ? 0 : (n < rows ? n : rows);
+}
+
+}  // namespace moe

@@ -1,0 +1,442 @@
+// Products over rows sorted by expert, and their gradients, for any sizes
+// and strides (gfx950 matrix cores).
+//
+//   forward         y[i][n]  = sum_k x[i][k] w[e][n][k]
+//   input gradient  dx[i][k] = sum_n dy[i][n] w[e][n][k]
+//   weight gradient dw[e][n][k] = sum_i dy[i][n] x[i][k]
+//
+// for the rows i of expert e, offsets[e] <= i < offsets[e + 1]. All three
+// are out[a][b] = sum_c P(c, a) Q(c, b): an operand either holds its
+// contracted index c along its rows (x and w of the forward, dy of the input
+// gradient) or down its columns (the others).
+#include "ragged_device.hpp"
+
+namespace moe {
+namespace {
+
+enum RaggedMode { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
+
+struct RaggedParams {
+  const void* p;  // rows a (forward: x; input gradient: dy; weight gradient: dy)
+  const void* q;  // rows b (forward, input gradient: w; weight gradient: x)
+  void* out;      // y, dx, or dw
+  float* slots;   // weight gradient: partial sums of the chunks past the first
+  const int32_t* offsets;
+  int64_t ldp, ldq, ldo;  // elements
+  int rows, E;
+  int A, B, C;   // extents of a (weight gradient), b and c (forward, input gradient)
+  int chunk;     // weight gradient: rows of a chunk
+  int n_slots;   // weight gradient: slots of the workspace
+  int accumulate;
+  int tiles_b;   // tiles along b
+  int tiles_a;   // weight gradient: tiles along a
+};
+
+// One MFMA step of a type: 32 x 32 outputs, lane l supplies row l % 32.
+template <typename T>
+struct Mma;
+template <>
+struct Mma<bf16> {
+  static constexpr int kSteps = 2;  // per 64 bytes of c
+  typedef bf16x8 frag_t;
+  __device__ static __forceinline__ f32x16 mma(frag_t a, frag_t b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+};
+template <>
+struct Mma<f16> {
+  static constexpr int kSteps = 2;
+  typedef f16x8 frag_t;
+  __device__ static __forceinline__ f32x16 mma(frag_t a, frag_t b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  }
+};
+template <>
+struct Mma<float> {
+  static constexpr int kSteps = 8;
+  typedef float frag_t;
+  __device__ static __forceinline__ f32x16 mma(frag_t a, frag_t b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, c, 0, 0, 0);
+  }
+};
+
+typedef __attribute__((address_space(3))) char lds_char;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// 16 bytes of a row of which `n` elements exist (n may be <= 0), the rest
+// zero. The address need only be aligned to an element: gfx950 loads 16
+// bytes from any address.
+template <typename T>
+__device__ __forceinline__ u32x4 load16(const T* at, int n) {
+  constexpr int kV = 16 / sizeof(T);
+  union {
+    T e[kV];
+    u32x4 v;
+  } r;
+  r.v = u32x4{0, 0, 0, 0};
+  if (n >= kV) {
+    __builtin_memcpy(&r.v, at, 16);
+    return r.v;
+  }
+#pragma unroll
+  for (int i = 0; i < kV; ++i)
+    if (i < n) r.e[i] = at[i];
+  return r.v;
+}
+
+// One operand's share of a stage: `kExt` rows of its output index by 64
+// bytes of c. Along: 64 bytes of c per row in LDS, at a pitch of 80 bytes.
+// Down: one LDS row per c, kExt elements and 16 bytes of padding.
+template <typename T, bool kAlong, int kExt>
+struct Operand {
+  static constexpr int kEs = sizeof(T);
+  static constexpr int kV = 16 / kEs;
+  static constexpr int kCk = 64 / kEs;
+  static constexpr int kPitch = kAlong ? 80 : kExt * kEs + 16;
+  static constexpr int kBytes = kAlong ? kExt * 80 : kCk * kPitch;
+  static constexpr int kPieces = kExt / 64;  // 16-byte pieces per thread
+
+  const T* base;  // c = 0 of the tile's first row
+  int64_t ld;
+  int ext;  // rows of the output index that exist
+  u32x4 reg[kPieces];
+
+  // pieces of the stage at c0, where c exists below c_end
+  __device__ __forceinline__ void load(int c0, int c_end) {
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int id = (int)threadIdx.x + 256 * u;
+      if constexpr (kAlong) {
+        const int row = id >> 2, c = c0 + (id & 3) * kV;
+        reg[u] = load16(base + row * ld + c, row < ext ? c_end - c : 0);
+      } else {
+        constexpr int kPer = kExt * kEs / 16;
+        const int c = c0 + id / kPer, row = (id % kPer) * kV;
+        reg[u] = load16(base + c * ld + row, c < c_end ? ext - row : 0);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(char* lds) const {
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int id = (int)threadIdx.x + 256 * u;
+      int off;
+      if constexpr (kAlong) {
+        off = (id >> 2) * 80 + (id & 3) * 16;
+      } else {
+        constexpr int kPer = kExt * kEs / 16;
+        off = (id / kPer) * kPitch + (id % kPer) * 16;
+      }
+      *reinterpret_cast<u32x4*>(lds + off) = reg[u];
+    }
+  }
+  // this lane's fragment of MFMA step s, rows row0 .. row0 + 31
+  __device__ static __forceinline__ typename Mma<T>::frag_t frag(const char* lds, int row0,
+                                                                 int s) {
+    const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5;
+    typedef typename Mma<T>::frag_t frag_t;
+    if constexpr (kEs == 4) {
+      const int c = 2 * s + half;
+      return kAlong ? *reinterpret_cast<const float*>(lds + (row0 + l32) * 80 + c * 4)
+                    : *reinterpret_cast<const float*>(lds + c * kPitch + (row0 + l32) * 4);
+    } else if constexpr (kAlong) {
+      return *reinterpret_cast<const frag_t*>(lds + (row0 + l32) * 80 + s * 32 + half * 16);
+    } else {
+      // transposing LDS read: in each group of 16 lanes, lane i receives
+      // 16-bit element i % 4 of the 8 bytes addressed by lanes 4 j + i / 4,
+      // j = 0..3, so lane i gets row i of the group at four consecutive c
+      const int grp = lane >> 4, gj = (lane >> 2) & 3, gq = lane & 3;
+      const int c = 16 * s + 8 * (grp >> 1) + gj;
+      const char* at = lds + c * kPitch + (row0 + 16 * (grp & 1) + 4 * gq) * 2;
+      const s16x4 lo =
+          __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_char*)at);
+      const s16x4 hi =
+          __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_char*)(at + 4 * kPitch));
+      return __builtin_bit_cast(frag_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  }
+};
+
+// Slots of the experts below e: an expert's chunks past its first.
+__device__ __forceinline__ int slots_before(const int32_t* offsets, int e, int n, int chunk) {
+  const int lane = threadIdx.x & 63;
+  int sum = 0;
+  for (int base = 0; base < e; base += kWave) {
+    int start, rows, own = 0;
+    if (base + lane < e) {
+      expert_rows(offsets, base + lane, n, &start, &rows);
+      own = rows > 0 ? (int)(((int64_t)rows + chunk - 1) / chunk) - 1 : 0;
+    }
+    sum += __builtin_amdgcn_readlane(wave_inclusive_scan(own), kWave - 1);
+  }
+  return sum;
+}
+
+// General kernel: one workgroup per output tile of 64 W x 64 W, 2 x 2
+// wavefronts of W x W blocks of 32 x 32. Stages of 64 bytes of c go through
+// registers into two LDS buffers, the next stage's loads in flight while a
+// stage is multiplied. Takes every size, stride and element alignment.
+template <typename T, int kMode, int W>
+__global__ __launch_bounds__(256) void ragged_general_kernel(RaggedParams p) {
+  constexpr int kTile = 64 * W;
+  constexpr bool kPAlong = kMode != kWeightGrad;
+  constexpr bool kQAlong = kMode == kForward;
+  typedef Operand<T, kPAlong, kTile> P_t;
+  typedef Operand<T, kQAlong, kTile> Q_t;
+  constexpr int kCk = P_t::kCk;
+  __shared__ __attribute__((aligned(16))) char lds[2][P_t::kBytes + Q_t::kBytes];
+
+  const int per = kMode == kWeightGrad ? p.tiles_a * p.tiles_b : p.tiles_b;
+  ExpertUnit u;
+  const int t = blockIdx.x;
+  const bool found = find_unit(
+      p.offsets, p.E, p.rows, t,
+      [&](int rows) {
+        if constexpr (kMode == kWeightGrad) {
+          // an expert without rows still stores its zeros
+          const int n = (int)(((int64_t)rows + p.chunk - 1) / p.chunk);
+          return (n == 0 && !p.accumulate ? 1 : n) * per;
+        } else {
+          return (int)(((int64_t)rows + kTile - 1) / kTile) * per;
+        }
+      },
+      &u);
+  if (!found) return;
+  const int local = t - u.first;
+
+  P_t P;
+  Q_t Q;
+  int c_begin = 0, c_end, a0, b0, a_ext, part = 0;
+  if constexpr (kMode == kWeightGrad) {
+    part = local / per;
+    a0 = (local % per) / p.tiles_b * kTile;
+    b0 = (local % per) % p.tiles_b * kTile;
+    c_begin = part * p.chunk;
+    c_end = u.rows - c_begin < p.chunk ? u.rows : c_begin + p.chunk;
+    a_ext = p.A - a0;
+    P.base = static_cast<const T*>(p.p) + (int64_t)u.start * p.ldp + a0;
+    Q.base = static_cast<const T*>(p.q) + (int64_t)u.start * p.ldq + b0;
+  } else {
+    a0 = local / p.tiles_b * kTile;
+    b0 = local % p.tiles_b * kTile;
+    c_end = p.C;
+    a_ext = u.rows - a0;
+    P.base = static_cast<const T*>(p.p) + ((int64_t)u.start + a0) * p.ldp;
+    Q.base = static_cast<const T*>(p.q) + (int64_t)u.e * p.B * p.C +
+             (kMode == kForward ? (int64_t)b0 * p.ldq : (int64_t)b0);
+  }
+  P.ld = p.ldp;
+  Q.ld = p.ldq;
+  P.ext = a_ext;
+  Q.ext = p.B - b0;
+
+  // weight gradient: the slot of this chunk (past the last one only if the
+  // offsets overlap: then it is not stored)
+  int slot = 0;
+  if (kMode == kWeightGrad && part > 0) {
+    slot = slots_before(p.offsets, u.e, p.rows, p.chunk) + part - 1;
+    if (slot >= p.n_slots) return;
+  }
+  const int wave = threadIdx.x >> 6;
+  const int wa = (wave >> 1) * 32 * W, wb = (wave & 1) * 32 * W;
+  f32x16 acc[W][W];
+#pragma unroll
+  for (int i = 0; i < W; ++i)
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+
+  if (c_begin < c_end) {
+    P.load(c_begin, c_end);
+    Q.load(c_begin, c_end);
+    int buf = 0;
+    for (int c = c_begin; c < c_end; c += kCk, buf ^= 1) {
+      // the buffer's last readers passed the previous stage's barrier
+      P.store(lds[buf]);
+      Q.store(lds[buf] + P_t::kBytes);
+      __syncthreads();
+      if (c + kCk < c_end) {
+        P.load(c + kCk, c_end);
+        Q.load(c + kCk, c_end);
+      }
+#pragma unroll
+      for (int s = 0; s < Mma<T>::kSteps; ++s) {
+        typename Mma<T>::frag_t fa[W], fb[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) fa[i] = P_t::frag(lds[buf], wa + 32 * i, s);
+#pragma unroll
+        for (int j = 0; j < W; ++j) fb[j] = Q_t::frag(lds[buf] + P_t::kBytes, wb + 32 * j, s);
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+#pragma unroll
+          for (int j = 0; j < W; ++j) acc[i][j] = Mma<T>::mma(fa[i], fb[j], acc[i][j]);
+      }
+    }
+  }
+
+  // lane: column b = l % 32 of a block, rows a = 8 (v / 4) + 4 (l / 32) + v % 4
+  const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const int b = b0 + wb + 32 * j + l32;
+      if (b >= p.B) continue;
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int da = wa + 32 * i + 8 * (v >> 2) + 4 * half + (v & 3);
+        if (da >= a_ext) continue;
+        const float r = acc[i][j][v];
+        if constexpr (kMode == kWeightGrad) {
+          if (part == 0) {
+            float* o = static_cast<float*>(p.out) + ((int64_t)u.e * p.A + a0 + da) * p.B + b;
+            *o = p.accumulate ? *o + r : r;
+          } else {
+            p.slots[((int64_t)slot * p.A + a0 + da) * p.B + b] = r;
+          }
+        } else {
+          static_cast<T*>(p.out)[((int64_t)u.start + a0 + da) * p.ldo + b] = from_f32<T>(r);
+        }
+      }
+    }
+  }
+}
+
+// Adds the slots of every expert that has any to dw, in chunk order. Grid:
+// x over [N][K], y: the y-th, y + gridDim.y-th ... expert.
+__global__ __launch_bounds__(256) void ragged_add_slots_kernel(RaggedParams p) {
+  const int64_t n = (int64_t)p.A * p.B;
+  for (int e = blockIdx.y; e < p.E; e += gridDim.y) {
+    int start, rows;
+    expert_rows(p.offsets, e, p.rows, &start, &rows);
+    const int parts = (int)(((int64_t)rows + p.chunk - 1) / p.chunk);
+    if (parts <= 1) continue;
+    const int first = slots_before(p.offsets, e, p.rows, p.chunk);
+    const int own = first + parts - 1 <= p.n_slots ? parts - 1 : p.n_slots - first;
+    float* o = static_cast<float*>(p.out) + (int64_t)e * n;
+    const float* s = p.slots + (int64_t)first * n;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n;
+         i += (int64_t)gridDim.x * 256) {
+      float r = o[i];
+      for (int k = 0; k < own; ++k) r += s[(int64_t)k * n + i];
+      o[i] = r;
+    }
+  }
+}
+
+int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+// Tile of the general kernel: 128 x 128 unless the outputs are too few to
+// give every CU one.
+template <typename T, int kMode>
+hipError_t launch_general(RaggedParams p, int num_cus, hipStream_t st) {
+  auto jobs = [&](int tile) -> int64_t {
+    p.tiles_b = ceil_div(p.B, tile);
+    p.tiles_a = ceil_div(p.A, tile);
+    // the most units that offsets can make: every expert's last one partial
+    if (kMode == kWeightGrad)
+      return ((int64_t)p.rows / p.chunk + p.E) * p.tiles_a * p.tiles_b;
+    return ((int64_t)p.rows / tile + (p.rows < p.E ? p.rows : p.E)) * p.tiles_b;
+  };
+  const int64_t large = jobs(128);
+  if (large >= 2 * (int64_t)num_cus) {
+    hipLaunchKernelGGL((ragged_general_kernel<T, kMode, 2>), dim3((unsigned)large), dim3(256), 0,
+                       st, p);
+  } else {
+    const int64_t small = jobs(64);
+    hipLaunchKernelGGL((ragged_general_kernel<T, kMode, 1>), dim3((unsigned)small), dim3(256), 0,
+                       st, p);
+  }
+  return hipGetLastError();
+}
+
+template <int kMode>
+hipError_t dispatch(ElemType t, const RaggedParams& p, int num_cus, hipStream_t st) {
+  switch (t) {
+    case ElemType::kF32: return launch_general<float, kMode>(p, num_cus, st);
+    case ElemType::kBF16: return launch_general<bf16, kMode>(p, num_cus, st);
+    default: return launch_general<f16, kMode>(p, num_cus, st);
+  }
+}
+
+RaggedParams base_params(const RaggedShape& s, const int32_t* offsets) {
+  RaggedParams p{};
+  p.offsets = offsets;
+  p.rows = (int)s.rows;
+  p.E = s.E;
+  return p;
+}
+
+}  // namespace
+
+// Chunks: as many as give about four jobs a CU of the 256 x 256 tiles, so
+// that an expert with many rows does not hold up the launch, but at least
+// 512 rows each (a chunk past the first costs a write and a read of [N][K]
+// in fp32, its product 2 N K flops a row: below some hundred rows the
+// traffic would outweigh it). A function of the shape alone: it fixes the
+// order of the sums.
+DwSplit dw_split(const RaggedShape& s) {
+  const int64_t tiles = (int64_t)ceil_div(s.N, 256) * ceil_div(s.K, 256);
+  int64_t chunk = (s.rows * tiles + 1023) / 1024;
+  chunk = chunk < 512 ? 512 : (chunk + 63) / 64 * 64;
+  return DwSplit{chunk, s.rows / chunk};
+}
+
+hipError_t launch_ragged_gemm(const RaggedShape& s, const int32_t* offsets, const void* x,
+                              const void* w, void* y, int num_cus, hipStream_t st) {
+  if (s.rows == 0) return hipSuccess;
+  RaggedParams p = base_params(s, offsets);
+  p.p = x;
+  p.q = w;
+  p.out = y;
+  p.ldp = s.ld_x;
+  p.ldq = s.K;
+  p.ldo = s.ld_y;
+  p.B = s.N;
+  p.C = s.K;
+  return dispatch<kForward>(s.type, p, num_cus, st);
+}
+
+hipError_t launch_ragged_dx(const RaggedShape& s, const int32_t* offsets, const void* dy,
+                            const void* w, void* dx, int num_cus, hipStream_t st) {
+  if (s.rows == 0) return hipSuccess;
+  RaggedParams p = base_params(s, offsets);
+  p.p = dy;
+  p.q = w;
+  p.out = dx;
+  p.ldp = s.ld_y;
+  p.ldq = s.K;
+  p.ldo = s.ld_x;
+  p.B = s.K;
+  p.C = s.N;
+  return dispatch<kInputGrad>(s.type, p, num_cus, st);
+}
+
+hipError_t launch_ragged_dw(const RaggedShape& s, const int32_t* offsets, const void* x,
+                            const void* dy, float* dw, float* slots, bool accumulate,
+                            int num_cus, hipStream_t st) {
+  const DwSplit split = dw_split(s);
+  RaggedParams p = base_params(s, offsets);
+  p.p = dy;
+  p.q = x;
+  p.out = dw;
+  p.slots = slots;
+  p.ldp = s.ld_y;
+  p.ldq = s.ld_x;
+  p.A = s.N;
+  p.B = s.K;
+  p.chunk = (int)split.chunk;
+  p.n_slots = (int)split.slots;
+  p.accumulate = accumulate ? 1 : 0;
+  hipError_t e = dispatch<kWeightGrad>(s.type, p, num_cus, st);
+  if (e != hipSuccess || split.slots == 0) return e;
+  int gx = ceil_div((int64_t)s.N * s.K, 1024);
+  gx = gx > 4096 ? 4096 : gx;
+  const int gy = s.E < 64 ? s.E : 64;
+  hipLaunchKernelGGL(ragged_add_slots_kernel, dim3(gx, gy), dim3(256), 0, st, p);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,150 @@
+// SwiGLU between the experts' products, and its gradient, on rows [g, u]:
+//
+//   h = g s(g) u        s = 1 / (1 + e^-g)
+//   du = dh g s
+//   dg = dh u s (1 + g (1 - s))
+//
+// All arithmetic is fp32; h, dg and du are rounded once, to their type.
+#include "ragged_device.hpp"
+
+namespace moe {
+namespace {
+
+// s(g) and 1 - s(g), both to a few ulp for every g: with a = e^-|g| they
+// are 1 / (1 + a) and a / (1 + a), in the order of g's sign, so neither
+// cancels and no exponential overflows.
+struct Gate {
+  float s, rest;
+};
+// For 16-bit types the hardware's base-2 exponential and reciprocal (1 ulp
+// each; the product |g| log2 e is off by at most |g| 2^-24 relative, far
+// below half a step of fp16); for fp32 the full-precision functions.
+template <typename T>
+__device__ __forceinline__ Gate gate(float g) {
+  float a, r;
+  if constexpr (sizeof(T) == 2) {
+    a = __builtin_amdgcn_exp2f(__builtin_fabsf(g) * -1.44269504088896341f);
+    r = __builtin_amdgcn_rcpf(1.0f + a);
+  } else {
+    a = expf(-__builtin_fabsf(g));
+    r = 1.0f / (1.0f + a);
+  }
+  const float q = a * r;
+  return g >= 0.f ? Gate{r, q} : Gate{q, r};
+}
+
+template <typename T, int V>
+struct Vec {
+  T e[V];
+} ;
+
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> load(const T* p) {
+  if constexpr (V == 1) {
+    return Vec<T, 1>{{*p}};
+  } else {
+    return __builtin_bit_cast(Vec<T, V>, *reinterpret_cast<const u32x4*>(p));
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store(T* p, const Vec<T, V>& v) {
+  if constexpr (V == 1)
+    *p = v.e[0];
+  else
+    *reinterpret_cast<u32x4*>(p) = __builtin_bit_cast(u32x4, v);
+}
+
+struct SwigluParams {
+  const void* gu;
+  const void* dh;
+  void* out;  // h or dgu
+  int64_t ld_gu, ld_dh, ld_out;
+  const int32_t* n_rows;
+  int64_t rows;
+  uint32_t per;  // vectors of V features per row
+  int64_t f;
+};
+
+template <typename T, int V, bool kBackward>
+__global__ __launch_bounds__(256) void swiglu_kernel(SwigluParams p) {
+  const int64_t total = live_rows(p.rows, p.n_rows) * p.per;
+  const T* gu = static_cast<const T*>(p.gu);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / p.per;
+    const int64_t c = (i - row * p.per) * V;
+    const Vec<T, V> g = load<T, V>(gu + row * p.ld_gu + c);
+    const Vec<T, V> u = load<T, V>(gu + row * p.ld_gu + p.f + c);
+    if constexpr (!kBackward) {
+      Vec<T, V> h;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float gf = to_f32(g.e[v]);
+        h.e[v] = from_f32<T>(gf * gate<T>(gf).s * to_f32(u.e[v]));
+      }
+      store<T, V>(static_cast<T*>(p.out) + row * p.ld_out + c, h);
+    } else {
+      const Vec<T, V> d = load<T, V>(static_cast<const T*>(p.dh) + row * p.ld_dh + c);
+      Vec<T, V> dg, du;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float gf = to_f32(g.e[v]), df = to_f32(d.e[v]);
+        const Gate k = gate<T>(gf);
+        dg.e[v] = from_f32<T>(df * (k.s * (1.0f + gf * k.rest)) * to_f32(u.e[v]));
+        du.e[v] = from_f32<T>(df * (gf * k.s));
+      }
+      T* o = static_cast<T*>(p.out) + row * p.ld_out + c;
+      store<T, V>(o, dg);
+      store<T, V>(o + p.f, du);
+    }
+  }
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+template <typename T, bool kBackward>
+hipError_t run(SwigluParams p, int num_cus, hipStream_t st) {
+  constexpr int kV = 16 / sizeof(T);
+  // 16-byte vectors where every row of every buffer starts at one
+  const bool vec = p.f % kV == 0 && p.ld_gu % kV == 0 && p.ld_out % kV == 0 &&
+                   (!kBackward || p.ld_dh % kV == 0) && aligned16(p.gu) && aligned16(p.out) &&
+                   (!kBackward || aligned16(p.dh));
+  p.per = (uint32_t)(vec ? p.f / kV : p.f);
+  const int64_t blocks = (p.rows * (int64_t)p.per + 255) / 256;
+  const int64_t most = (int64_t)num_cus * 16;
+  const unsigned grid = (unsigned)(blocks < most ? blocks : most);
+  if (vec)
+    hipLaunchKernelGGL((swiglu_kernel<T, kV, kBackward>), dim3(grid), dim3(256), 0, st, p);
+  else
+    hipLaunchKernelGGL((swiglu_kernel<T, 1, kBackward>), dim3(grid), dim3(256), 0, st, p);
+  return hipGetLastError();
+}
+
+template <bool kBackward>
+hipError_t dispatch(ElemType t, const SwigluParams& p, int num_cus, hipStream_t st) {
+  if (p.rows == 0) return hipSuccess;
+  switch (t) {
+    case ElemType::kF32: return run<float, kBackward>(p, num_cus, st);
+    case ElemType::kBF16: return run<bf16, kBackward>(p, num_cus, st);
+    default: return run<f16, kBackward>(p, num_cus, st);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_swiglu(ElemType t, int64_t rows, int64_t f, const void* gu, int64_t ld_gu,
+                         void* h, int64_t ld_h, const int32_t* n_rows, int num_cus,
+                         hipStream_t st) {
+  return dispatch<false>(t, SwigluParams{gu, nullptr, h, ld_gu, 0, ld_h, n_rows, rows, 0, f},
+                         num_cus, st);
+}
+
+hipError_t launch_swiglu_backward(ElemType t, int64_t rows, int64_t f, const void* gu,
+                                  int64_t ld_gu, const void* dh, int64_t ld_dh, void* dgu,
+                                  int64_t ld_dgu, const int32_t* n_rows, int num_cus,
+                                  hipStream_t st) {
+  return dispatch<true>(t, SwigluParams{gu, dh, dgu, ld_gu, ld_dh, ld_dgu, n_rows, rows, 0, f},
+                        num_cus, st);
+}
+
+}  // namespace moe

@@ -8,6 +8,7 @@
 // 0.5, 1, 1.5, 2, 3, 4 and 6 (a sign bit, two bits of exponent, one of
 // mantissa), ending at 6; the block's largest magnitude lies in [4, 8).
 #include "ragged_device.hpp"
+#include "ragged_ring.hpp"
 
 namespace moe {
 namespace {
@@ -283,6 +284,29 @@ hipError_t launch_mx_gemm(const RaggedShape& s, const int32_t* offsets, const ui
                           const uint8_t* xs, const uint8_t* wq, const uint8_t* ws, void* y,
                           int num_cus, hipStream_t st) {
   if (s.rows == 0) return hipSuccess;
+  const int64_t es = elem_bytes(s.type);
+  if (s.rows > 16 * (int64_t)s.E) {
+    RingParams r{};
+    r.act = reinterpret_cast<const char*>(xq);
+    r.w = reinterpret_cast<const char*>(wq);
+    r.act_scales = reinterpret_cast<const char*>(xs);
+    r.w_scales = reinterpret_cast<const char*>(ws);
+    r.out = static_cast<char*>(y);
+    r.offsets = offsets;
+    r.lda = r.ldw = s.K / 2;
+    r.ldo = s.ld_y * es;
+    r.lds = mx_scale_stride(s.K);
+    r.wbytes = (int64_t)s.N * s.K / 2;
+    r.rows = (int)s.rows;
+    r.E = s.E;
+    r.B = s.N;
+    r.cbytes = s.K / 2;
+    r.out_vec = s.N % (16 / es) == 0 && s.ld_y % (16 / es) == 0 && aligned16(y);
+    return launch_ring(s.type == ElemType::kBF16  ? RingKind::kMxBF16
+                       : s.type == ElemType::kF16 ? RingKind::kMxF16
+                                                  : RingKind::kMxF32,
+                       r, num_cus, st);
+  }
   const MxParams p{xq,     xs,          wq,  ws,  y,   offsets,
                    s.ld_y, (int)s.rows, s.E, s.N, s.K, (int)mx_scale_stride(s.K), 0};
   switch (s.type) {

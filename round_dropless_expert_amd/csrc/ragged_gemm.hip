@@ -10,6 +10,7 @@
 // contracted index c along its rows (x and w of the forward, dy of the input
 // gradient) or down its columns (the others).
 #include "ragged_device.hpp"
+#include "ragged_ring.hpp"
 
 namespace moe {
 namespace {
@@ -361,6 +362,35 @@ hipError_t dispatch(ElemType t, const RaggedParams& p, int num_cus, hipStream_t 
   }
 }
 
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// The ring kernel takes 16-bit rows of whole 16-byte chunks; the output may
+// have any alignment.
+bool ring_takes(const RaggedShape& s, const void* act, int64_t ld, const void* w, int c) {
+  return s.type != ElemType::kF32 && c % 8 == 0 && s.K % 8 == 0 && ld % 8 == 0 &&
+         aligned16(act) && aligned16(w);
+}
+
+RingParams ring_params(const RaggedShape& s, const int32_t* offsets, const void* act, int64_t ld,
+                       const void* w, void* out, int64_t ldo, int c, int b) {
+  RingParams r{};
+  r.act = static_cast<const char*>(act);
+  r.w = static_cast<const char*>(w);
+  r.out = static_cast<char*>(out);
+  r.offsets = offsets;
+  r.lda = ld * 2;
+  r.ldw = (int64_t)s.K * 2;
+  r.ldo = ldo * 2;
+  r.wbytes = (int64_t)s.N * s.K * 2;
+  r.rows = (int)s.rows;
+  r.E = s.E;
+  r.B = b;
+  r.C = c;
+  r.cbytes = c * 2;
+  r.out_vec = b % 8 == 0 && ldo % 8 == 0 && aligned16(out);
+  return r;
+}
+
 RaggedParams base_params(const RaggedShape& s, const int32_t* offsets) {
   RaggedParams p{};
   p.offsets = offsets;
@@ -387,6 +417,10 @@ DwSplit dw_split(const RaggedShape& s) {
 hipError_t launch_ragged_gemm(const RaggedShape& s, const int32_t* offsets, const void* x,
                               const void* w, void* y, int num_cus, hipStream_t st) {
   if (s.rows == 0) return hipSuccess;
+  if (ring_takes(s, x, s.ld_x, w, s.K))
+    return launch_ring(
+        s.type == ElemType::kBF16 ? RingKind::kForwardBF16 : RingKind::kForwardF16,
+        ring_params(s, offsets, x, s.ld_x, w, y, s.ld_y, s.K, s.N), num_cus, st);
   RaggedParams p = base_params(s, offsets);
   p.p = x;
   p.q = w;
@@ -402,6 +436,10 @@ hipError_t launch_ragged_gemm(const RaggedShape& s, const int32_t* offsets, cons
 hipError_t launch_ragged_dx(const RaggedShape& s, const int32_t* offsets, const void* dy,
                             const void* w, void* dx, int num_cus, hipStream_t st) {
   if (s.rows == 0) return hipSuccess;
+  if (ring_takes(s, dy, s.ld_y, w, s.N))
+    return launch_ring(
+        s.type == ElemType::kBF16 ? RingKind::kInputGradBF16 : RingKind::kInputGradF16,
+        ring_params(s, offsets, dy, s.ld_y, w, dx, s.ld_x, s.N, s.K), num_cus, st);
   RaggedParams p = base_params(s, offsets);
   p.p = dy;
   p.q = w;

@@ -22,7 +22,8 @@ CALIB_SOURCE = "calibrate.hip"
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["route_plan.hip", "dispatch_combine.hip", "grouped_gemm.hip",
-           "wgrad.hip", "backward.hip", "api.hip", "ragged_gemm.hip", "ragged_ring.hip", "swiglu.hip",
+           "wgrad.hip", "backward.hip", "api.hip", "ragged_gemm.hip", "ragged_ring.hip",
+           "ragged_wgrad.hip", "swiglu.hip",
            "mxfp4.hip", "ragged_api.hip"]
 HEADERS = ["device_common.hpp", "launch.hpp", "api_common.hpp", "ragged.hpp",
            "ragged_device.hpp", "ragged_ring.hpp"]

@@ -411,6 +411,10 @@ DwSplit dw_split(const RaggedShape& s) {
   const int64_t tiles = (int64_t)ceil_div(s.N, 256) * ceil_div(s.K, 256);
   int64_t chunk = (s.rows * tiles + 1023) / 1024;
   chunk = chunk < 512 ? 512 : (chunk + 63) / 64 * 64;
+  // a chunk's rows are addressed with 32-bit byte offsets
+  const int64_t ld = (s.ld_x > s.ld_y ? s.ld_x : s.ld_y) * elem_bytes(s.type);
+  const int64_t most = (((int64_t)1 << 31) - 1) / ld / 64 * 64;
+  if (chunk > most) chunk = most;
   return DwSplit{chunk, s.rows / chunk};
 }
 
@@ -468,7 +472,16 @@ hipError_t launch_ragged_dw(const RaggedShape& s, const int32_t* offsets, const 
   p.chunk = (int)split.chunk;
   p.n_slots = (int)split.slots;
   p.accumulate = accumulate ? 1 : 0;
-  hipError_t e = dispatch<kWeightGrad>(s.type, p, num_cus, st);
+  hipError_t e;
+  if (s.type != ElemType::kF32 && s.rows > 0 && s.ld_x % 8 == 0 && s.ld_y % 8 == 0 &&
+      aligned16(x) && aligned16(dy)) {
+    const WgradRingParams r{static_cast<const char*>(dy), static_cast<const char*>(x), dw, slots,
+                            offsets, s.ld_y * 2, s.ld_x * 2, (int)s.rows, s.E, s.N, s.K,
+                            p.chunk, p.n_slots, p.accumulate};
+    e = launch_wgrad_ring(s.type == ElemType::kBF16, r, num_cus, st);
+  } else {
+    e = dispatch<kWeightGrad>(s.type, p, num_cus, st);
+  }
   if (e != hipSuccess || split.slots == 0) return e;
   int gx = ceil_div((int64_t)s.N * s.K, 1024);
   gx = gx > 4096 ? 4096 : gx;

@@ -33,6 +33,23 @@ struct RingParams {
   int out_vec; // rows of out are 16-byte aligned and hold whole chunks
 };
 
+// Weight gradient: strides in bytes (16-byte multiples), chunk * stride below
+// 2^31.
+struct WgradRingParams {
+  const char* dy;  // [rows][N], ldy apart
+  const char* x;   // [rows][K], ldx apart
+  float* dw;       // [E][N][K]
+  float* slots;    // [n_slots][N][K]
+  const int32_t* offsets;
+  int64_t ldy, ldx;
+  int rows, E, N, K;
+  int chunk, n_slots;
+  int accumulate;
+};
+
+hipError_t launch_wgrad_ring(bool is_bf16, const WgradRingParams& p, int num_cus,
+                             hipStream_t st);
+
 hipError_t launch_ring(RingKind kind, const RingParams& p, int num_cus, hipStream_t st);
 
 }  // namespace moe

@@ -1,0 +1,347 @@
+// Weight gradient of the product over rows sorted by expert, 16-bit types,
+// through an LDS ring (gfx950 matrix cores):
+//
+//   dw[e][n][k] = sum over e's rows i of dy[i][n] x[i][k]      (fp32)
+//
+// The contraction runs down the rows of both operands, while the matrix
+// cores want each lane to hold consecutive rows of one column: stages of 32
+// rows are copied into LDS as they lie, by LDS-direct loads that read 256
+// bytes of a row at a time, and the fragments come back through gfx950's
+// transposing LDS read. A workgroup computes a 256 (n) x 256 (k) tile of one
+// expert's chunk of rows with 2 x 2 wavefronts of 128 x 128. Four LDS slots
+// form a ring with three stages in flight. Persistent: an XCD's workgroups
+// walk consecutive tiles, which share their operands in its L2, and the ring
+// runs on across a workgroup's tiles, so that the next tile's first stages
+// land while the current one is stored.
+//
+// An expert with more rows than a chunk is summed in several tiles; those
+// past the first go to slots of the workspace and a second launch adds them
+// in chunk order.
+#include "ragged_device.hpp"
+#include "ragged_ring.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kTile = 256;
+constexpr int kStageRows = 32;
+constexpr int kOpBytes = kStageRows * kTile * 2;  // one operand's stage
+constexpr int kSlotBytes = 2 * kOpBytes;          // dy, then x
+constexpr int kSlots = 4;
+constexpr int kLoads = kSlotBytes / (256 * 16);  // 16-byte loads per thread and stage
+constexpr int kRsrcWord3 = 0x00020000;
+constexpr uint32_t kOutOfRange = 0x80000000u;
+
+typedef __attribute__((address_space(3))) char lds_char;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// LDS-direct load: lane i's 16 bytes at voff + soff to LDS at lds + 16 i. In
+// asm: the compiler neither moves nor waits on it, every wait is the
+// kernel's own vmcnt count. No register results.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void lds_load16(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff,
+                                           uint32_t soff, uint32_t lds) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, %3 offen lds"
+      :
+      : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+      : "m0");
+}
+#pragma clang diagnostic pop
+
+template <int N>
+__device__ __forceinline__ void wait_vmem_barrier() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ float acc_read(float a) {
+  float v;
+  asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
+  return v;
+}
+
+template <typename T>
+__device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
+  if constexpr (__is_same(T, bf16))
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+template <typename T>
+__global__ __launch_bounds__(256, 1) void ragged_wgrad_kernel(WgradRingParams p) {
+  __shared__ __attribute__((aligned(1024))) char lds[kSlots][kSlotBytes];
+  __shared__ int32_t tiles_to[kRaggedMaxExperts];  // tiles of the experts up to e
+  __shared__ int32_t slots_to[kRaggedMaxExperts];  // slots of the experts below e
+  __shared__ int32_t first_row[kRaggedMaxExperts];
+  __shared__ int32_t n_rows[kRaggedMaxExperts];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wa = wave & 1, wb = wave >> 1;  // this wavefront's 128 x 128 quarter
+  const int l32 = lane & 31, half = lane >> 5;
+
+  const int ta = (p.N + kTile - 1) / kTile, tb = (p.K + kTile - 1) / kTile;
+  const int per = ta * tb;
+  if (wave == 0) {
+    int tiles = 0, slots = 0;
+    for (int base = 0; base < p.E; base += kWave) {
+      const int e = base + lane;
+      int start = 0, rows = 0, parts = 0;
+      if (e < p.E) {
+        expert_rows(p.offsets, e, p.rows, &start, &rows);
+        parts = (int)(((int64_t)rows + p.chunk - 1) / p.chunk);
+      }
+      const int extra = parts > 1 ? parts - 1 : 0;
+      // an expert without rows still stores its zeros
+      const int jobs = e < p.E && parts == 0 && !p.accumulate ? 1 : parts;
+      const int incl = wave_inclusive_scan(jobs * per) + tiles;
+      const int sincl = wave_inclusive_scan(extra) + slots;
+      if (e < p.E) {
+        tiles_to[e] = incl;
+        slots_to[e] = sincl - extra;
+        first_row[e] = start;
+        n_rows[e] = rows;
+      }
+      tiles = __builtin_amdgcn_readlane(incl, kWave - 1);
+      slots = __builtin_amdgcn_readlane(sincl, kWave - 1);
+    }
+  }
+  __syncthreads();
+  const int total = __builtin_amdgcn_readfirstlane(tiles_to[p.E - 1]);
+
+  // XCD x takes the tiles [x n8, (x + 1) n8), its Q workgroups every Q-th.
+  const int Q = (int)gridDim.x / 8;
+  const int xcd = (int)(blockIdx.x % 8), q = (int)(blockIdx.x / 8);
+  const int n8 = (total + 7) / 8;
+  const int t_first = xcd * n8 + q;
+  const int t_end = (xcd + 1) * n8 < total ? (xcd + 1) * n8 : total;
+  if (t_first >= t_end) return;
+
+  struct Tile {
+    int e, part, a0, b0, cnt;  // cnt: rows of the chunk
+    int64_t row;               // first row
+  };
+  auto tile_at = [&](int t) {
+    Tile J;
+    int e = 0;
+    for (int base = 0; base < p.E; base += kWave) {
+      const bool before = base + lane < p.E && tiles_to[base + lane] <= t;
+      e += __builtin_popcountll(__builtin_amdgcn_ballot_w64(before));
+    }
+    const int local = t - (e > 0 ? __builtin_amdgcn_readfirstlane(tiles_to[e - 1]) : 0);
+    const int rows = __builtin_amdgcn_readfirstlane(n_rows[e]);
+    J.e = e;
+    J.part = local / per;
+    J.a0 = local % per / tb * kTile;
+    J.b0 = local % per % tb * kTile;
+    const int left = rows - J.part * p.chunk;
+    J.cnt = left < p.chunk ? left : p.chunk;
+    J.row = (int64_t)__builtin_amdgcn_readfirstlane(first_row[e]) + (int64_t)J.part * p.chunk;
+    return J;
+  };
+
+  // Loads of a stage: wavefronts 0-1 fetch dy, 2-3 x; each 128 columns, as
+  // eight pieces of 1 KiB: four rows by 256 bytes, lane i row i / 16 of the
+  // piece. Chunk c of row r sits at c ^ 4 (r % 4): the transposing reads
+  // then cover all banks. Columns past the matrix read the next row's (or
+  // zeros past the last): they feed sums that are never stored. Rows past
+  // the chunk lie past the range and read as zeros.
+  const int op = wave >> 1;
+  const uint32_t ld = (uint32_t)(op == 0 ? p.ldy : p.ldx);  // bytes
+  const char* src = op == 0 ? p.dy : p.x;
+  const int width = op == 0 ? p.N : p.K;
+  const uint32_t vo =
+      (uint32_t)(lane >> 4) * ld + (uint32_t)((lane & 15) ^ (4 * (lane >> 4))) * 16;
+  const uint32_t dst0 = (uint32_t)(uintptr_t)(lds_char*)&lds[0][0] +
+                        (uint32_t)(op * kOpBytes + (wave & 1) * (kOpBytes / 2));
+  struct FetchTile {
+    __amdgpu_buffer_rsrc_t rs;
+    int stages;
+  };
+  auto fetch_tile = [&](const Tile& J) {
+    FetchTile F;
+    const int col = (op == 0 ? J.a0 : J.b0) + 128 * (wave & 1);
+    F.stages = (J.cnt + kStageRows - 1) / kStageRows;
+    F.rs = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(src + J.row * ld + (int64_t)col * 2), 0,
+        J.cnt > 0 && col < width
+            ? (int)((uint32_t)(J.cnt - 1) * ld + (uint32_t)(width - col) * 2u)
+            : 0,
+        kRsrcWord3);
+    return F;
+  };
+  // The fetch cursor: tile ft of the workgroup's list, its stage fs; past the
+  // last tile, stages that load nothing, so that every stage issues the same
+  // loads.
+  int ft = t_first, fs = 0;
+  FetchTile F = fetch_tile(tile_at(ft));
+  auto next_stage = [&]() -> uint32_t {
+    while (ft < t_end && fs >= F.stages) {
+      ft += Q;
+      fs = 0;
+      if (ft < t_end) F = fetch_tile(tile_at(ft));
+    }
+    const uint32_t off = ft < t_end ? (uint32_t)(fs * kStageRows) * ld : kOutOfRange;
+    ++fs;
+    return off;
+  };
+  auto fetch = [&](uint32_t off, int slot, int x) {
+    lds_load16(F.rs, vo, off + (uint32_t)(4 * x) * ld, dst0 + (uint32_t)(slot * kSlotBytes + x * 1024));
+  };
+
+  // Transposed read: in each group of 16 lanes, lane i receives 16-bit
+  // element i % 4 of the 8 bytes addressed by lanes 4 j + i / 4, j = 0..3.
+  // Lanes 4 j + q of group g address row 8 (g / 2) + j (+ 4) of the step's
+  // 16 and columns 16 (g % 2) + 4 q of a 32-column block.
+  const int grp = lane >> 4, gj = (lane >> 2) & 3, gq = lane & 3;
+  const int tr = (2 * (grp >> 1)) * 1024 + gj * 256 + (gq & 1) * 8;
+  const lds_char* ldsb = (const lds_char*)&lds[0][0];
+  auto frag = [&](int o, int slot, int blk, int ks) -> u32x4 {
+    const int chunk = (blk * 4 + 2 * (grp & 1) + (gq >> 1)) ^ (4 * gj);
+    const lds_char* at = ldsb + slot * kSlotBytes + o * kOpBytes +
+                         (o == 0 ? wa : wb) * (kOpBytes / 2) + ks * 4096 + tr + chunk * 16;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 1024));
+    return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+
+  f32x16 acc[4][4];  // [k block][n block]
+  u32x4 fb0[4], fa0[4], fb1[4], fa1[4];
+  // in the order the MFMAs first use them
+  auto read_one = [&](u32x4 (&fb)[4], u32x4 (&fa)[4], int slot, int ks, int x) {
+    if (x == 0)
+      fb[0] = frag(1, slot, 0, ks);
+    else if (x <= 4)
+      fa[x - 1] = frag(0, slot, x - 1, ks);
+    else
+      fb[x - 4] = frag(1, slot, x - 4, ks);
+  };
+  constexpr int kOps = 12;  // 8 fragment reads, 4 loads
+  auto mma_step = [&](const u32x4 (&fb)[4], const u32x4 (&fa)[4], auto op_) {
+#pragma unroll
+    for (int n = 0; n < 16; ++n) {
+      const int i = n / 4, j = n % 4;
+      acc[i][j] = mma<T>(fa[j], fb[i], acc[i][j]);
+#pragma unroll
+      for (int x = n * kOps / 16; x < (n + 1) * kOps / 16; ++x) op_(x);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  // Lane: k = column l32 of a block, n = rows 8 (v / 4) + 4 half + v % 4:
+  // every store writes two 128-byte row pieces.
+  const uint32_t rowb = (uint32_t)p.K * 4u;
+  auto epilogue = [&](const Tile& J) {
+    asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+    float* out = p.dw + (int64_t)J.e * p.N * p.K;
+    bool add = p.accumulate != 0;
+    if (J.part > 0) {
+      const int slot = __builtin_amdgcn_readfirstlane(slots_to[J.e]) + J.part - 1;
+      if (slot >= p.n_slots) return;  // only if the offsets overlap
+      out = p.slots + (int64_t)slot * p.N * p.K;
+      add = false;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int ab = J.a0 + wa * 128 + j * 32;
+      if (ab >= p.N) continue;
+      const int an = p.N - ab < 32 ? p.N - ab : 32;
+      const __amdgpu_buffer_rsrc_t ro = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(out + (int64_t)ab * p.K), 0, (int)((uint32_t)an * rowb), kRsrcWord3);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int b = J.b0 + wb * 128 + i * 32 + l32;
+        const uint32_t vo_o =
+            b < p.K ? (uint32_t)(4 * half) * rowb + (uint32_t)b * 4u : kOutOfRange;
+        auto so = [&](int v) { return (int)((uint32_t)(8 * (v / 4) + v % 4) * rowb); };
+        if (add) {
+          float o[16];
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            o[v] = __builtin_bit_cast(
+                float, __builtin_amdgcn_raw_buffer_load_b32(ro, (int)vo_o, so(v), 0));
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            __builtin_amdgcn_raw_buffer_store_b32(
+                __builtin_bit_cast(uint32_t, acc_read(acc[i][j][v]) + o[v]), ro, (int)vo_o, so(v),
+                0);
+        } else {
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            __builtin_amdgcn_raw_buffer_store_b32(
+                __builtin_bit_cast(uint32_t, acc_read(acc[i][j][v])), ro, (int)vo_o, so(v), 0);
+        }
+      }
+    }
+  };
+
+  // prologue: three stages in flight, the first waited for
+#pragma unroll
+  for (int st = 0; st < 3; ++st) {
+    const uint32_t off = next_stage();
+#pragma unroll
+    for (int x = 0; x < 8; ++x) fetch(off, st, x);
+  }
+  wait_vmem_barrier<2 * kLoads>();
+#pragma unroll
+  for (int x = 0; x < 8; ++x) read_one(fb0, fa0, 0, 0, x);
+
+  // Stage g (slot g % 4): the first step's MFMAs run while the second's
+  // fragments are read and half of stage g + 3 is fetched into the slot of
+  // g - 1; the barrier waits for g + 1; the second step's MFMAs run while
+  // g + 1's first fragments are read and the rest of g + 3 is fetched.
+  int g = 0;
+  for (int ct = t_first; ct < t_end; ct += Q) {
+    const Tile CT = tile_at(ct);
+    const int stages = (CT.cnt + kStageRows - 1) / kStageRows;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    for (int cs = 0; cs < stages; ++cs, ++g) {
+      const int u = g & 3;
+      const uint32_t off = next_stage();
+      mma_step(fb0, fa0, [&](int x) {
+        if (x < 8)
+          read_one(fb1, fa1, u, 1, x);
+        else
+          fetch(off, (u + 3) & 3, x - 8);
+      });
+      wait_vmem_barrier<kLoads + kLoads / 2>();
+      mma_step(fb1, fa1, [&](int x) {
+        if (x < 8)
+          read_one(fb0, fa0, (u + 1) & 3, 0, x);
+        else
+          fetch(off, (u + 3) & 3, x - 4);
+      });
+    }
+    epilogue(CT);
+  }
+  // the loads that ran past the last stage read nothing but still write LDS
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+}  // namespace
+
+hipError_t launch_wgrad_ring(bool is_bf16, const WgradRingParams& p, int num_cus,
+                             hipStream_t st) {
+  const int grid = num_cus < 8 ? 8 : num_cus / 8 * 8;
+  if (is_bf16)
+    hipLaunchKernelGGL((ragged_wgrad_kernel<bf16>), dim3(grid), dim3(256), 0, st, p);
+  else
+    hipLaunchKernelGGL((ragged_wgrad_kernel<f16>), dim3(grid), dim3(256), 0, st, p);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -305,24 +305,38 @@ __global__ __launch_bounds__(256) void ragged_general_kernel(RaggedParams p) {
   }
 }
 
-// Adds the slots of every expert that has any to dw, in chunk order. Grid:
-// x over [N][K], y: the y-th, y + gridDim.y-th ... expert.
+// Adds the slots of every expert that has any to dw, in chunk order. The
+// workgroups share [N][K] of each such expert (found 64 experts at a time).
+// V: floats per lane and step.
+template <int V>
 __global__ __launch_bounds__(256) void ragged_add_slots_kernel(RaggedParams p) {
-  const int64_t n = (int64_t)p.A * p.B;
-  for (int e = blockIdx.y; e < p.E; e += gridDim.y) {
-    int start, rows;
-    expert_rows(p.offsets, e, p.rows, &start, &rows);
-    const int parts = (int)(((int64_t)rows + p.chunk - 1) / p.chunk);
-    if (parts <= 1) continue;
-    const int first = slots_before(p.offsets, e, p.rows, p.chunk);
-    const int own = first + parts - 1 <= p.n_slots ? parts - 1 : p.n_slots - first;
-    float* o = static_cast<float*>(p.out) + (int64_t)e * n;
-    const float* s = p.slots + (int64_t)first * n;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n;
-         i += (int64_t)gridDim.x * 256) {
-      float r = o[i];
-      for (int k = 0; k < own; ++k) r += s[(int64_t)k * n + i];
-      o[i] = r;
+  typedef float vec_t __attribute__((ext_vector_type(V)));
+  const int64_t n = (int64_t)p.A * p.B / V;
+  const int lane = threadIdx.x & 63;
+  int before = 0;  // slots of the experts below
+  for (int base = 0; base < p.E; base += kWave) {
+    int start, rows = 0, own = 0;
+    if (base + lane < p.E) {
+      expert_rows(p.offsets, base + lane, p.rows, &start, &rows);
+      own = rows > 0 ? (int)(((int64_t)rows + p.chunk - 1) / p.chunk) - 1 : 0;
+    }
+    const int incl = wave_inclusive_scan(own) + before;
+    before = __builtin_amdgcn_readlane(incl, kWave - 1);
+    uint64_t todo = __builtin_amdgcn_ballot_w64(own > 0);
+    while (todo) {
+      const int l = __builtin_ctzll(todo);
+      todo &= todo - 1;
+      const int last = __builtin_amdgcn_readlane(incl, l);
+      const int first = last - __builtin_amdgcn_readlane(own, l);
+      const int count = (last < p.n_slots ? last : p.n_slots) - first;
+      vec_t* o = static_cast<vec_t*>(p.out) + (base + l) * n;
+      const vec_t* s = reinterpret_cast<const vec_t*>(p.slots) + first * n;
+      for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n;
+           i += (int64_t)gridDim.x * 256) {
+        vec_t r = o[i];
+        for (int k = 0; k < count; ++k) r += s[k * n + i];
+        o[i] = r;
+      }
     }
   }
 }
@@ -401,15 +415,16 @@ RaggedParams base_params(const RaggedShape& s, const int32_t* offsets) {
 
 }  // namespace
 
-// Chunks: as many as give about four jobs a CU of the 256 x 256 tiles, so
-// that an expert with many rows does not hold up the launch, but at least
+// Chunks: an expert's tiles run at once, so a chunk may hold half of the rows
+// that a CU sums in all (rows * tiles / 256), or an expert with many rows
+// holds up the launch; but at least
 // 512 rows each (a chunk past the first costs a write and a read of [N][K]
 // in fp32, its product 2 N K flops a row: below some hundred rows the
 // traffic would outweigh it). A function of the shape alone: it fixes the
 // order of the sums.
 DwSplit dw_split(const RaggedShape& s) {
   const int64_t tiles = (int64_t)ceil_div(s.N, 256) * ceil_div(s.K, 256);
-  int64_t chunk = (s.rows * tiles + 1023) / 1024;
+  int64_t chunk = (s.rows * tiles + 511) / 512;
   chunk = chunk < 512 ? 512 : (chunk + 63) / 64 * 64;
   // a chunk's rows are addressed with 32-bit byte offsets
   const int64_t ld = (s.ld_x > s.ld_y ? s.ld_x : s.ld_y) * elem_bytes(s.type);
@@ -477,16 +492,19 @@ hipError_t launch_ragged_dw(const RaggedShape& s, const int32_t* offsets, const 
       aligned16(x) && aligned16(dy)) {
     const WgradRingParams r{static_cast<const char*>(dy), static_cast<const char*>(x), dw, slots,
                             offsets, s.ld_y * 2, s.ld_x * 2, (int)s.rows, s.E, s.N, s.K,
-                            p.chunk, p.n_slots, p.accumulate};
+                            p.chunk, p.n_slots, p.accumulate, 1};
     e = launch_wgrad_ring(s.type == ElemType::kBF16, r, num_cus, st);
   } else {
     e = dispatch<kWeightGrad>(s.type, p, num_cus, st);
   }
   if (e != hipSuccess || split.slots == 0) return e;
-  int gx = ceil_div((int64_t)s.N * s.K, 1024);
-  gx = gx > 4096 ? 4096 : gx;
-  const int gy = s.E < 64 ? s.E : 64;
-  hipLaunchKernelGGL(ragged_add_slots_kernel, dim3(gx, gy), dim3(256), 0, st, p);
+  const bool vec = (int64_t)s.N * s.K % 4 == 0 && aligned16(dw);
+  const int most = num_cus * 8, blocks = ceil_div((int64_t)s.N * s.K, vec ? 1024 : 256);
+  const dim3 grid(blocks < most ? blocks : most);
+  if (vec)
+    hipLaunchKernelGGL((ragged_add_slots_kernel<4>), grid, dim3(256), 0, st, p);
+  else
+    hipLaunchKernelGGL((ragged_add_slots_kernel<1>), grid, dim3(256), 0, st, p);
   return hipGetLastError();
 }
 

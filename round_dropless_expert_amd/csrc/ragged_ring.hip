@@ -91,6 +91,7 @@ __device__ __forceinline__ float acc_read(float a) {
 // Operand kinds.
 struct OpBf16 {
   static constexpr bool kScaled = false;
+  template <int kStep>
   __device__ static __forceinline__ f32x16 mma(u32x4 a, u32x4 b, int, int, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -98,38 +99,48 @@ struct OpBf16 {
 };
 struct OpF16 {
   static constexpr bool kScaled = false;
+  template <int kStep>
   __device__ static __forceinline__ f32x16 mma(u32x4 a, u32x4 b, int, int, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
   }
 };
 // 4-bit values: lane l supplies row l % 32, values 32 (l / 32) .. + 31 of
-// the step's 64 (one block) and the block's scale byte.
+// the step's 64 (one block) and the block's scale, byte 2 kStep of its
+// scale register (the instruction's byte select).
 struct OpMx {
   static constexpr bool kScaled = true;
+  template <int kStep>
   __device__ static __forceinline__ f32x16 mma(u32x4 a, u32x4 b, int sa, int sb, f32x16 c) {
     const i32x8 av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
     const i32x8 bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, 0, sa, 0, sb);
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, 2 * kStep, sa,
+                                                           2 * kStep, sb);
   }
 };
 
 template <int WI, int WJ>
 struct Frags {
   u32x4 a[WI], b[WJ];
-  int sa[WI], sb[WJ];  // scale bytes (MXFP4)
+};
+// Scales of a stage (MXFP4): byte 0 is the lane's block of step 0, byte 2 of
+// step 1.
+template <int WI, int WJ>
+struct Scales {
+  int a[WI], b[WJ];
 };
 
 // One MFMA step with kOps other operations spread over it in a fixed order
 // (op(x) after MFMA i for x in [i kOps / M, (i + 1) kOps / M)), each group
 // fenced so that the compiler keeps the order.
-template <typename Op, int WI, int WJ, int kOps, typename F>
-__device__ __forceinline__ void mma_step(f32x16 (&acc)[WI][WJ], const Frags<WI, WJ>& f, F op) {
+template <typename Op, int kStep, int WI, int WJ, int kOps, typename F>
+__device__ __forceinline__ void mma_step(f32x16 (&acc)[WI][WJ], const Frags<WI, WJ>& f,
+                                         const Scales<WI, WJ>& s, F op) {
   constexpr int M = WI * WJ;
 #pragma unroll
   for (int i = 0; i < M; ++i) {
-    acc[i / WJ][i % WJ] = Op::mma(f.a[i / WJ], f.b[i % WJ], f.sa[i / WJ], f.sb[i % WJ],
-                                  acc[i / WJ][i % WJ]);
+    acc[i / WJ][i % WJ] = Op::template mma<kStep>(f.a[i / WJ], f.b[i % WJ], s.a[i / WJ],
+                                                  s.b[i % WJ], acc[i / WJ][i % WJ]);
 #pragma unroll
     for (int x = i * kOps / M; x < (i + 1) * kOps / M; ++x) op(x);
     __builtin_amdgcn_sched_barrier(0);
@@ -143,7 +154,79 @@ struct TileSrc {
   __amdgpu_buffer_rsrc_t rs[kScaleLoads > 0 ? kScaleLoads : 1];
 };
 
-template <typename Op, typename Out, int WI, int WJ, int SPB, bool kTransW>
+// A wavefront's part of a tile's output: rows m0 .. of the expert's m (from
+// buffer row `start`), features n0 .. Lane (l32, half) holds, for token l32
+// of a 32-token block, features 8 q + 4 half + 0..3 of each 32-feature
+// block. The wavefront turns 32 tokens x 128 bytes of features around in 4
+// KiB of LDS and stores whole 128-byte row pieces. 16-byte chunk q of row r
+// sits at q ^ (r % 8), against bank conflicts. Non-temporal: the output is
+// next read when this launch has ended and should not displace operands in
+// L2. (The accumulators are read by asm: the caller gives the last MFMAs the
+// wait states that the compiler cannot see.)
+template <typename Out, int WI, int WJ, bool kOutVec>
+__device__ __forceinline__ void store_tile(const RingParams& p, const f32x16 (&acc)[WI][WJ],
+                                           char* stg, int start, int m, int n0, int m0, int wn,
+                                           int wm, int lane) {
+  constexpr int BN = 64 * WI, BM = 64 * WJ;
+  const int half = lane >> 5, l32 = lane & 31;
+
+  constexpr int kOs = sizeof(Out), kPerBlk = kOs == 2 ? 2 : 1;  // 32-feature blocks
+  const int mr = m - m0 < BM ? m - m0 : BM;
+  const uint32_t ldo = (uint32_t)p.ldo;
+  const __amdgpu_buffer_rsrc_t ro = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(p.out + ((int64_t)start + m0) * p.ldo), 0,
+      (int)((uint32_t)(mr - 1) * ldo + (uint32_t)p.B * kOs), kRsrcWord3);
+  const int rrow = lane >> 3, rchunk = lane & 7;
+#pragma unroll
+  for (int jb = 0; jb < WJ; ++jb) {
+    const int row0 = wm * (BM / 2) + jb * 32;
+#pragma unroll
+    for (int ip = 0; ip < WI / kPerBlk; ++ip) {
+#pragma unroll
+      for (int u = 0; u < kPerBlk; ++u) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          typedef Out vec4_t __attribute__((ext_vector_type(4)));
+          vec4_t o;
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            o[v] = from_f32<Out>(acc_read(acc[kPerBlk * ip + u][jb][4 * q + v]));
+          if constexpr (kOs == 2) {
+            const int chunk = (u * 4 + q) ^ (l32 & 7);
+            *reinterpret_cast<u32x2*>(stg + l32 * 128 + chunk * 16 + half * 8) =
+                __builtin_bit_cast(u32x2, o);
+          } else {
+            const int chunk = (2 * q + half) ^ (l32 & 7);
+            *reinterpret_cast<u32x4*>(stg + l32 * 128 + chunk * 16) =
+                __builtin_bit_cast(u32x4, o);
+          }
+        }
+      }
+      const int feat = n0 + wn * (BN / 2) + ip * 32 * kPerBlk + rchunk * (16 / kOs);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + rrow;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(
+            stg + r * 128 + ((rchunk ^ (r & 7)) * 16));
+        // rows past the expert's fall past the range
+        const uint32_t at = (uint32_t)(row0 + r) * ldo + (uint32_t)feat * kOs;
+        if constexpr (kOutVec) {
+          __builtin_amdgcn_raw_buffer_store_b128(v, ro, feat < p.B ? at : kOutOfRange, 0,
+                                                 kNonTemporal);
+        } else if (row0 + r < mr) {
+          Out* o = reinterpret_cast<Out*>(p.out + ((int64_t)start + m0) * p.ldo + at);
+          typedef Out vec_t __attribute__((ext_vector_type(16 / kOs)));
+          const vec_t e = __builtin_bit_cast(vec_t, v);
+#pragma unroll
+          for (int k = 0; k < 16 / kOs; ++k)
+            if (feat + k < p.B) o[k] = e[k];
+        }
+      }
+    }
+  }
+}
+
+template <typename Op, typename Out, int WI, int WJ, int SPB, bool kTransW, bool kOutVec>
 __global__ __launch_bounds__(256, 1) void ring_kernel(RingParams p) {
   constexpr bool kScaled = Op::kScaled;
   static_assert(!kScaled || !kTransW, "MXFP4: forward only");
@@ -282,25 +365,32 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(RingParams p) {
         exists ? (int)((uint32_t)(mr - 1) * lda + (uint32_t)p.cbytes) : 0, kRsrcWord3);
 #pragma unroll
     for (int j = 0; j < kScaleLoads; ++j) {
-      // piece j 4 + wave: 64 weight rows, then 64 token rows
+      // piece j 4 + wave: 64 positions of the weight rows, then of the tokens'
       const int piece = j * 4 + wave;
       const bool w = piece < kWPasses;
-      const int r0 = (w ? piece : piece - kWPasses) * 64;
-      const int live = (w ? fw : mr) - r0;
-      const char* base = w ? p.w_scales + ((int64_t)T.e * p.B + T.n0 + r0) * p.lds
-                           : p.act_scales + (row + r0) * p.lds;
+      const char* base = w ? p.w_scales + ((int64_t)T.e * p.B + T.n0) * p.lds
+                           : p.act_scales + row * p.lds;
       S.rs[j] = __builtin_amdgcn_make_buffer_rsrc(
           (void*)base, 0,
-          exists && piece < kPasses && live > 0 ? (int)((uint32_t)(live < 64 ? live : 64) *
-                                                        (uint32_t)p.lds)
-                                                : 0,
+          exists && piece < kPasses ? (int)((uint32_t)(w ? fw : mr) * (uint32_t)p.lds) : 0,
           kRsrcWord3);
     }
     return S;
   };
 
   const uint32_t lds_wave = (uint32_t)wave * 1024u;
-  const uint32_t vo_s = (uint32_t)lane * (uint32_t)p.lds;
+  // Scale dwords: position l32 W + r of a wavefront's 32 W rows is row 32 r
+  // + l32, so that one LDS read brings a lane the scales of its W blocks.
+  uint32_t vo_s[kScaleLoads > 0 ? kScaleLoads : 1];
+#pragma unroll
+  for (int j = 0; j < kScaleLoads; ++j) {
+    const int piece = j * 4 + wave;
+    const bool w = piece < kWPasses;
+    const int pos = (w ? piece : piece - kWPasses) * 64 + lane, W = w ? WI : WJ;
+    const int in = pos % (32 * W);
+    const int row = pos / (32 * W) * (32 * W) + in % W * 32 + in / W;
+    vo_s[j] = (uint32_t)row * (uint32_t)p.lds;
+  }
   struct StageOff {
     uint32_t w[SPB], t[SPB], vw[SPB], vt[SPB];
   };
@@ -329,7 +419,7 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(RingParams p) {
     } else if constexpr (kScaled) {
       const int j = i - kPasses;
       // a stage's four scale bytes of a row: 1/16 of its bytes of codes
-      lds_load4(S.rs[j], vo_s, o.t[sub] == kOutOfRange ? kOutOfRange : o.t[sub] / 16,
+      lds_load4(S.rs[j], vo_s[j], o.t[sub] == kOutOfRange ? kOutOfRange : o.t[sub] / 16,
                 at + (BN + BM) * kRowBytes + (uint32_t)(j * 4 + wave) * 256u);
     }
   };
@@ -362,27 +452,45 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(RingParams p) {
     return *reinterpret_cast<const u32x4*>(stage + row * kRowBytes +
                                            (((2 * s + half) ^ ((row >> 2) & 3)) << 4));
   };
-  // scale byte of a row's block 2 s + half. A block past K holds no codes,
-  // but its scale byte may be anything: in the stage that ends K, 0 (keep:
-  // this lane's mask of step s)
-  auto sfrag = [&](const char* stage, int row, int s, int keep) -> int {
-    return keep & *reinterpret_cast<const uint8_t*>(stage + (BN + BM) * kRowBytes + row * 4 +
-                                                    2 * s + half);
+  // Scales of a stage. The lane's two blocks are bytes half and 2 + half of
+  // its rows' dwords: shifted to bytes 0 and 2. A block past K holds no codes,
+  // but its scale byte may be anything: in the stage that ends K it becomes 0
+  // (`keep`).
+  const int nb = tail / 16;  // blocks of the last stage
+  const int keep_last = kScaled ? (half < nb ? 255 : 0) | (2 + half < nb ? 255 << 16 : 0) : 0;
+  auto read_scales = [&](int (&raw)[WI + WJ], const char* stage) {
+    const char* sc = stage + (BN + BM) * kRowBytes;
+    typedef int wi_t __attribute__((ext_vector_type(WI)));
+    typedef int wj_t __attribute__((ext_vector_type(WJ)));
+    const wi_t a = *reinterpret_cast<const wi_t*>(sc + (wn * 32 + l32) * 4 * WI);
+    const wj_t b = *reinterpret_cast<const wj_t*>(sc + BN * 4 + (wm * 32 + l32) * 4 * WJ);
+#pragma unroll
+    for (int i = 0; i < WI; ++i) raw[i] = a[i];
+#pragma unroll
+    for (int j = 0; j < WJ; ++j) raw[WI + j] = b[j];
+  };
+  auto set_scales = [&](Scales<WI, WJ>& sc, const int (&raw)[WI + WJ], int g) {
+    const int keep = g == KT - 1 ? keep_last : 0x00ff00ff;
+#pragma unroll
+    for (int i = 0; i < WI; ++i) sc.a[i] = (int)((uint32_t)raw[i] >> (8 * half)) & keep;
+#pragma unroll
+    for (int j = 0; j < WJ; ++j) sc.b[j] = (int)((uint32_t)raw[WI + j] >> (8 * half)) & keep;
   };
   Frags<WI, WJ> f0, f1;
-  // `g`: the stage's number
-  auto keep_of = [&](int g, int s) {
-    return !kScaled || g != KT - 1 || (2 * s + half) * 16 < tail ? 255 : 0;
-  };
-  auto read_one = [&](Frags<WI, WJ>& f, const char* stage, int s, int keep, int r) {
-    if (r < WI) {
+  Scales<WI, WJ> sc;
+  int raw[WI + WJ];
+  auto read_one = [&](Frags<WI, WJ>& f, const char* stage, int s, int r) {
+    if (r < WI)
       f.a[r] = wfrag(stage, r, s);
-      if constexpr (kScaled) f.sa[r] = sfrag(stage, wn * (BN / 2) + r * 32 + l32, s, keep);
-    } else {
+    else
       f.b[r - WI] = tfrag(stage, r - WI, s);
-      if constexpr (kScaled)
-        f.sb[r - WI] = sfrag(stage, BN + wm * (BM / 2) + (r - WI) * 32 + l32, s, keep);
-    }
+  };
+  // what a stage's first step needs
+  auto read_first = [&](const char* stage) {
+    if constexpr (kScaled) read_scales(raw, stage);
+#pragma unroll
+    for (int r = 0; r < kReads; ++r) read_one(f0, stage, 0, r);
+    if constexpr (kScaled) set_scales(sc, raw, 0);
   };
 
   Tile T = locate(tile);
@@ -397,8 +505,7 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(RingParams p) {
     for (int x = 0; x < kLoads; ++x) fetch_one(slot2, o2, cur, x);
   }
   wait_vmem_barrier<kWait>();
-#pragma unroll
-  for (int r = 0; r < kReads; ++r) read_one(f0, slot0, 0, keep_of(0, 0), r);
+  read_first(slot0);
 
   f32x16 acc[WI][WJ];
   while (true) {
@@ -425,25 +532,25 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(RingParams p) {
       const char* cs = CUR + sub * kStageBytes;                                         \
       const char* ns = sub + 1 < SPB ? CUR + (sub + 1) * kStageBytes : NXT;             \
       const int g = (KS_) * SPB + sub;                                                  \
-      const int k1 = keep_of(g, 1);                                                     \
-      mma_step<Op, WI, WJ, kReads + kLoadsPerStep>(acc, f0, [&](int x) {                \
+      mma_step<Op, 0, WI, WJ, kReads + kLoadsPerStep>(acc, f0, sc, [&](int x) {         \
         if (x < kReads) {                                                               \
-          read_one(f1, cs, 1, k1, x);                                                   \
+          read_one(f1, cs, 1, x);                                                       \
         } else {                                                                        \
           const int li = 2 * sub * kLoadsPerStep + x - kReads;                          \
           if (li < kLoads) fetch_one(FSLOT, SO, F, li);                                 \
         }                                                                               \
       });                                                                               \
       if (sub + 1 == SPB) wait_vmem_barrier<kWait>();                                   \
-      const int k0 = keep_of(g + 1 == KS4 * SPB ? 0 : g + 1, 0);                        \
-      mma_step<Op, WI, WJ, kReads + kLoadsPerStep>(acc, f1, [&](int x) {                \
+      if constexpr (kScaled) read_scales(raw, ns);                                      \
+      mma_step<Op, 1, WI, WJ, kReads + kLoadsPerStep>(acc, f1, sc, [&](int x) {         \
         if (x < kReads) {                                                               \
-          read_one(f0, ns, 0, k0, x);                                                   \
+          read_one(f0, ns, 0, x);                                                       \
         } else {                                                                        \
           const int li = (2 * sub + 1) * kLoadsPerStep + x - kReads;                    \
           if (li < kLoads) fetch_one(FSLOT, SO, F, li);                                 \
         }                                                                               \
       });                                                                               \
+      if constexpr (kScaled) set_scales(sc, raw, g + 1 == KS4 * SPB ? 0 : g + 1);       \
     }                                                                                   \
   }
     src_t F = cur;
@@ -470,63 +577,8 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(RingParams p) {
     // (The accumulators are read by asm: give the last MFMAs the wait states
     // that the compiler cannot see.)
     asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
-    {
-      constexpr int kOs = sizeof(Out), kPerBlk = kOs == 2 ? 2 : 1;  // 32-feature blocks
-      const int mr = T.m - T.m0 < BM ? T.m - T.m0 : BM;
-      const uint32_t ldo = (uint32_t)p.ldo;
-      const __amdgpu_buffer_rsrc_t ro = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(p.out + ((int64_t)T.start + T.m0) * p.ldo), 0,
-          (int)((uint32_t)(mr - 1) * ldo + (uint32_t)p.B * kOs), kRsrcWord3);
-      char* stg = slot3 + wave * 4096;
-      const int rrow = lane >> 3, rchunk = lane & 7;
-#pragma unroll
-      for (int jb = 0; jb < WJ; ++jb) {
-        const int row0 = wm * (BM / 2) + jb * 32;
-#pragma unroll
-        for (int ip = 0; ip < WI / kPerBlk; ++ip) {
-#pragma unroll
-          for (int u = 0; u < kPerBlk; ++u) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              typedef Out vec4_t __attribute__((ext_vector_type(4)));
-              vec4_t o;
-#pragma unroll
-              for (int v = 0; v < 4; ++v)
-                o[v] = from_f32<Out>(acc_read(acc[kPerBlk * ip + u][jb][4 * q + v]));
-              if constexpr (kOs == 2) {
-                const int chunk = (u * 4 + q) ^ (l32 & 7);
-                *reinterpret_cast<u32x2*>(stg + l32 * 128 + chunk * 16 + half * 8) =
-                    __builtin_bit_cast(u32x2, o);
-              } else {
-                const int chunk = (2 * q + half) ^ (l32 & 7);
-                *reinterpret_cast<u32x4*>(stg + l32 * 128 + chunk * 16) =
-                    __builtin_bit_cast(u32x4, o);
-              }
-            }
-          }
-          const int feat = T.n0 + wn * (BN / 2) + ip * 32 * kPerBlk + rchunk * (16 / kOs);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = i * 8 + rrow;
-            const u32x4 v = *reinterpret_cast<const u32x4*>(
-                stg + r * 128 + ((rchunk ^ (r & 7)) * 16));
-            // rows past the expert's fall past the range
-            const uint32_t at = (uint32_t)(row0 + r) * ldo + (uint32_t)feat * kOs;
-            if (p.out_vec) {
-              __builtin_amdgcn_raw_buffer_store_b128(v, ro, feat < p.B ? at : kOutOfRange, 0,
-                                                     kNonTemporal);
-            } else if (row0 + r < mr) {
-              Out* o = reinterpret_cast<Out*>(p.out + ((int64_t)T.start + T.m0) * p.ldo + at);
-              typedef Out vec_t __attribute__((ext_vector_type(16 / kOs)));
-              const vec_t e = __builtin_bit_cast(vec_t, v);
-#pragma unroll
-              for (int k = 0; k < 16 / kOs; ++k)
-                if (feat + k < p.B) o[k] = e[k];
-            }
-          }
-        }
-      }
-    }
+    store_tile<Out, WI, WJ, kOutVec>(p, acc, slot3 + wave * 4096, T.start, T.m, T.n0, T.m0, wn, wm,
+                                     lane);
     // every wavefront's staging reads are done before the next tile's ring
     // writes slot 3
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -534,8 +586,316 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(RingParams p) {
     asm volatile("" ::: "memory");
     if (!has_next) break;
     // slot 0 holds the next tile's first stage
+    read_first(slot0);
+    tile = tile_n;
+    T = Tn;
+    cur = nxt;
+  }
+  // the loads that ran past the last tile read nothing but still write LDS
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// The 256 x 256 tile on wide slots: 128 bytes of c per row, so that every
+// load reads whole 128-byte lines (a 64-byte stage asks the L2 for each line
+// twice, and the L2's request rate is what the tile is nearest to). A slot is
+// 64 KiB, two fit; a slot's last fragments are read a step before its last
+// MFMAs, so the loads of the slot after the next one start there: half in
+// the slot's last step, half in the first step of the next, and have two
+// steps (1024 MFMA cycles) and more to land.
+template <typename Op, typename Out, bool kTransW, bool kOutVec>
+__global__ __launch_bounds__(256, 1) void wide_ring_kernel(RingParams p) {
+  constexpr bool kScaled = Op::kScaled;
+  static_assert(!kScaled || !kTransW, "MXFP4: forward only");
+  constexpr int WI = 4, WJ = 4, BN = 256, BM = 256;
+  constexpr int kWide = 128;                 // bytes of c per row and slot
+  constexpr int kOpBytes = 256 * kWide;      // one operand's share of a slot
+  constexpr int kSlotBytes = 2 * kOpBytes;
+  constexpr int kPasses = 16;                // 16-byte loads per slot and thread
+  constexpr int kReads = WI + WJ;
+
+  __shared__ __attribute__((aligned(1024))) char slots[2][kSlotBytes];
+  __shared__ __attribute__((aligned(1024))) char staging[4][4096];
+  // scales of two slots: 16 bytes a row
+  __shared__ __attribute__((aligned(1024))) char scales[kScaled ? 512 * 16 : 16];
+  __shared__ int32_t tiles_to[kRaggedMaxExperts];  // tiles of the experts up to e
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave & 1, wm = wave >> 1;
+  const int half = lane >> 5, l32 = lane & 31;
+
+  const int nt = (p.B + BN - 1) / BN;
+  if (wave == 0) {
+    int carry = 0;
+    for (int base = 0; base < p.E; base += kWave) {
+      int start = 0, rows = 0;
+      if (base + lane < p.E) expert_rows(p.offsets, base + lane, p.rows, &start, &rows);
+      const int incl = wave_inclusive_scan((rows + BM - 1) / BM * nt) + carry;
+      if (base + lane < p.E) tiles_to[base + lane] = incl;
+      carry = __builtin_amdgcn_readlane(incl, kWave - 1);
+    }
+  }
+  __syncthreads();
+  const int total = __builtin_amdgcn_readfirstlane(tiles_to[p.E - 1]);
+
+  const int G = gridDim.x;
+  int tile = (int)(blockIdx.x % 8) * (G / 8) + (int)(blockIdx.x / 8);
+  if (tile >= total) return;
+
+  struct Tile {
+    int e, start, m, n0, m0;
+  };
+  auto locate = [&](int t) {
+    Tile T;
+    int e = 0;
+    for (int base = 0; base < p.E; base += kWave) {
+      const bool before = base + lane < p.E && tiles_to[base + lane] <= t;
+      e += __builtin_popcountll(__builtin_amdgcn_ballot_w64(before));
+    }
+    T.e = e;
+    expert_rows(p.offsets, e, p.rows, &T.start, &T.m);
+    T.start = __builtin_amdgcn_readfirstlane(T.start);
+    T.m = __builtin_amdgcn_readfirstlane(T.m);
+    const int mt = (T.m + BM - 1) / BM;
+    const int local = t - (e > 0 ? __builtin_amdgcn_readfirstlane(tiles_to[e - 1]) : 0);
+    T.n0 = local / mt * BN;
+    T.m0 = local % mt * BM;
+    return T;
+  };
+
+  const uint32_t lda = (uint32_t)p.lda, ldw = (uint32_t)p.ldw;
+  // c along the rows: a load moves 32 rows by 128 bytes, lane tid 16 bytes of
+  // row tid / 8, to chunk tid % 8; logical chunk q of row r sits at q ^ (r /
+  // 2) % 8, so that the 16 rows of a fragment read's cycle cover all banks.
+  const int lr = tid >> 3, lc = (tid & 7) ^ ((lr >> 1) & 7);
+  const uint32_t vo_t = (uint32_t)lr * lda + (uint32_t)lc * 16;
+  // c down the columns: 32 rows c by 128 features are eight pieces of 1 KiB
+  // (four rows by 256 bytes); a slot holds 64 rows c
+  const uint32_t vo_w =
+      kTransW ? (uint32_t)(lane >> 4) * ldw + (uint32_t)((lane & 15) ^ (4 * (lane >> 4))) * 16
+              : (uint32_t)lr * ldw + (uint32_t)lc * 16;
+  const int KP = (p.cbytes + kWide - 1) / kWide;  // slots of a tile that hold any c
+  const int KP2 = (KP + 1) / 2 * 2;
+  const bool dead = (KP - 1) * kWide + lc * 16 >= p.cbytes;
+  const uint32_t vo_t_last = dead ? kOutOfRange : vo_t;
+  const uint32_t vo_w_last = !kTransW && dead ? kOutOfRange : vo_w;
+  const uint32_t wstep = kTransW ? 64u * ldw : (uint32_t)kWide;
+  const uint32_t vo_s = (uint32_t)((wave & 1) * 128 + lane) * (uint32_t)p.lds;
+
+  struct Src {
+    __amdgpu_buffer_rsrc_t rw, ra, rs;
+  };
+  auto sources = [&](const Tile& T, bool exists) {
+    Src S;
+    const int fw = p.B - T.n0 < BN ? p.B - T.n0 : BN;
+    const int mr = T.m - T.m0 < BM ? T.m - T.m0 : BM;
+    const char* wb = p.w + (int64_t)T.e * p.wbytes;
+    if constexpr (kTransW)  // features past B read the next row's: never stored
+      S.rw = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(wb + (int64_t)T.n0 * 2), 0,
+          exists ? (int)((uint32_t)(p.C - 1) * ldw + (uint32_t)(p.B - T.n0) * 2u) : 0, kRsrcWord3);
+    else
+      S.rw = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(wb + (int64_t)T.n0 * p.ldw), 0,
+          exists ? (int)((uint32_t)(fw - 1) * ldw + (uint32_t)p.cbytes) : 0, kRsrcWord3);
+    const int64_t row = (int64_t)T.start + T.m0;
+    S.ra = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(p.act + row * p.lda), 0,
+        exists ? (int)((uint32_t)(mr - 1) * lda + (uint32_t)p.cbytes) : 0, kRsrcWord3);
+    S.rs = S.ra;
+    if constexpr (kScaled) {
+      // wavefronts 0-1 fetch the weights' scales, 2-3 the tokens'. A row's
+      // last 16 bytes may reach past it: into the next row, or past the
+      // array, which the range ends (dword by dword).
+      const int64_t w_row = (int64_t)T.e * p.B + T.n0;
+      const bool w = wave < 2;
+      const int64_t left = ((w ? (int64_t)p.E * p.B - w_row : p.rows - row)) * p.lds;
+      const int64_t most = (int64_t)(w ? fw : mr) * p.lds + 12;
+      S.rs = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(w ? p.w_scales + w_row * p.lds : p.act_scales + row * p.lds), 0,
+          exists ? (int)(left < most ? left : most) : 0, kRsrcWord3);
+    }
+    return S;
+  };
+
+  // Load x of slot position ks into slot c.
+  struct Off {
+    uint32_t w, t, s, vw, vt;
+  };
+  auto offsets_of = [&](int ks) {
+    Off o;
+    const bool in = ks < KP, last = ks == KP - 1;
+    o.w = in ? (uint32_t)ks * wstep : kOutOfRange;
+    o.t = in ? (uint32_t)ks * (uint32_t)kWide : kOutOfRange;
+    o.s = in ? (uint32_t)ks * 8u : kOutOfRange;  // ks even: 16 bytes per two slots
+    o.vw = last ? vo_w_last : vo_w;
+    o.vt = last ? vo_t_last : vo_t;
+    return o;
+  };
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char*)&slots[0][0];
+  const uint32_t lds_scales = (uint32_t)(uintptr_t)(lds_char*)&scales[0];
+  const uint32_t lds_wave = (uint32_t)wave * 1024u;
+  auto fetch = [&](int c, const Off& o, const Src& S, int x) {
+    const uint32_t at = lds0 + (uint32_t)c * kSlotBytes;
+    if (x < 8) {
+      if constexpr (kTransW) {
+        // sub-stage x / 4 (32 rows c), piece wave 4 + x % 4 of its 16
+        const int piece = wave * 4 + (x & 3);
+        lds_load16(S.rw, o.vw,
+                   o.w + (uint32_t)((x >> 2) * 32 + 4 * (piece & 7)) * ldw +
+                       (uint32_t)(piece >> 3) * 256u,
+                   at + (uint32_t)((x >> 2) * 16384 + piece * 1024));
+      } else {
+        lds_load16(S.rw, o.vw, o.w + (uint32_t)(32 * x) * ldw, at + x * 4096 + lds_wave);
+      }
+    } else if (x < 16) {
+      lds_load16(S.ra, o.vt, o.t + (uint32_t)(32 * (x - 8)) * lda, at + x * 4096 + lds_wave);
+    } else if constexpr (kScaled) {
+      // scale rows 128 (wave % 2) + 64 (x - 16) + lane of the operand
+      lds_load16(S.rs, vo_s, o.s + (uint32_t)(64 * (x - 16)) * (uint32_t)p.lds,
+                 lds_scales + (uint32_t)(wave * 2 + x - 16) * 1024u);
+    }
+  };
+
+  const int grp = lane >> 4, gj = (lane >> 2) & 3, gq = lane & 3;
+  const int tr_row = (2 * (grp >> 1)) * 1024 + gj * 256 + (gq & 1) * 8;
+  const char* const slots0 = &slots[0][0];
+  // fragment r (weight blocks, then token blocks) of step s of slot c
+  Frags<WI, WJ> f0, f1;
+  auto read_one = [&](Frags<WI, WJ>& f, int c, int s, int r) {
+    const char* at = slots0 + c * kSlotBytes;
+    if (kTransW && r < WI) {
+      const int blk = wn * WI + r;
+      const int chunk = ((blk & 3) * 4 + 2 * (grp & 1) + (gq >> 1)) ^ (4 * gj);
+      const char* q = at + (s >> 1) * 16384 + (blk >> 2) * 8192 + (s & 1) * 4096 + tr_row +
+                      chunk * 16;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_char*)q);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_char*)(q + 1024));
+      f.a[r] = __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      const int row = r < WI ? wn * 128 + r * 32 + l32 : BN + wm * 128 + (r - WI) * 32 + l32;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(
+          at + row * kWide + (((2 * s + half) ^ ((row >> 1) & 7)) << 4));
+      if (r < WI)
+        f.a[r] = v;
+      else
+        f.b[r - WI] = v;
+    }
+  };
+  // Scales: raw holds two slots' (four stages of two steps) for the lane's
+  // rows; stage q's bytes half and 2 + half, shifted to bytes 0 and 2, are
+  // the lane's blocks. A block past K holds no codes, but its scale byte may
+  // be anything: it becomes 0.
+  const int KT = (p.cbytes + 63) / 64;
+  const int nb = (p.cbytes - (KT - 1) * 64) / 16;
+  const int keep_last = (half < nb ? 255 : 0) | (2 + half < nb ? 255 << 16 : 0);
+  u32x4 raw[kScaled ? 8 : 1];
+  Scales<WI, WJ> sc;
+  auto read_scales = [&]() {
 #pragma unroll
-    for (int r = 0; r < kReads; ++r) read_one(f0, slot0, 0, keep_of(0, 0), r);
+    for (int r = 0; r < kReads; ++r) {
+      const int row = r < WI ? wn * 128 + r * 32 + l32 : BN + wm * 128 + (r - WI) * 32 + l32;
+      raw[r] = *reinterpret_cast<const u32x4*>(scales + row * 16);
+    }
+  };
+  auto set_scales = [&](int q, int g) {  // stage g (q = g % 4)
+    const int keep = g < KT - 1 ? 0x00ff00ff : g == KT - 1 ? keep_last : 0;
+#pragma unroll
+    for (int i = 0; i < WI; ++i) sc.a[i] = (int)(raw[i][q] >> (8 * half)) & keep;
+#pragma unroll
+    for (int j = 0; j < WJ; ++j) sc.b[j] = (int)(raw[WI + j][q] >> (8 * half)) & keep;
+  };
+
+  // loads of a slot: 16, and 2 of scales into even ones; kFirst of them in
+  // the step that frees the slot, the rest in the next
+  constexpr int kFirst = 8;
+  constexpr int kEven = kPasses + (kScaled ? 2 : 0);
+
+  Tile T = locate(tile);
+  Src cur = sources(T, true);
+  {
+    const Off o0 = offsets_of(0), o1 = offsets_of(1);
+#pragma unroll
+    for (int x = 0; x < kEven; ++x) fetch(0, o0, cur, x);
+#pragma unroll
+    for (int x = 0; x < kFirst; ++x) fetch(1, o1, cur, x);
+  }
+  wait_vmem_barrier<kFirst>();
+  auto read_first = [&]() {
+    if constexpr (kScaled) read_scales();
+#pragma unroll
+    for (int r = 0; r < kReads; ++r) read_one(f0, 0, 0, r);
+    if constexpr (kScaled) set_scales(0, 0);
+  };
+  read_first();
+
+  f32x16 acc[WI][WJ];
+  while (true) {
+    const int tile_n = tile + G;
+    const bool has_next = tile_n < total;
+    Tile Tn = T;
+    if (has_next) Tn = locate(tile_n);
+    const Src nxt = sources(Tn, has_next);
+
+#pragma unroll
+    for (int i = 0; i < WI; ++i)
+#pragma unroll
+      for (int j = 0; j < WJ; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+
+    // Position ks in slot C. Step 0 issues the rest of position ks + 1's
+    // loads (slot 1 - C); the barrier before step 3 waits for them; step 3
+    // issues the first of ks + 2's into slot C.
+#define MOE_WIDE(C, KS_, F0, K0, F3, K3)                                                \
+  {                                                                                     \
+    constexpr int kL0 = (C) == 1 ? kEven - kFirst : kPasses - kFirst;                   \
+    {                                                                                   \
+      const Off SO = offsets_of(K0);                                                    \
+      mma_step<Op, 0, WI, WJ, kReads + kL0>(acc, f0, sc, [&](int x) {                   \
+        if (x < kReads)                                                                 \
+          read_one(f1, C, 1, x);                                                        \
+        else                                                                            \
+          fetch(1 - (C), SO, F0, kFirst + x - kReads);                                  \
+      });                                                                               \
+    }                                                                                   \
+    mma_step<Op, 1, WI, WJ, kReads>(acc, f1, sc, [&](int x) { read_one(f0, C, 2, x); }); \
+    if constexpr (kScaled) set_scales(2 * (C) + 1, 2 * (KS_) + 1);                      \
+    mma_step<Op, 0, WI, WJ, kReads>(acc, f0, sc, [&](int x) { read_one(f1, C, 3, x); }); \
+    wait_vmem_barrier<0>();                                                             \
+    if constexpr (kScaled && (C) == 1) read_scales();                                   \
+    {                                                                                   \
+      const Off SO = offsets_of(K3);                                                    \
+      mma_step<Op, 1, WI, WJ, kReads + kFirst>(acc, f1, sc, [&](int x) {                \
+        if (x < kReads)                                                                 \
+          read_one(f0, 1 - (C), 0, x);                                                  \
+        else                                                                            \
+          fetch(C, SO, F3, x - kReads);                                                 \
+      });                                                                               \
+    }                                                                                   \
+    if constexpr (kScaled)                                                              \
+      set_scales((2 * (C) + 2) & 3, (KS_) + 1 == KP2 ? 0 : 2 * (KS_) + 2);              \
+  }
+    Src F = cur;
+    int fofs = 0;
+    for (int ks = 0; ks < KP2; ks += 2) {
+      if (ks + 2 == KP2) {
+        F = nxt;
+        fofs = KP2;
+      }
+      // position ks + 1 is this tile's; from ks + 2 on the next tile's at
+      // the end
+      MOE_WIDE(0, ks, cur, ks + 1, F, ks + 2 - fofs)
+      MOE_WIDE(1, ks + 1, F, ks + 2 - fofs, F, ks + 3 - fofs)
+    }
+#undef MOE_WIDE
+
+    // Epilogue, as the narrow ring's, through a staging area of its own.
+    asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+    store_tile<Out, WI, WJ, kOutVec>(p, acc, &staging[wave][0], T.start, T.m, T.n0, T.m0, wn, wm,
+                                     lane);
+    if (!has_next) break;
+    read_first();
     tile = tile_n;
     T = Tn;
     cur = nxt;
@@ -546,8 +906,12 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(RingParams p) {
 
 template <typename Op, typename Out, int WI, int WJ, int SPB, bool kTransW>
 hipError_t launch(const RingParams& p, int grid, hipStream_t st) {
-  hipLaunchKernelGGL((ring_kernel<Op, Out, WI, WJ, SPB, kTransW>), dim3((unsigned)grid), dim3(256),
-                     0, st, p);
+  if (p.out_vec)
+    hipLaunchKernelGGL((ring_kernel<Op, Out, WI, WJ, SPB, kTransW, true>), dim3((unsigned)grid),
+                       dim3(256), 0, st, p);
+  else
+    hipLaunchKernelGGL((ring_kernel<Op, Out, WI, WJ, SPB, kTransW, false>), dim3((unsigned)grid),
+                       dim3(256), 0, st, p);
   return hipGetLastError();
 }
 
@@ -565,7 +929,18 @@ hipError_t choose(const RingParams& p, int num_cus, hipStream_t st) {
   const float big = cost(256, 256, 1.0f), medium = cost(256, 128, 0.85f),
               small = cost(128, 64, 0.45f);
   const int grid = num_cus < 8 ? 8 : num_cus / 8 * 8;
-  if (big <= medium && big <= small) return launch<Op, Out, 4, 4, 1, kTransW>(p, grid, st);
+  if (big <= medium && big <= small) {
+    // the transposed weights' loads read whole lines already: the narrow ring
+    // looks further ahead
+    if constexpr (kTransW) return launch<Op, Out, 4, 4, 1, kTransW>(p, grid, st);
+    if (p.out_vec)
+      hipLaunchKernelGGL((wide_ring_kernel<Op, Out, kTransW, true>), dim3((unsigned)grid),
+                         dim3(256), 0, st, p);
+    else
+      hipLaunchKernelGGL((wide_ring_kernel<Op, Out, kTransW, false>), dim3((unsigned)grid),
+                         dim3(256), 0, st, p);
+    return hipGetLastError();
+  }
   if (medium <= small) return launch<Op, Out, 4, 2, 1, kTransW>(p, grid, st);
   return launch<Op, Out, 2, 1, 2, kTransW>(p, grid, st);
 }

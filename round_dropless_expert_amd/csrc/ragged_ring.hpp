@@ -45,9 +45,10 @@ struct WgradRingParams {
   int rows, E, N, K;
   int chunk, n_slots;
   int accumulate;
+  int group;       // set by the launch: workgroups that take a chunk's tiles together
 };
 
-hipError_t launch_wgrad_ring(bool is_bf16, const WgradRingParams& p, int num_cus,
+hipError_t launch_wgrad_ring(bool is_bf16, const WgradRingParams& params, int num_cus,
                              hipStream_t st);
 
 hipError_t launch_ring(RingKind kind, const RingParams& p, int num_cus, hipStream_t st);

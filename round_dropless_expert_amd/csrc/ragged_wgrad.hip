@@ -9,10 +9,17 @@
 // bytes of a row at a time, and the fragments come back through gfx950's
 // transposing LDS read. A workgroup computes a 256 (n) x 256 (k) tile of one
 // expert's chunk of rows with 2 x 2 wavefronts of 128 x 128. Four LDS slots
-// form a ring with three stages in flight. Persistent: an XCD's workgroups
-// walk consecutive tiles, which share their operands in its L2, and the ring
-// runs on across a workgroup's tiles, so that the next tile's first stages
-// land while the current one is stored.
+// form a ring with three stages in flight. Persistent: the ring runs on
+// across a workgroup's tiles, so that the next tile's first stages land
+// while the current one is stored.
+//
+// Experts have very different numbers of rows, and a tile takes as long as
+// its chunk has rows. The tiles of a chunk are dealt out in blocks of `group`
+// (32 where a chunk has that many: the workgroups of one XCD, which then
+// share the chunk's rows in its L2), largest chunk first, each block to the
+// group of workgroups with the least work so far; past kDealt blocks they go
+// round the groups in turn. Every workgroup works the whole deal out for
+// itself, so it needs no memory and no order of arrival.
 //
 // An expert with more rows than a chunk is summed in several tiles; those
 // past the first go to slots of the workspace and a second launch adds them
@@ -77,13 +84,36 @@ __device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
+// Smallest value of the 64 lanes.
+__device__ __forceinline__ uint32_t wave_min(uint32_t v) {
+#define MOE_MIN_STEP(ctrl, rows)                                                             \
+  {                                                                                          \
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp((int)0xffffffff, (int)v, ctrl,  \
+                                                             rows, 0xf, false);              \
+    v = v < o ? v : o;                                                                       \
+  }
+  MOE_MIN_STEP(0x111, 0xf)  // row_shr:1, 2, 4, 8: lane 15 of each row of 16
+  MOE_MIN_STEP(0x112, 0xf)
+  MOE_MIN_STEP(0x114, 0xf)
+  MOE_MIN_STEP(0x118, 0xf)
+  MOE_MIN_STEP(0x142, 0xa)  // row_bcast:15 into rows 1 and 3
+  MOE_MIN_STEP(0x143, 0xc)  // row_bcast:31 into rows 2 and 3
+#undef MOE_MIN_STEP
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+constexpr int kDealt = 64;
+
 template <typename T>
 __global__ __launch_bounds__(256, 1) void ragged_wgrad_kernel(WgradRingParams p) {
   __shared__ __attribute__((aligned(1024))) char lds[kSlots][kSlotBytes];
-  __shared__ int32_t tiles_to[kRaggedMaxExperts];  // tiles of the experts up to e
-  __shared__ int32_t slots_to[kRaggedMaxExperts];  // slots of the experts below e
   __shared__ int32_t first_row[kRaggedMaxExperts];
   __shared__ int32_t n_rows[kRaggedMaxExperts];
+  __shared__ int32_t slots_to[kRaggedMaxExperts];   // slots of the experts below e
+  __shared__ int32_t order[kRaggedMaxExperts];      // experts by falling rows
+  __shared__ int32_t blocks_to[kRaggedMaxExperts];  // blocks up to that place of the order
+  __shared__ int32_t dealt[kDealt];                 // this group's among the first blocks
+  __shared__ int32_t n_dealt;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wa = wave & 1, wb = wave >> 1;  // this wavefront's 128 x 128 quarter
@@ -91,62 +121,118 @@ __global__ __launch_bounds__(256, 1) void ragged_wgrad_kernel(WgradRingParams p)
 
   const int ta = (p.N + kTile - 1) / kTile, tb = (p.K + kTile - 1) / kTile;
   const int per = ta * tb;
-  if (wave == 0) {
-    int tiles = 0, slots = 0;
-    for (int base = 0; base < p.E; base += kWave) {
-      const int e = base + lane;
-      int start = 0, rows = 0, parts = 0;
-      if (e < p.E) {
-        expert_rows(p.offsets, e, p.rows, &start, &rows);
-        parts = (int)(((int64_t)rows + p.chunk - 1) / p.chunk);
-      }
-      const int extra = parts > 1 ? parts - 1 : 0;
-      // an expert without rows still stores its zeros
-      const int jobs = e < p.E && parts == 0 && !p.accumulate ? 1 : parts;
-      const int incl = wave_inclusive_scan(jobs * per) + tiles;
-      const int sincl = wave_inclusive_scan(extra) + slots;
-      if (e < p.E) {
-        tiles_to[e] = incl;
-        slots_to[e] = sincl - extra;
-        first_row[e] = start;
-        n_rows[e] = rows;
-      }
-      tiles = __builtin_amdgcn_readlane(incl, kWave - 1);
-      slots = __builtin_amdgcn_readlane(sincl, kWave - 1);
-    }
+  for (int e = tid; e < p.E; e += 256) {
+    int start, rows;
+    expert_rows(p.offsets, e, p.rows, &start, &rows);
+    first_row[e] = start;
+    n_rows[e] = rows;
   }
   __syncthreads();
-  const int total = __builtin_amdgcn_readfirstlane(tiles_to[p.E - 1]);
+  for (int e = tid; e < p.E; e += 256) {
+    const int r = n_rows[e];
+    int before = 0;
+    for (int j = 0; j < p.E; ++j) before += n_rows[j] > r || (n_rows[j] == r && j < e);
+    order[before] = e;
+  }
+  __syncthreads();
 
-  // XCD x takes the tiles [x n8, (x + 1) n8), its Q workgroups every Q-th.
-  const int Q = (int)gridDim.x / 8;
-  const int xcd = (int)(blockIdx.x % 8), q = (int)(blockIdx.x / 8);
-  const int n8 = (total + 7) / 8;
-  const int t_first = xcd * n8 + q;
-  const int t_end = (xcd + 1) * n8 < total ? (xcd + 1) * n8 : total;
-  if (t_first >= t_end) return;
+  // this workgroup's group and its place in it; an XCD's workgroups (b % 8)
+  // are consecutive
+  const int place = (int)(blockIdx.x % 8) * ((int)gridDim.x / 8) + (int)(blockIdx.x / 8);
+  const int groups = (int)gridDim.x / p.group;
+  const int my_group = place / p.group, member = place % p.group;
+  const int per_blocks = (per + p.group - 1) / p.group;  // blocks of a chunk
+  auto parts_of = [&](int rows) {
+    const int n = (int)(((int64_t)rows + p.chunk - 1) / p.chunk);
+    return n == 0 && !p.accumulate ? 1 : n;  // without rows: its zeros are stored
+  };
+  if (wave == 0) {
+    int blocks = 0, slots = 0;
+    for (int base = 0; base < p.E; base += kWave) {
+      const int i = base + lane;
+      const int jobs = i < p.E ? parts_of(n_rows[order[i]]) : 0;
+      const int extra = i < p.E ? parts_of(n_rows[i]) - 1 : 0;
+      const int incl = wave_inclusive_scan(jobs * per_blocks) + blocks;
+      const int own = extra > 0 ? extra : 0;
+      const int sincl = wave_inclusive_scan(own) + slots;
+      if (i < p.E) {
+        blocks_to[i] = incl;
+        slots_to[i] = sincl - own;
+      }
+      blocks = __builtin_amdgcn_readlane(incl, kWave - 1);
+      slots = __builtin_amdgcn_readlane(sincl, kWave - 1);
+    }
+    // the deal: lane g holds group g's work so far, in stages (a block's
+    // store counts as eight)
+    int mine = 0;
+    if (groups < kDealt) {
+      const int n = blocks < kDealt ? blocks : kDealt;
+      uint32_t load = lane < groups ? 0u : 0x7fffffffu;
+      int place_e = 0, part = 0, blk = 0;
+      int rows = __builtin_amdgcn_readfirstlane(n_rows[order[0]]);
+      int parts = parts_of(rows);
+      for (int s = 0; s < n; ++s) {
+        while (part == parts) {  // the next expert with blocks
+          part = 0;
+          ++place_e;
+          rows = __builtin_amdgcn_readfirstlane(n_rows[order[place_e]]);
+          parts = parts_of(rows);
+        }
+        const int left = rows - part * p.chunk;
+        const uint32_t cost = (uint32_t)((left < p.chunk ? left : p.chunk) / kStageRows + 8);
+        const uint32_t least = wave_min(load);
+        const int g = __builtin_ctzll(__builtin_amdgcn_ballot_w64(load == least));
+        if (lane == g) load += cost;
+        if (g == my_group) {
+          if (lane == 0) dealt[mine] = s;
+          ++mine;
+        }
+        if (++blk == per_blocks) {
+          blk = 0;
+          ++part;
+        }
+      }
+    }
+    if (lane == 0) n_dealt = mine;
+  }
+  __syncthreads();
+  const int total = __builtin_amdgcn_readfirstlane(blocks_to[p.E - 1]);
+  const int mine = __builtin_amdgcn_readfirstlane(n_dealt);
+  const int in_turn = groups < kDealt ? kDealt : 0;  // blocks from here on go in turn
 
   struct Tile {
-    int e, part, a0, b0, cnt;  // cnt: rows of the chunk
+    int e, part, a0, b0, cnt;  // cnt: rows of the chunk (-1: no tile)
     int64_t row;               // first row
   };
-  auto tile_at = [&](int t) {
-    Tile J;
-    int e = 0;
-    for (int base = 0; base < p.E; base += kWave) {
-      const bool before = base + lane < p.E && tiles_to[base + lane] <= t;
-      e += __builtin_popcountll(__builtin_amdgcn_ballot_w64(before));
+  // The k-th job of this workgroup: false past its last. A block may have no
+  // tile for this member: cnt = -1.
+  auto job = [&](int k, Tile* J) -> bool {
+    int t;
+    if (k < mine) {
+      t = __builtin_amdgcn_readfirstlane(dealt[k]);
+    } else {
+      // every second turn backwards: the blocks fall in size
+      const int turn = k - mine;
+      t = in_turn + turn * groups + (turn & 1 ? groups - 1 - my_group : my_group);
+      if (t >= total) return false;
     }
-    const int local = t - (e > 0 ? __builtin_amdgcn_readfirstlane(tiles_to[e - 1]) : 0);
+    int i = 0;
+    for (int base = 0; base < p.E; base += kWave) {
+      const bool before = base + lane < p.E && blocks_to[base + lane] <= t;
+      i += __builtin_popcountll(__builtin_amdgcn_ballot_w64(before));
+    }
+    const int local = t - (i > 0 ? __builtin_amdgcn_readfirstlane(blocks_to[i - 1]) : 0);
+    const int e = __builtin_amdgcn_readfirstlane(order[i]);
     const int rows = __builtin_amdgcn_readfirstlane(n_rows[e]);
-    J.e = e;
-    J.part = local / per;
-    J.a0 = local % per / tb * kTile;
-    J.b0 = local % per % tb * kTile;
-    const int left = rows - J.part * p.chunk;
-    J.cnt = left < p.chunk ? left : p.chunk;
-    J.row = (int64_t)__builtin_amdgcn_readfirstlane(first_row[e]) + (int64_t)J.part * p.chunk;
-    return J;
+    const int tile = local % per_blocks * p.group + member;
+    J->e = e;
+    J->part = local / per_blocks;
+    J->a0 = tile / tb * kTile;
+    J->b0 = tile % tb * kTile;
+    const int left = rows - J->part * p.chunk;
+    J->cnt = tile < per ? (left < p.chunk ? left : p.chunk) : -1;
+    J->row = (int64_t)__builtin_amdgcn_readfirstlane(first_row[e]) + (int64_t)J->part * p.chunk;
+    return true;
   };
 
   // Loads of a stage: wavefronts 0-1 fetch dy, 2-3 x; each 128 columns, as
@@ -170,7 +256,7 @@ __global__ __launch_bounds__(256, 1) void ragged_wgrad_kernel(WgradRingParams p)
   auto fetch_tile = [&](const Tile& J) {
     FetchTile F;
     const int col = (op == 0 ? J.a0 : J.b0) + 128 * (wave & 1);
-    F.stages = (J.cnt + kStageRows - 1) / kStageRows;
+    F.stages = J.cnt > 0 ? (J.cnt + kStageRows - 1) / kStageRows : 0;
     F.rs = __builtin_amdgcn_make_buffer_rsrc(
         (void*)(src + J.row * ld + (int64_t)col * 2), 0,
         J.cnt > 0 && col < width
@@ -179,18 +265,20 @@ __global__ __launch_bounds__(256, 1) void ragged_wgrad_kernel(WgradRingParams p)
         kRsrcWord3);
     return F;
   };
-  // The fetch cursor: tile ft of the workgroup's list, its stage fs; past the
-  // last tile, stages that load nothing, so that every stage issues the same
-  // loads.
-  int ft = t_first, fs = 0;
-  FetchTile F = fetch_tile(tile_at(ft));
+  // The fetch cursor: job fj, its stage fs; past the last job, stages that
+  // load nothing, so that every stage issues the same loads.
+  int fj = 0, fs = 0;
+  Tile FT;
+  bool more = job(0, &FT);
+  if (!more) return;
+  FetchTile F = fetch_tile(FT);
   auto next_stage = [&]() -> uint32_t {
-    while (ft < t_end && fs >= F.stages) {
-      ft += Q;
+    while (more && fs >= F.stages) {
       fs = 0;
-      if (ft < t_end) F = fetch_tile(tile_at(ft));
+      more = job(++fj, &FT);
+      if (more) F = fetch_tile(FT);
     }
-    const uint32_t off = ft < t_end ? (uint32_t)(fs * kStageRows) * ld : kOutOfRange;
+    const uint32_t off = more ? (uint32_t)(fs * kStageRows) * ld : kOutOfRange;
     ++fs;
     return off;
   };
@@ -300,8 +388,9 @@ __global__ __launch_bounds__(256, 1) void ragged_wgrad_kernel(WgradRingParams p)
   // g - 1; the barrier waits for g + 1; the second step's MFMAs run while
   // g + 1's first fragments are read and the rest of g + 3 is fetched.
   int g = 0;
-  for (int ct = t_first; ct < t_end; ct += Q) {
-    const Tile CT = tile_at(ct);
+  Tile CT;
+  for (int cj = 0; job(cj, &CT); ++cj) {
+    if (CT.cnt < 0) continue;
     const int stages = (CT.cnt + kStageRows - 1) / kStageRows;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -334,9 +423,14 @@ __global__ __launch_bounds__(256, 1) void ragged_wgrad_kernel(WgradRingParams p)
 
 }  // namespace
 
-hipError_t launch_wgrad_ring(bool is_bf16, const WgradRingParams& p, int num_cus,
+hipError_t launch_wgrad_ring(bool is_bf16, const WgradRingParams& params, int num_cus,
                              hipStream_t st) {
   const int grid = num_cus < 8 ? 8 : num_cus / 8 * 8;
+  WgradRingParams p = params;
+  // the largest group that wastes at most an eighth of a chunk's blocks
+  const int tiles = ((p.N + kTile - 1) / kTile) * ((p.K + kTile - 1) / kTile);
+  for (p.group = 32; p.group > 1; p.group /= 2)
+    if ((tiles + p.group - 1) / p.group * p.group * 8 <= tiles * 9 && grid / 8 % p.group == 0) break;
   if (is_bf16)
     hipLaunchKernelGGL((ragged_wgrad_kernel<bf16>), dim3(grid), dim3(256), 0, st, p);
   else

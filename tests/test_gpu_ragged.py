@@ -590,3 +590,26 @@ def test_gradients_of_a_ragged_ffn_against_differences(B):
             # of a sum of a few SwiGLU terms with weights of order 0.3 well
             # below 50; rounding: fp32 errors of y (24 terms) over the step
             assert abs(num - grads[a].view(-1)[pos].item()) <= 50 / 6 * step ** 2 + 1e-3, (a, pos)
+
+
+@pytest.mark.parametrize("K", [544, 608, 1056, 2080, 4128])
+def test_mxfp4_product_reads_no_scales_past_its_arrays(B, K):
+    """Scale rows that do not end at 16 bytes, arrays of exactly their size:
+    the last row's scales count, what lies behind the array (NaN scales, in
+    the same allocation) does not."""
+    rows, N, S = 1500, 512, B.mxfp4_scale_stride(K)
+    off = R.offsets_of([rows])
+    xc, xs, xq, xsc = mx_operand(rows, K, 1, 3)
+    wc, wsb, wq, wsc = mx_operand(N, K, 2, 3)
+
+    def behind(t, fill):
+        buf = torch.full((t.shape[0] + 64, t.shape[1]), fill, dtype=torch.uint8, device="cuda")
+        buf[: t.shape[0]] = t
+        return buf[: t.shape[0]]
+
+    xsc, wsc, xq, wq = behind(xsc, 255), behind(wsc, 255), behind(xq, 0x77), behind(wq, 0x77)
+    y = torch.empty(rows, N, device="cuda")
+    B.moe_mxfp4_grouped_gemm(B.grouped(rows, 1, N, K, "f32"), dev_off(off), xq, xsc, wq, wsc, y)
+    ref, s = R.product(off, torch.from_numpy(R.values_of(xc, xs)),
+                       torch.from_numpy(R.values_of(wc, wsb)).view(1, N, K), rows)
+    check(y, ref, R.sum_bound(ref, s, K, torch.float32), "y")

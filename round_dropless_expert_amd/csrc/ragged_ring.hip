@@ -130,6 +130,12 @@ struct Scales {
   int a[WI], b[WJ];
 };
 
+// Operation x of a step that mixes kReads fragment reads evenly with n loads:
+// the loads among the first x operations.
+__host__ __device__ constexpr int loads_before(int x, int reads, int n) {
+  return x * n / (reads + n);
+}
+
 // One MFMA step with kOps other operations spread over it in a fixed order
 // (op(x) after MFMA i for x in [i kOps / M, (i + 1) kOps / M)), each group
 // fenced so that the compiler keeps the order.
@@ -533,20 +539,22 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(RingParams p) {
       const char* ns = sub + 1 < SPB ? CUR + (sub + 1) * kStageBytes : NXT;             \
       const int g = (KS_) * SPB + sub;                                                  \
       mma_step<Op, 0, WI, WJ, kReads + kLoadsPerStep>(acc, f0, sc, [&](int x) {         \
-        if (x < kReads) {                                                               \
-          read_one(f1, cs, 1, x);                                                       \
+        const int lb = loads_before(x, kReads, kLoadsPerStep);                          \
+        if (loads_before(x + 1, kReads, kLoadsPerStep) == lb) {                         \
+          read_one(f1, cs, 1, x - lb);                                                  \
         } else {                                                                        \
-          const int li = 2 * sub * kLoadsPerStep + x - kReads;                          \
+          const int li = 2 * sub * kLoadsPerStep + lb;                                  \
           if (li < kLoads) fetch_one(FSLOT, SO, F, li);                                 \
         }                                                                               \
       });                                                                               \
       if (sub + 1 == SPB) wait_vmem_barrier<kWait>();                                   \
       if constexpr (kScaled) read_scales(raw, ns);                                      \
       mma_step<Op, 1, WI, WJ, kReads + kLoadsPerStep>(acc, f1, sc, [&](int x) {         \
-        if (x < kReads) {                                                               \
-          read_one(f0, ns, 0, x);                                                       \
+        const int lb = loads_before(x, kReads, kLoadsPerStep);                          \
+        if (loads_before(x + 1, kReads, kLoadsPerStep) == lb) {                         \
+          read_one(f0, ns, 0, x - lb);                                                  \
         } else {                                                                        \
-          const int li = (2 * sub + 1) * kLoadsPerStep + x - kReads;                    \
+          const int li = (2 * sub + 1) * kLoadsPerStep + lb;                            \
           if (li < kLoads) fetch_one(FSLOT, SO, F, li);                                 \
         }                                                                               \
       });                                                                               \
@@ -853,10 +861,11 @@ __global__ __launch_bounds__(256, 1) void wide_ring_kernel(RingParams p) {
     {                                                                                   \
       const Off SO = offsets_of(K0);                                                    \
       mma_step<Op, 0, WI, WJ, kReads + kL0>(acc, f0, sc, [&](int x) {                   \
-        if (x < kReads)                                                                 \
-          read_one(f1, C, 1, x);                                                        \
+        const int lb = loads_before(x, kReads, kL0);                                    \
+        if (loads_before(x + 1, kReads, kL0) == lb)                                     \
+          read_one(f1, C, 1, x - lb);                                                   \
         else                                                                            \
-          fetch(1 - (C), SO, F0, kFirst + x - kReads);                                  \
+          fetch(1 - (C), SO, F0, kFirst + lb);                                          \
       });                                                                               \
     }                                                                                   \
     mma_step<Op, 1, WI, WJ, kReads>(acc, f1, sc, [&](int x) { read_one(f0, C, 2, x); }); \
@@ -867,10 +876,11 @@ __global__ __launch_bounds__(256, 1) void wide_ring_kernel(RingParams p) {
     {                                                                                   \
       const Off SO = offsets_of(K3);                                                    \
       mma_step<Op, 1, WI, WJ, kReads + kFirst>(acc, f1, sc, [&](int x) {                \
-        if (x < kReads)                                                                 \
-          read_one(f0, 1 - (C), 0, x);                                                  \
+        const int lb = loads_before(x, kReads, kFirst);                                 \
+        if (loads_before(x + 1, kReads, kFirst) == lb)                                  \
+          read_one(f0, 1 - (C), 0, x - lb);                                             \
         else                                                                            \
-          fetch(C, SO, F3, x - kReads);                                                 \
+          fetch(C, SO, F3, lb);                                                         \
       });                                                                               \
     }                                                                                   \
     if constexpr (kScaled)                                                              \

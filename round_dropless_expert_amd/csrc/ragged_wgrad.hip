@@ -313,7 +313,7 @@ __global__ __launch_bounds__(256, 1) void ragged_wgrad_kernel(WgradRingParams p)
     else
       fb[x - 4] = frag(1, slot, x - 4, ks);
   };
-  constexpr int kOps = 12;  // 8 fragment reads, 4 loads
+  constexpr int kOps = 12;  // 8 fragment reads, a load after every second
   auto mma_step = [&](const u32x4 (&fb)[4], const u32x4 (&fa)[4], auto op_) {
 #pragma unroll
     for (int n = 0; n < 16; ++n) {
@@ -402,17 +402,17 @@ __global__ __launch_bounds__(256, 1) void ragged_wgrad_kernel(WgradRingParams p)
       const int u = g & 3;
       const uint32_t off = next_stage();
       mma_step(fb0, fa0, [&](int x) {
-        if (x < 8)
-          read_one(fb1, fa1, u, 1, x);
+        if (x % 3 < 2)
+          read_one(fb1, fa1, u, 1, x - x / 3);
         else
-          fetch(off, (u + 3) & 3, x - 8);
+          fetch(off, (u + 3) & 3, x / 3);
       });
       wait_vmem_barrier<kLoads + kLoads / 2>();
       mma_step(fb1, fa1, [&](int x) {
-        if (x < 8)
-          read_one(fb0, fa0, (u + 1) & 3, 0, x);
+        if (x % 3 < 2)
+          read_one(fb0, fa0, (u + 1) & 3, 0, x - x / 3);
         else
-          fetch(off, (u + 3) & 3, x - 4);
+          fetch(off, (u + 3) & 3, 4 + x / 3);
       });
     }
     epilogue(CT);

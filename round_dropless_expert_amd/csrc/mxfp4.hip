@@ -13,11 +13,101 @@
 namespace moe {
 namespace {
 
-// Code (0 .. 7) of a magnitude in [0, 8): the number of borders it has
-// passed. A border between an odd and an even code belongs to the even one.
-__device__ __forceinline__ uint32_t code_of(float a) {
-  return (uint32_t)(a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) +
-         (a >= 3.5f) + (a > 5.0f);
+constexpr int kUnroll = 4;  // 16-byte vectors a lane has in flight
+
+// gfx950 converts two values at a time to and from the 4-bit format with a
+// scale (an fp32 power of two, of which it uses the exponent): to nearest,
+// ties to even, ending at 6, fp32 subnormals included.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ float scale_of(int byte) {
+  return __builtin_bit_cast(float, (uint32_t)byte << 23);
+}
+
+template <typename T>
+struct Codec;
+template <>
+struct Codec<bf16> {
+  typedef bf16x2 pair_t;
+  // largest magnitude of 16 bytes, as bits in the order of the values
+  __device__ static __forceinline__ uint32_t top(u32x4 v) { return top16(v); }
+  // and its fp32 bits
+  __device__ static __forceinline__ uint32_t bits(uint32_t t) { return t << 16; }
+  __device__ static __forceinline__ uint32_t top16(u32x4 v) {
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 m = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[i] & 0x7fff7fffu));
+    return m[0] > m[1] ? m[0] : m[1];
+  }
+  template <int kByte>
+  __device__ static __forceinline__ uint32_t encode(uint32_t old, u32x4 v, float s) {
+    const uint32_t two = v[kByte];
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, __builtin_bit_cast(pair_t, two), s, kByte);
+  }
+  template <int kByte>
+  __device__ static __forceinline__ pair_t decode(uint32_t q, float s) {
+    return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, kByte);
+  }
+};
+template <>
+struct Codec<f16> {
+  typedef f16x2 pair_t;
+  __device__ static __forceinline__ uint32_t top(u32x4 v) { return Codec<bf16>::top16(v); }
+  __device__ static __forceinline__ uint32_t bits(uint32_t t) {
+    return __builtin_bit_cast(uint32_t, (float)__builtin_bit_cast(f16, (uint16_t)t));
+  }
+  template <int kByte>
+  __device__ static __forceinline__ uint32_t encode(uint32_t old, u32x4 v, float s) {
+    const uint32_t two = v[kByte];
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(old, __builtin_bit_cast(pair_t, two), s, kByte);
+  }
+  template <int kByte>
+  __device__ static __forceinline__ pair_t decode(uint32_t q, float s) {
+    return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, s, kByte);
+  }
+};
+template <>
+struct Codec<float> {
+  typedef f32x2 pair_t;
+  __device__ static __forceinline__ uint32_t top(u32x4 v) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t b = v[i] & 0x7fffffffu;
+      m = m > b ? m : b;
+    }
+    return m;
+  }
+  __device__ static __forceinline__ uint32_t bits(uint32_t t) { return t; }
+  template <int kByte>
+  __device__ static __forceinline__ uint32_t encode(uint32_t old, u32x4 v, float s) {
+    const uint32_t a = v[2 * kByte], b = v[2 * kByte + 1];
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, __builtin_bit_cast(float, a),
+                                                    __builtin_bit_cast(float, b), s, kByte);
+  }
+  template <int kByte>
+  __device__ static __forceinline__ pair_t decode(uint32_t q, float s) {
+    return __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, kByte);
+  }
+};
+
+// Largest of the values of a block's lanes, 4 or 8 neighbours.
+template <int kLanes>
+__device__ __forceinline__ uint32_t block_max(uint32_t v) {
+#define MOE_MAX_STEP(ctrl)                                                                \
+  {                                                                                       \
+    const uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, ctrl, 0xf, 0xf, true);  \
+    v = v > o ? v : o;                                                                    \
+  }
+  MOE_MAX_STEP(0xb1)  // lanes 1, 0, 3, 2 of each four
+  MOE_MAX_STEP(0x4e)  // lanes 2, 3, 0, 1
+  if constexpr (kLanes == 8) MOE_MAX_STEP(0x141)  // each eight mirrored
+#undef MOE_MAX_STEP
+  return v;
 }
 
 struct QuantParams {
@@ -30,22 +120,22 @@ struct QuantParams {
   uint8_t* codes;
   uint8_t* scales;
   int64_t stride;  // bytes of a scale row
+  int log_lanes;   // lanes per row
 };
 
-// A lane takes V = 16 bytes of a row (kVec: the row's addresses are
-// 16-byte aligned), 32 / V lanes a block: its maximum is exchanged between
-// them, and each stores V / 2 bytes of codes.
+// A lane takes V = 16 bytes of a row at a time (kVec: the row's addresses
+// are 16-byte aligned), 32 / V neighbours a block: their maximum is exchanged
+// by DPP, and each stores V / 2 bytes of codes. kUnroll vectors of a row are
+// in flight per lane.
 template <typename T, bool kVec>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(QuantParams p) {
   constexpr int V = 16 / sizeof(T);
   constexpr int kLanes = kMxBlock / V;
-  const uint32_t per = (uint32_t)(p.K / V);
+  const int per = (int)(p.K / V);
   const int64_t rows = live_rows(p.rows, p.n_rows);
-  const int64_t total = rows * per;  // a multiple of kLanes
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / per;
-    const int c = (int)(i - row * per) * V;
+  const int lanes = 1 << p.log_lanes, c0 = threadIdx.x & (lanes - 1);
+  const int64_t row0 = (int64_t)blockIdx.x * (256 >> p.log_lanes) + (threadIdx.x >> p.log_lanes);
+  for (int64_t row = row0; row < rows; row += (int64_t)gridDim.x * (256 >> p.log_lanes)) {
     int64_t src = row;
     bool real = true;
     if (p.index) {
@@ -53,58 +143,48 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(QuantParams p) {
       src = a < 0 ? -1 : a / p.index_div;
       real = src >= 0 && src < p.src_rows;
     }
-    union {
-      T e[V];
-      u32x4 v;
-    } x;
-    x.v = u32x4{0, 0, 0, 0};
-    if (real) {
-      const T* at = static_cast<const T*>(p.x) + src * p.ld_x + c;
-      if constexpr (kVec) {
-        x.v = *reinterpret_cast<const u32x4*>(at);
-      } else {
+    const T* in = static_cast<const T*>(p.x) + (real ? src : 0) * p.ld_x;
+    uint8_t* out = p.codes + row * (p.K / 2);
+    uint8_t* sc = p.scales + row * p.stride;
+    for (int c = c0; c < per; c += lanes * kUnroll) {
+      u32x4 x[kUnroll];
 #pragma unroll
-        for (int v = 0; v < V; ++v) x.e[v] = at[v];
+      for (int u = 0; u < kUnroll; ++u) {
+        x[u] = u32x4{0, 0, 0, 0};
+        const int v = c + u * lanes;
+        if (v < per && real) {
+          if constexpr (kVec) {
+            x[u] = *reinterpret_cast<const u32x4*>(in + (int64_t)v * V);
+          } else {
+            __builtin_memcpy(&x[u], in + (int64_t)v * V, 16);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int v = c + u * lanes;
+        if (v >= per) break;  // a block's lanes go together
+        const uint32_t top = Codec<T>::bits(block_max<kLanes>(Codec<T>::top(x[u])));
+        // The scale's byte is the exponent field - 2, at least 0; infinities
+        // and NaN have the largest exponent field.
+        const int field = (int)(top >> 23);
+        const bool bad = field == 255;
+        const int byte = bad ? 255 : (field > 2 ? field - 2 : 0);
+        const float s = scale_of(byte);
+        uint32_t q = Codec<T>::template encode<0>(0u, x[u], s);
+        q = Codec<T>::template encode<1>(q, x[u], s);
+        if constexpr (V == 8) {
+          q = Codec<T>::template encode<2>(q, x[u], s);
+          q = Codec<T>::template encode<3>(q, x[u], s);
+          *reinterpret_cast<uint32_t*>(out + v * 4) = bad ? 0 : q;
+        } else {
+          *reinterpret_cast<uint16_t*>(out + v * 2) = (uint16_t)(bad ? 0 : q);
+        }
+        if (v % kLanes == 0) sc[v / kLanes] = (uint8_t)byte;
       }
     }
-    // largest magnitude, as the bits of an fp32 (their order is that of the
-    // values, with infinity and then NaN above every number)
-    uint32_t top = 0;
-    float f[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      f[v] = to_f32(x.e[v]);
-      const uint32_t b = __builtin_bit_cast(uint32_t, f[v]) & 0x7fffffffu;
-      top = top > b ? top : b;
-    }
-#pragma unroll
-    for (int m = 1; m < kLanes; m <<= 1) {
-      const uint32_t o = (uint32_t)__shfl_xor((int)top, m, kWave);
-      top = top > o ? top : o;
-    }
-    const bool bad = top >= 0x7f800000u;
-    // e + 127 = exponent field - 2; below 2^-124 the scale stays at 2^-127
-    const int byte = bad ? 255 : ((int)(top >> 23) > 2 ? (int)(top >> 23) - 2 : 0);
-    uint32_t packed = 0;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const uint32_t sign = __builtin_bit_cast(uint32_t, f[v]) >> 31;
-      const uint32_t q =
-          bad ? 0 : (sign << 3) | code_of(ldexpf(__builtin_fabsf(f[v]), 127 - byte));
-      packed |= q << (4 * v);
-    }
-    uint8_t* out = p.codes + row * (p.K / 2) + c / 2;
-    if constexpr (V == 8)
-      *reinterpret_cast<uint32_t*>(out) = packed;
-    else
-      *reinterpret_cast<uint16_t*>(out) = (uint16_t)packed;
-    if (c % kMxBlock == 0) {
-      uint8_t* s = p.scales + row * p.stride + c / kMxBlock;
-      *s = (uint8_t)byte;
-      // the padding of the scale row: blocks that hold nothing
-      if (c + kMxBlock == p.K)
-        for (int64_t k = p.K / kMxBlock; k < p.stride; ++k) *++s = 0;
-    }
+    // the padding of the scale row: blocks that hold nothing
+    if (c0 < p.stride - p.K / kMxBlock) sc[p.K / kMxBlock + c0] = 0;
   }
 }
 
@@ -114,56 +194,83 @@ struct DequantParams {
   void* y;
   int64_t ld_y, rows, K, stride;
   const int32_t* n_rows;
+  int log_lanes;
 };
 
 template <typename T, bool kVec>
 __global__ __launch_bounds__(256) void mx_dequantize_kernel(DequantParams p) {
   constexpr int V = 16 / sizeof(T);
-  const uint32_t per = (uint32_t)(p.K / V);
-  const int64_t total = live_rows(p.rows, p.n_rows) * per;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / per;
-    const int c = (int)(i - row * per) * V;
-    const uint8_t* at = p.codes + row * (p.K / 2) + c / 2;
-    const uint32_t q = V == 8 ? *reinterpret_cast<const uint32_t*>(at)
-                              : *reinterpret_cast<const uint16_t*>(at);
-    const int s = p.scales[row * p.stride + c / kMxBlock];
-    union {
-      T e[V];
-      u32x4 v;
-    } y;
+  const int per = (int)(p.K / V);
+  const int64_t rows = live_rows(p.rows, p.n_rows);
+  const int lanes = 1 << p.log_lanes, c0 = threadIdx.x & (lanes - 1);
+  const int64_t row0 = (int64_t)blockIdx.x * (256 >> p.log_lanes) + (threadIdx.x >> p.log_lanes);
+  for (int64_t row = row0; row < rows; row += (int64_t)gridDim.x * (256 >> p.log_lanes)) {
+    const uint8_t* in = p.codes + row * (p.K / 2);
+    const uint8_t* sc = p.scales + row * p.stride;
+    T* out = static_cast<T*>(p.y) + row * p.ld_y;
+    for (int c = c0; c < per; c += lanes * kUnroll) {
+      uint32_t q[kUnroll];
+      int s[kUnroll];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const uint32_t m = (q >> (4 * v)) & 7;
-      // magnitude: 0 and 0.5, then (1 + mantissa / 2) 2^(exponent - 1)
-      const float a = m < 2 ? 0.5f * (float)m
-                            : ldexpf(1.0f + 0.5f * (float)(m & 1), (int)(m >> 1) - 1);
-      float r = ldexpf((q >> (4 * v)) & 8 ? -a : a, s - 127);
-      if (s == 255) r = __builtin_nanf("");
-      y.e[v] = from_f32<T>(r);
-    }
-    T* out = static_cast<T*>(p.y) + row * p.ld_y + c;
-    if constexpr (kVec) {
-      *reinterpret_cast<u32x4*>(out) = y.v;
-    } else {
+      for (int u = 0; u < kUnroll; ++u) {
+        const int v = c + u * lanes;
+        q[u] = s[u] = 0;
+        if (v < per) {
+          q[u] = V == 8 ? *reinterpret_cast<const uint32_t*>(in + v * 4)
+                        : *reinterpret_cast<const uint16_t*>(in + v * 2);
+          s[u] = sc[v * V / kMxBlock];
+        }
+      }
 #pragma unroll
-      for (int v = 0; v < V; ++v) out[v] = y.e[v];
+      for (int u = 0; u < kUnroll; ++u) {
+        const int v = c + u * lanes;
+        if (v >= per) break;
+        const float f = scale_of(s[u]);
+        union {
+          typename Codec<T>::pair_t e[V / 2];
+          T t[V];
+          u32x4 v;
+        } y;
+        y.e[0] = Codec<T>::template decode<0>(q[u], f);
+        y.e[1] = Codec<T>::template decode<1>(q[u], f);
+        if constexpr (V == 8) {
+          y.e[2] = Codec<T>::template decode<2>(q[u], f);
+          y.e[3] = Codec<T>::template decode<3>(q[u], f);
+        }
+        if (s[u] == 255) {
+#pragma unroll
+          for (int k = 0; k < V; ++k) y.t[k] = from_f32<T>(__builtin_nanf(""));
+        }
+        if constexpr (kVec)
+          *reinterpret_cast<u32x4*>(out + (int64_t)v * V) = y.v;
+        else
+          __builtin_memcpy(out + (int64_t)v * V, &y.v, 16);
+      }
     }
   }
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-unsigned grid_of(int64_t lanes, int num_cus) {
-  const int64_t blocks = (lanes + 255) / 256, most = (int64_t)num_cus * 16;
+// Lanes per row: a power of two that leaves a lane about kUnroll vectors of
+// the row, 8 (a block's lanes) to 256.
+int log_lanes_of(int64_t per) {
+  int l = 3;
+  while (l < 8 && ((int64_t)kUnroll << l) < per) ++l;
+  return l;
+}
+
+unsigned grid_of(int64_t rows, int log_lanes, int num_cus) {
+  const int64_t at_once = 256 >> log_lanes, blocks = (rows + at_once - 1) / at_once;
+  const int64_t most = (int64_t)num_cus * 64;
   return (unsigned)(blocks < most ? blocks : most);
 }
 
 template <typename T>
-hipError_t quantize(const QuantParams& p, int num_cus, hipStream_t st) {
+hipError_t quantize(QuantParams p, int num_cus, hipStream_t st) {
   constexpr int V = 16 / sizeof(T);
-  const unsigned grid = grid_of(p.rows * (p.K / V), num_cus);
+  p.log_lanes = log_lanes_of(p.K / V);
+  const unsigned grid = grid_of(p.rows, p.log_lanes, num_cus);
   if (p.ld_x % V == 0 && aligned16(p.x))
     hipLaunchKernelGGL((mx_quantize_kernel<T, true>), dim3(grid), dim3(256), 0, st, p);
   else
@@ -172,9 +279,10 @@ hipError_t quantize(const QuantParams& p, int num_cus, hipStream_t st) {
 }
 
 template <typename T>
-hipError_t dequantize(const DequantParams& p, int num_cus, hipStream_t st) {
+hipError_t dequantize(DequantParams p, int num_cus, hipStream_t st) {
   constexpr int V = 16 / sizeof(T);
-  const unsigned grid = grid_of(p.rows * (p.K / V), num_cus);
+  p.log_lanes = log_lanes_of(p.K / V);
+  const unsigned grid = grid_of(p.rows, p.log_lanes, num_cus);
   if (p.ld_y % V == 0 && aligned16(p.y))
     hipLaunchKernelGGL((mx_dequantize_kernel<T, true>), dim3(grid), dim3(256), 0, st, p);
   else
@@ -260,7 +368,7 @@ hipError_t launch_mx_quantize(ElemType t, int64_t rows, int64_t K, const void* x
                               int num_cus, hipStream_t st) {
   if (rows == 0) return hipSuccess;
   const QuantParams p{x,    ld_x, src_rows, index,  index_div,         n_rows,
-                      rows, K,    codes,    scales, mx_scale_stride(K)};
+                      rows, K,    codes,    scales, mx_scale_stride(K), 0};
   switch (t) {
     case ElemType::kF32: return quantize<float>(p, num_cus, st);
     case ElemType::kBF16: return quantize<bf16>(p, num_cus, st);
@@ -272,7 +380,7 @@ hipError_t launch_mx_dequantize(ElemType t, int64_t rows, int64_t K, const uint8
                                 const uint8_t* scales, void* y, int64_t ld_y,
                                 const int32_t* n_rows, int num_cus, hipStream_t st) {
   if (rows == 0) return hipSuccess;
-  const DequantParams p{codes, scales, y, ld_y, rows, K, mx_scale_stride(K), n_rows};
+  const DequantParams p{codes, scales, y, ld_y, rows, K, mx_scale_stride(K), n_rows, 0};
   switch (t) {
     case ElemType::kF32: return dequantize<float>(p, num_cus, st);
     case ElemType::kBF16: return dequantize<bf16>(p, num_cus, st);

@@ -36,14 +36,15 @@ __device__ __forceinline__ Gate gate(float g) {
 template <typename T, int V>
 struct Vec {
   T e[V];
-} ;
+};
 
 template <typename T, int V>
 __device__ __forceinline__ Vec<T, V> load(const T* p) {
   if constexpr (V == 1) {
     return Vec<T, 1>{{*p}};
   } else {
-    return __builtin_bit_cast(Vec<T, V>, *reinterpret_cast<const u32x4*>(p));
+    return __builtin_bit_cast(
+        Vec<T, V>, __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p)));
   }
 }
 template <typename T, int V>
@@ -51,7 +52,7 @@ __device__ __forceinline__ void store(T* p, const Vec<T, V>& v) {
   if constexpr (V == 1)
     *p = v.e[0];
   else
-    *reinterpret_cast<u32x4*>(p) = __builtin_bit_cast(u32x4, v);
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(p));
 }
 
 struct SwigluParams {
@@ -61,41 +62,60 @@ struct SwigluParams {
   int64_t ld_gu, ld_dh, ld_out;
   const int32_t* n_rows;
   int64_t rows;
-  uint32_t per;  // vectors of V features per row
   int64_t f;
+  int log_lanes;  // lanes per row
 };
 
+constexpr int kUnroll = 2;  // vectors a lane has in flight per operand
+
+// 2^log_lanes lanes a row, each V features at a time. All of it is read and
+// written once: non-temporal.
 template <typename T, int V, bool kBackward>
 __global__ __launch_bounds__(256) void swiglu_kernel(SwigluParams p) {
-  const int64_t total = live_rows(p.rows, p.n_rows) * p.per;
-  const T* gu = static_cast<const T*>(p.gu);
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / p.per;
-    const int64_t c = (i - row * p.per) * V;
-    const Vec<T, V> g = load<T, V>(gu + row * p.ld_gu + c);
-    const Vec<T, V> u = load<T, V>(gu + row * p.ld_gu + p.f + c);
-    if constexpr (!kBackward) {
-      Vec<T, V> h;
+  const int64_t rows = live_rows(p.rows, p.n_rows);
+  const int per = (int)(p.f / V);
+  const int lanes = 1 << p.log_lanes, c0 = threadIdx.x & (lanes - 1);
+  const int64_t row0 = (int64_t)blockIdx.x * (256 >> p.log_lanes) + (threadIdx.x >> p.log_lanes);
+  for (int64_t row = row0; row < rows; row += (int64_t)gridDim.x * (256 >> p.log_lanes)) {
+    const T* gu = static_cast<const T*>(p.gu) + row * p.ld_gu;
+    const T* dh = static_cast<const T*>(p.dh) + row * p.ld_dh;
+    T* out = static_cast<T*>(p.out) + row * p.ld_out;
+    for (int c = c0; c < per; c += lanes * kUnroll) {
+      Vec<T, V> g[kUnroll], u[kUnroll], d[kUnroll];
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float gf = to_f32(g.e[v]);
-        h.e[v] = from_f32<T>(gf * gate<T>(gf).s * to_f32(u.e[v]));
+      for (int k = 0; k < kUnroll; ++k) {
+        const int64_t at = (int64_t)(c + k * lanes) * V;
+        if (c + k * lanes < per) {
+          g[k] = load<T, V>(gu + at);
+          u[k] = load<T, V>(gu + p.f + at);
+          if constexpr (kBackward) d[k] = load<T, V>(dh + at);
+        }
       }
-      store<T, V>(static_cast<T*>(p.out) + row * p.ld_out + c, h);
-    } else {
-      const Vec<T, V> d = load<T, V>(static_cast<const T*>(p.dh) + row * p.ld_dh + c);
-      Vec<T, V> dg, du;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float gf = to_f32(g.e[v]), df = to_f32(d.e[v]);
-        const Gate k = gate<T>(gf);
-        dg.e[v] = from_f32<T>(df * (k.s * (1.0f + gf * k.rest)) * to_f32(u.e[v]));
-        du.e[v] = from_f32<T>(df * (gf * k.s));
+      for (int k = 0; k < kUnroll; ++k) {
+        if (c + k * lanes >= per) break;
+        const int64_t at = (int64_t)(c + k * lanes) * V;
+        if constexpr (!kBackward) {
+          Vec<T, V> h;
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const float gf = to_f32(g[k].e[v]);
+            h.e[v] = from_f32<T>(gf * gate<T>(gf).s * to_f32(u[k].e[v]));
+          }
+          store<T, V>(out + at, h);
+        } else {
+          Vec<T, V> dg, du;
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const float gf = to_f32(g[k].e[v]), df = to_f32(d[k].e[v]);
+            const Gate q = gate<T>(gf);
+            dg.e[v] = from_f32<T>(df * (q.s * (1.0f + gf * q.rest)) * to_f32(u[k].e[v]));
+            du.e[v] = from_f32<T>(df * (gf * q.s));
+          }
+          store<T, V>(out + at, dg);
+          store<T, V>(out + p.f + at, du);
+        }
       }
-      T* o = static_cast<T*>(p.out) + row * p.ld_out + c;
-      store<T, V>(o, dg);
-      store<T, V>(o + p.f, du);
     }
   }
 }
@@ -109,9 +129,12 @@ hipError_t run(SwigluParams p, int num_cus, hipStream_t st) {
   const bool vec = p.f % kV == 0 && p.ld_gu % kV == 0 && p.ld_out % kV == 0 &&
                    (!kBackward || p.ld_dh % kV == 0) && aligned16(p.gu) && aligned16(p.out) &&
                    (!kBackward || aligned16(p.dh));
-  p.per = (uint32_t)(vec ? p.f / kV : p.f);
-  const int64_t blocks = (p.rows * (int64_t)p.per + 255) / 256;
-  const int64_t most = (int64_t)num_cus * 16;
+  const int64_t per = vec ? p.f / kV : p.f;
+  // lanes per row: a power of two that leaves a lane about kUnroll vectors
+  p.log_lanes = 3;
+  while (p.log_lanes < 8 && ((int64_t)kUnroll << p.log_lanes) < per) ++p.log_lanes;
+  const int64_t at_once = 256 >> p.log_lanes, blocks = (p.rows + at_once - 1) / at_once;
+  const int64_t most = (int64_t)num_cus * 64;
   const unsigned grid = (unsigned)(blocks < most ? blocks : most);
   if (vec)
     hipLaunchKernelGGL((swiglu_kernel<T, kV, kBackward>), dim3(grid), dim3(256), 0, st, p);
@@ -135,7 +158,7 @@ hipError_t dispatch(ElemType t, const SwigluParams& p, int num_cus, hipStream_t 
 hipError_t launch_swiglu(ElemType t, int64_t rows, int64_t f, const void* gu, int64_t ld_gu,
                          void* h, int64_t ld_h, const int32_t* n_rows, int num_cus,
                          hipStream_t st) {
-  return dispatch<false>(t, SwigluParams{gu, nullptr, h, ld_gu, 0, ld_h, n_rows, rows, 0, f},
+  return dispatch<false>(t, SwigluParams{gu, nullptr, h, ld_gu, 0, ld_h, n_rows, rows, f, 0},
                          num_cus, st);
 }
 
@@ -143,7 +166,7 @@ hipError_t launch_swiglu_backward(ElemType t, int64_t rows, int64_t f, const voi
                                   int64_t ld_gu, const void* dh, int64_t ld_dh, void* dgu,
                                   int64_t ld_dgu, const int32_t* n_rows, int num_cus,
                                   hipStream_t st) {
-  return dispatch<true>(t, SwigluParams{gu, dh, dgu, ld_gu, ld_dh, ld_dgu, n_rows, rows, 0, f},
+  return dispatch<true>(t, SwigluParams{gu, dh, dgu, ld_gu, ld_dh, ld_dgu, n_rows, rows, f, 0},
                         num_cus, st);
 }
 

@@ -500,35 +500,51 @@ def grouped_dw_workspace_size(g: MoeGrouped) -> int:
 
 def mxfp4_scale_stride(K: int) -> int:
     """Bytes of a row of MXFP4 scales."""
-    n = load().moe_mxfp4_scale_stride(int(K))
-    if n < 0:
+    if K < 32 or K % 32:
         raise ValueError(f"K = {K} must be a positive multiple of 32")
-    return n
+    return (K // 32 + 3) // 4 * 4
 
 
-def _on_device(t, name):
+# The ragged calls are also made for single tokens, where the host's time per
+# call counts: an argument that is what the call needs is passed by a few
+# attribute reads, anything else goes through the functions that say what is
+# wrong with it.
+_get_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call_stream(stream, dev):
+    if stream is None and _get_raw_stream is not None:
+        return _get_raw_stream(dev)
+    return _stream(stream)
+
+
+def _on_device(t, name, dev):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor or an int address")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a device (cuda) tensor, got {t.device}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {t.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, the current device is cuda:{dev}")
 
 
-def _dense(t, name, dtype, numel):
-    """_arg for a tensor that must live on the current device."""
+def _dense(t, name, dtype, numel, dev):
+    """Address of a contiguous tensor of at least numel elements on the
+    current device."""
     if t is None or isinstance(t, int):
         return t
-    _on_device(t, name)
-    return _arg(t, name, dtype, numel)
+    _on_device(t, name, dev)
+    if t.dtype is dtype and t.is_contiguous() and t.numel() >= numel:
+        return t.data_ptr()
+    return _arg(t, name, dtype, numel)  # raises
 
 
-def _mat(t, name, dtype, rows, cols, ld):
+def _mat(t, name, dtype, rows, cols, ld, dev):
     """Address of a [rows, cols] matrix whose rows are ld elements apart."""
     if t is None or isinstance(t, int):
         return t
-    _on_device(t, name)
+    _on_device(t, name, dev)
+    if t.dtype is dtype and t.shape == (rows, cols) and t.stride() == (ld, 1):
+        return t.data_ptr()
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
@@ -540,24 +556,40 @@ def _mat(t, name, dtype, rows, cols, ld):
     return t.data_ptr()
 
 
-def _rows_of(t, name):
+def _rows_of(t, name, dev):
     """(dtype, rows, width, row stride) of a matrix argument."""
-    _on_device(t, name)
+    _on_device(t, name, dev)
     if t.dim() != 2:
         raise ValueError(f"{name}: expected a matrix, got {t.dim()} dimensions")
     if t.dtype not in _DTYPES:
         raise ValueError(f"{name}: dtype {t.dtype} is not supported")
     r, c = t.shape
-    if c > 1 and t.stride(1) != 1:
+    ld, one = t.stride()
+    if c > 1 and one != 1:
         raise ValueError(f"{name}: elements of a row must be adjacent")
-    ld = t.stride(0) if r > 1 else c
+    if r <= 1:
+        ld = c
     if ld < c:
         raise ValueError(f"{name}: rows overlap (row stride {ld}, width {c})")
     return t.dtype, r, c, ld
 
 
-def _offsets(offsets, E):
-    return _dense(offsets, "offsets", torch.int32, E + 1)
+def _pair_of(t, name, dtype, rows, cols, dev):
+    """Address and row stride of a [rows, cols] matrix of any row stride."""
+    dt, r, c, ld = _rows_of(t, name, dev)
+    if dt is not dtype:
+        raise ValueError(f"{name}: dtype {dt}, expected {dtype}")
+    if r != rows or c != cols:
+        raise ValueError(f"{name}: shape ({r}, {c}), expected ({rows}, {cols})")
+    return t.data_ptr(), ld
+
+
+def _offsets(offsets, E, dev):
+    return _dense(offsets, "offsets", torch.int32, E + 1, dev)
+
+
+def _n_rows(n_rows, dev):
+    return None if n_rows is None else _dense(n_rows, "n_rows", torch.int32, 1, dev)
 
 
 def _grouped_dims(g):
@@ -570,57 +602,61 @@ def moe_grouped_gemm(g, offsets, x, w, y, stream=None):
     """y[i] = w[e] x[i] for the rows i of every expert e: x [rows, K], w
     [E, N, K], y [rows, N]; rows of no expert keep what they held."""
     el, ld_x, ld_y = _grouped_dims(g)
+    rows, E, N, K, dev = g.rows, g.E, g.N, g.K, torch.cuda.current_device()
     _check(load().moe_grouped_gemm(
-        ctypes.byref(g), _offsets(offsets, g.E), _mat(x, "x", el, g.rows, g.K, ld_x),
-        _dense(w, "w", el, g.E * g.N * g.K), _mat(y, "y", el, g.rows, g.N, ld_y),
-        _stream(stream)))
+        g, _offsets(offsets, E, dev), _mat(x, "x", el, rows, K, ld_x, dev),
+        _dense(w, "w", el, E * N * K, dev), _mat(y, "y", el, rows, N, ld_y, dev),
+        _call_stream(stream, dev)))
 
 
 def moe_grouped_gemm_dx(g, offsets, dy, w, dx, stream=None):
     """dx[i] = w[e]^T dy[i]."""
     el, ld_x, ld_y = _grouped_dims(g)
+    rows, E, N, K, dev = g.rows, g.E, g.N, g.K, torch.cuda.current_device()
     _check(load().moe_grouped_gemm_dx(
-        ctypes.byref(g), _offsets(offsets, g.E), _mat(dy, "dy", el, g.rows, g.N, ld_y),
-        _dense(w, "w", el, g.E * g.N * g.K), _mat(dx, "dx", el, g.rows, g.K, ld_x),
-        _stream(stream)))
+        g, _offsets(offsets, E, dev), _mat(dy, "dy", el, rows, N, ld_y, dev),
+        _dense(w, "w", el, E * N * K, dev), _mat(dx, "dx", el, rows, K, ld_x, dev),
+        _call_stream(stream, dev)))
 
 
 def moe_grouped_gemm_dw(g, offsets, x, dy, dw, ws=None, accumulate=False, stream=None):
     """dw[e] = sum over e's rows of dy[i] x[i]^T (fp32 [E, N, K]), added to dw
     with accumulate; ws: grouped_dw_workspace_size bytes (None if 0)."""
     el, ld_x, ld_y = _grouped_dims(g)
-    # an empty workspace tensor has no address
-    w_ptr = None if ws is None or (isinstance(ws, torch.Tensor) and ws.numel() == 0) \
-        else _dense(ws, "ws", None, None)
-    if isinstance(ws, int):
-        raise TypeError("ws: expected a torch.Tensor (its size is checked)")
+    rows, E, N, K, dev = g.rows, g.E, g.N, g.K, torch.cuda.current_device()
+    w_ptr, w_bytes = None, 0
+    if ws is not None:
+        _on_device(ws, "ws", dev)
+        if not ws.is_contiguous():
+            raise ValueError("ws: must be contiguous")
+        w_bytes = _nbytes(ws)
+        w_ptr = ws.data_ptr() if w_bytes else None  # an empty tensor has no address
     _check(load().moe_grouped_gemm_dw(
-        ctypes.byref(g), _offsets(offsets, g.E), _mat(x, "x", el, g.rows, g.K, ld_x),
-        _mat(dy, "dy", el, g.rows, g.N, ld_y),
-        _dense(dw, "dw", torch.float32, g.E * g.N * g.K), int(bool(accumulate)), w_ptr,
-        0 if ws is None else _nbytes(ws), _stream(stream)))
+        g, _offsets(offsets, E, dev), _mat(x, "x", el, rows, K, ld_x, dev),
+        _mat(dy, "dy", el, rows, N, ld_y, dev),
+        _dense(dw, "dw", torch.float32, E * N * K, dev), 1 if accumulate else 0, w_ptr,
+        w_bytes, _call_stream(stream, dev)))
 
 
 def moe_swiglu(gu, h, n_rows=None, stream=None):
     """h = silu(g) u for rows gu = [g, u]: gu [rows, 2f], h [rows, f]. n_rows:
     a one-element int32 device tensor, rows from it on are left alone."""
-    dt, rows, f, ld_h = _rows_of(h, "h")
-    ld_gu = _rows_of(gu, "gu")[3]
-    _check(load().moe_swiglu(
-        _DTYPES[dt], rows, f, _mat(gu, "gu", dt, rows, 2 * f, ld_gu), ld_gu,
-        _mat(h, "h", dt, rows, f, ld_h), ld_h,
-        _dense(n_rows, "n_rows", torch.int32, 1), _stream(stream)))
+    dev = torch.cuda.current_device()
+    dt, rows, f, ld_h = _rows_of(h, "h", dev)
+    gu_ptr, ld_gu = _pair_of(gu, "gu", dt, rows, 2 * f, dev)
+    _check(load().moe_swiglu(_DTYPES[dt], rows, f, gu_ptr, ld_gu, h.data_ptr(), ld_h,
+                             _n_rows(n_rows, dev), _call_stream(stream, dev)))
 
 
 def moe_swiglu_backward(gu, dh, dgu, n_rows=None, stream=None):
     """dgu [rows, 2f] from gu [rows, 2f] and dh [rows, f]."""
-    dt, rows, f, ld_dh = _rows_of(dh, "dh")
-    ld_gu, ld_dgu = _rows_of(gu, "gu")[3], _rows_of(dgu, "dgu")[3]
+    dev = torch.cuda.current_device()
+    dt, rows, f, ld_dh = _rows_of(dh, "dh", dev)
+    gu_ptr, ld_gu = _pair_of(gu, "gu", dt, rows, 2 * f, dev)
+    dgu_ptr, ld_dgu = _pair_of(dgu, "dgu", dt, rows, 2 * f, dev)
     _check(load().moe_swiglu_backward(
-        _DTYPES[dt], rows, f, _mat(gu, "gu", dt, rows, 2 * f, ld_gu), ld_gu,
-        _mat(dh, "dh", dt, rows, f, ld_dh), ld_dh,
-        _mat(dgu, "dgu", dt, rows, 2 * f, ld_dgu), ld_dgu,
-        _dense(n_rows, "n_rows", torch.int32, 1), _stream(stream)))
+        _DTYPES[dt], rows, f, gu_ptr, ld_gu, dh.data_ptr(), ld_dh, dgu_ptr, ld_dgu,
+        _n_rows(n_rows, dev), _call_stream(stream, dev)))
 
 
 def moe_mxfp4_quantize(x, codes, scales, index=None, index_div=1, n_rows=None,
@@ -628,42 +664,47 @@ def moe_mxfp4_quantize(x, codes, scales, index=None, index_div=1, n_rows=None,
     """Rows of x [src_rows, K] to MXFP4: codes uint8 [..., K / 2] and scales
     uint8 [..., mxfp4_scale_stride(K)], contiguous, of as many rows as index
     (int32) has entries, row i from x[index[i] // index_div] (zeros where that
-    is no row); without index, of x's rows."""
-    if x.dim() > 2 and x.is_contiguous():  # weights [E, N, K]
+    is no row); without index, of x's rows (a contiguous x may have more
+    dimensions: weights [E, N, K])."""
+    dev = torch.cuda.current_device()
+    if isinstance(x, torch.Tensor) and x.dim() > 2 and x.is_contiguous():
         x = x.view(-1, x.shape[-1])
-    dt, src, K, ld_x = _rows_of(x, "x")
-    rows = src if index is None else index.numel()
+    dt, src, K, ld_x = _rows_of(x, "x", dev)
+    rows, index_ptr = src, None
+    if index is not None:
+        rows = index.numel()
+        index_ptr = _dense(index, "index", torch.int32, rows, dev)
+    u8 = torch.uint8
     _check(load().moe_mxfp4_quantize(
-        _DTYPES[dt], rows, K, x.data_ptr(), ld_x, src,
-        _dense(index, "index", torch.int32, rows), int(index_div),
-        _dense(n_rows, "n_rows", torch.int32, 1),
-        _dense(codes, "codes", torch.uint8, rows * (K // 2)),
-        _dense(scales, "scales", torch.uint8, rows * mxfp4_scale_stride(K)),
-        _stream(stream)))
+        _DTYPES[dt], rows, K, x.data_ptr(), ld_x, src, index_ptr, int(index_div),
+        _n_rows(n_rows, dev), _dense(codes, "codes", u8, rows * (K // 2), dev),
+        _dense(scales, "scales", u8, rows * mxfp4_scale_stride(K), dev),
+        _call_stream(stream, dev)))
 
 
 def moe_mxfp4_dequantize(codes, scales, y, n_rows=None, stream=None):
     """The values of codes and scales, y [rows, K]."""
-    dt, rows, K, ld_y = _rows_of(y, "y")
+    dev = torch.cuda.current_device()
+    dt, rows, K, ld_y = _rows_of(y, "y", dev)
+    u8 = torch.uint8
     _check(load().moe_mxfp4_dequantize(
-        _DTYPES[dt], rows, K, _dense(codes, "codes", torch.uint8, rows * (K // 2)),
-        _dense(scales, "scales", torch.uint8, rows * mxfp4_scale_stride(K)),
-        _mat(y, "y", dt, rows, K, ld_y), ld_y,
-        _dense(n_rows, "n_rows", torch.int32, 1), _stream(stream)))
+        _DTYPES[dt], rows, K, _dense(codes, "codes", u8, rows * (K // 2), dev),
+        _dense(scales, "scales", u8, rows * mxfp4_scale_stride(K), dev),
+        y.data_ptr(), ld_y, _n_rows(n_rows, dev), _call_stream(stream, dev)))
 
 
 def moe_mxfp4_grouped_gemm(g, offsets, x_codes, x_scales, w_codes, w_scales, y,
                            stream=None):
     """moe_grouped_gemm on MXFP4 operands; y has g's dtype."""
     el, _, ld_y = _grouped_dims(g)
-    S, u8 = mxfp4_scale_stride(g.K), torch.uint8
+    rows, E, N, K, dev = g.rows, g.E, g.N, g.K, torch.cuda.current_device()
+    S, u8 = mxfp4_scale_stride(K), torch.uint8
     _check(load().moe_mxfp4_grouped_gemm(
-        ctypes.byref(g), _offsets(offsets, g.E),
-        _dense(x_codes, "x_codes", u8, g.rows * (g.K // 2)),
-        _dense(x_scales, "x_scales", u8, g.rows * S),
-        _dense(w_codes, "w_codes", u8, g.E * g.N * (g.K // 2)),
-        _dense(w_scales, "w_scales", u8, g.E * g.N * S),
-        _mat(y, "y", el, g.rows, g.N, ld_y), _stream(stream)))
+        g, _offsets(offsets, E, dev), _dense(x_codes, "x_codes", u8, rows * (K // 2), dev),
+        _dense(x_scales, "x_scales", u8, rows * S, dev),
+        _dense(w_codes, "w_codes", u8, E * N * (K // 2), dev),
+        _dense(w_scales, "w_scales", u8, E * N * S, dev),
+        _mat(y, "y", el, rows, N, ld_y, dev), _call_stream(stream, dev)))
 
 
 def workspace_views(cfg: MoeConfig, ws: torch.Tensor) -> dict:

@@ -138,7 +138,10 @@ def test_elementwise_calls_are_checked(B):
 
 def test_scale_rows(B):
     assert [B.mxfp4_scale_stride(k) for k in (32, 64, 128, 160, 256, 7168)] == [4, 4, 4, 8, 8, 224]
+    for k in (32, 64, 128, 160, 1056, 7168):
+        assert B.load().moe_mxfp4_scale_stride(k) == B.mxfp4_scale_stride(k)
     for k in (0, -32, 31, 48):
+        assert B.load().moe_mxfp4_scale_stride(k) == -1
         with pytest.raises(ValueError):
             B.mxfp4_scale_stride(k)
 
@@ -154,7 +157,8 @@ def test_calls_without_rows_launch_nothing(B):
                                 None) == B.MOE_OK
 
 
-def test_host_tensors_are_refused(B):
+def test_host_tensors_are_refused(B, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     g = B.grouped(4, 1, 8, 32, "bf16")
     t = torch.zeros(4, 32, dtype=torch.bfloat16)
     off = torch.zeros(2, dtype=torch.int32)

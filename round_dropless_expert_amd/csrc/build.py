@@ -23,8 +23,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["route_plan.hip", "dispatch_combine.hip", "grouped_gemm.hip",
            "wgrad.hip", "backward.hip", "api.hip", "ragged_gemm.hip", "ragged_ring.hip",
-           "ragged_wgrad.hip", "swiglu.hip",
-           "mxfp4.hip", "ragged_api.hip"]
+           "ragged_skinny.hip", "ragged_wgrad.hip", "swiglu.hip", "mxfp4.hip",
+           "ragged_api.hip"]
 HEADERS = ["device_common.hpp", "launch.hpp", "api_common.hpp", "ragged.hpp",
            "ragged_device.hpp", "ragged_ring.hpp"]
 

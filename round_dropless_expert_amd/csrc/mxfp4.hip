@@ -290,76 +290,6 @@ hipError_t dequantize(DequantParams p, int num_cus, hipStream_t st) {
   return hipGetLastError();
 }
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-
-struct MxParams {
-  const uint8_t* xq;
-  const uint8_t* xs;
-  const uint8_t* wq;
-  const uint8_t* ws;
-  void* y;
-  const int32_t* offsets;
-  int64_t ld_y;
-  int rows, E, N, K;
-  int stride;  // bytes of a scale row
-  int tiles_n;
-};
-
-// v_mfma_scale_f32_16x16x128_f8f6f4 on 4-bit operands: lane l supplies row
-// l % 16 and block l / 16 (32 values, 16 bytes) of 128 values of c, and its
-// block's scale byte.
-__device__ __forceinline__ f32x4 mx_mma16(u32x4 a, int sa, u32x4 b, int sb, f32x4 c) {
-  const i32x8 av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
-  const i32x8 bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, sa, 0, sb);
-}
-
-// One wavefront per 16 rows x 16 features.
-template <typename T>
-__global__ __launch_bounds__(64) void mx_gemm_kernel(MxParams p) {
-  ExpertUnit u;
-  const int t = blockIdx.x;
-  if (!find_unit(p.offsets, p.E, p.rows, t,
-                 [&](int rows) { return (rows + 15) / 16 * p.tiles_n; }, &u))
-    return;
-  const int local = t - u.first;
-  const int m0 = local / p.tiles_n * 16, n0 = local % p.tiles_n * 16;
-  const int lane = threadIdx.x, l16 = lane & 15, blk = lane >> 4;
-  const int row = m0 + l16, feat = n0 + l16;
-  const bool xin = row < u.rows, win = feat < p.N;
-  const int64_t xr = (int64_t)u.start + (xin ? row : 0);
-  const int64_t wr = (int64_t)u.e * p.N + (win ? feat : 0);
-  const int64_t kb = p.K / 2;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  const u32x4 none = {0, 0, 0, 0};
-  for (int k = blk * kMxBlock; k < (p.K + 127) / 128 * 128; k += 128) {
-    const bool in = k < p.K;
-    const u32x4 x = xin && in ? *reinterpret_cast<const u32x4*>(p.xq + xr * kb + k / 2) : none;
-    const u32x4 w = win && in ? *reinterpret_cast<const u32x4*>(p.wq + wr * kb + k / 2) : none;
-    const int sx = xin && in ? p.xs[xr * p.stride + k / kMxBlock] : 127;
-    const int sw = win && in ? p.ws[wr * p.stride + k / kMxBlock] : 127;
-    acc = mx_mma16(x, sx, w, sw, acc);
-  }
-  // lane: feature l % 16, rows 4 (l / 16) + v
-  if (!win) return;
-#pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    const int r = m0 + 4 * blk + v;
-    if (r < u.rows)
-      static_cast<T*>(p.y)[((int64_t)u.start + r) * p.ld_y + feat] = from_f32<T>(acc[v]);
-  }
-}
-
-template <typename T>
-hipError_t mx_gemm(MxParams p, int num_cus, hipStream_t st) {
-  (void)num_cus;
-  p.tiles_n = (p.N + 15) / 16;
-  const int64_t jobs =
-      ((int64_t)p.rows / 16 + (p.rows < p.E ? p.rows : p.E)) * p.tiles_n;
-  hipLaunchKernelGGL((mx_gemm_kernel<T>), dim3((unsigned)jobs), dim3(64), 0, st, p);
-  return hipGetLastError();
-}
-
 }  // namespace
 
 hipError_t launch_mx_quantize(ElemType t, int64_t rows, int64_t K, const void* x, int64_t ld_x,
@@ -393,35 +323,26 @@ hipError_t launch_mx_gemm(const RaggedShape& s, const int32_t* offsets, const ui
                           int num_cus, hipStream_t st) {
   if (s.rows == 0) return hipSuccess;
   const int64_t es = elem_bytes(s.type);
-  if (s.rows > 16 * (int64_t)s.E) {
-    RingParams r{};
-    r.act = reinterpret_cast<const char*>(xq);
-    r.w = reinterpret_cast<const char*>(wq);
-    r.act_scales = reinterpret_cast<const char*>(xs);
-    r.w_scales = reinterpret_cast<const char*>(ws);
-    r.out = static_cast<char*>(y);
-    r.offsets = offsets;
-    r.lda = r.ldw = s.K / 2;
-    r.ldo = s.ld_y * es;
-    r.lds = mx_scale_stride(s.K);
-    r.wbytes = (int64_t)s.N * s.K / 2;
-    r.rows = (int)s.rows;
-    r.E = s.E;
-    r.B = s.N;
-    r.cbytes = s.K / 2;
-    r.out_vec = s.N % (16 / es) == 0 && s.ld_y % (16 / es) == 0 && aligned16(y);
-    return launch_ring(s.type == ElemType::kBF16  ? RingKind::kMxBF16
-                       : s.type == ElemType::kF16 ? RingKind::kMxF16
-                                                  : RingKind::kMxF32,
-                       r, num_cus, st);
-  }
-  const MxParams p{xq,     xs,          wq,  ws,  y,   offsets,
-                   s.ld_y, (int)s.rows, s.E, s.N, s.K, (int)mx_scale_stride(s.K), 0};
-  switch (s.type) {
-    case ElemType::kF32: return mx_gemm<float>(p, num_cus, st);
-    case ElemType::kBF16: return mx_gemm<bf16>(p, num_cus, st);
-    default: return mx_gemm<f16>(p, num_cus, st);
-  }
+  RingParams r{};
+  r.act = reinterpret_cast<const char*>(xq);
+  r.w = reinterpret_cast<const char*>(wq);
+  r.act_scales = reinterpret_cast<const char*>(xs);
+  r.w_scales = reinterpret_cast<const char*>(ws);
+  r.out = static_cast<char*>(y);
+  r.offsets = offsets;
+  r.lda = r.ldw = s.K / 2;
+  r.ldo = s.ld_y * es;
+  r.lds = mx_scale_stride(s.K);
+  r.wbytes = (int64_t)s.N * s.K / 2;
+  r.rows = (int)s.rows;
+  r.E = s.E;
+  r.B = s.N;
+  r.cbytes = s.K / 2;
+  r.out_vec = s.N % (16 / es) == 0 && s.ld_y % (16 / es) == 0 && aligned16(y);
+  return launch_ring(s.type == ElemType::kBF16  ? RingKind::kMxBF16
+                     : s.type == ElemType::kF16 ? RingKind::kMxF16
+                                                : RingKind::kMxF32,
+                     r, num_cus, st);
 }
 
 }  // namespace moe

@@ -51,6 +51,10 @@ struct WgradRingParams {
 hipError_t launch_wgrad_ring(bool is_bf16, const WgradRingParams& params, int num_cus,
                              hipStream_t st);
 
+// The same products for experts of few rows (ragged_skinny.hip; forward
+// kinds).
+hipError_t launch_skinny(RingKind kind, const RingParams& p, int num_cus, hipStream_t st);
+
 hipError_t launch_ring(RingKind kind, const RingParams& p, int num_cus, hipStream_t st);
 
 }  // namespace moe

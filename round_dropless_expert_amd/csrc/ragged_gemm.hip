@@ -38,7 +38,7 @@ template <typename T>
 struct Mma;
 template <>
 struct Mma<bf16> {
-  static constexpr int kSteps = 2;  // per 64 bytes of c
+  static constexpr int kStepBytes = 32;  // of c
   typedef bf16x8 frag_t;
   __device__ static __forceinline__ f32x16 mma(frag_t a, frag_t b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
@@ -46,7 +46,7 @@ struct Mma<bf16> {
 };
 template <>
 struct Mma<f16> {
-  static constexpr int kSteps = 2;
+  static constexpr int kStepBytes = 32;
   typedef f16x8 frag_t;
   __device__ static __forceinline__ f32x16 mma(frag_t a, frag_t b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
@@ -54,7 +54,7 @@ struct Mma<f16> {
 };
 template <>
 struct Mma<float> {
-  static constexpr int kSteps = 8;
+  static constexpr int kStepBytes = 8;
   typedef float frag_t;
   __device__ static __forceinline__ f32x16 mma(frag_t a, frag_t b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, c, 0, 0, 0);
@@ -86,30 +86,65 @@ __device__ __forceinline__ u32x4 load16(const T* at, int n) {
   return r.v;
 }
 
-// One operand's share of a stage: `kExt` rows of its output index by 64
-// bytes of c. Along: 64 bytes of c per row in LDS, at a pitch of 80 bytes.
-// Down: one LDS row per c, kExt elements and 16 bytes of padding.
+constexpr int kStage = 128;  // bytes of c
+constexpr int kAhead = 2;    // stages of loads in flight
+
+// One operand's share of a stage: `kExt` rows of its output index by kStage
+// bytes of c. Along: one LDS row per row, 16 bytes of padding. Down: one LDS
+// row per c, kExt elements and 16 bytes of padding.
 template <typename T, bool kAlong, int kExt>
 struct Operand {
   static constexpr int kEs = sizeof(T);
   static constexpr int kV = 16 / kEs;
-  static constexpr int kCk = 64 / kEs;
-  static constexpr int kPitch = kAlong ? 80 : kExt * kEs + 16;
-  static constexpr int kBytes = kAlong ? kExt * 80 : kCk * kPitch;
-  static constexpr int kPieces = kExt / 64;  // 16-byte pieces per thread
+  static constexpr int kCk = kStage / kEs;
+  static constexpr int kChunks = kStage / 16;  // of a row along c
+  static constexpr int kPitch = (kAlong ? kStage : kExt * kEs) + 16;
+  static constexpr int kBytes = kAlong ? kExt * kPitch : kCk * kPitch;
+  static constexpr int kPieces = kExt * kChunks / 256;  // 16-byte pieces per thread
+  typedef u32x4 regs_t[kPieces];
 
   const T* base;  // c = 0 of the tile's first row
   int64_t ld;
   int ext;  // rows of the output index that exist
-  u32x4 reg[kPieces];
+  // Where this thread's pieces of a whole stage lie, from the stage's first
+  // c: rows past ext read the last one instead (they feed outputs that are
+  // never stored). `whole`: no such load leaves its row; otherwise (a last,
+  // partial chunk of columns) it reads on into the next row, which the
+  // matrix's last row does not have.
+  int64_t at[kPieces];
+  bool whole;
 
-  // pieces of the stage at c0, where c exists below c_end
-  __device__ __forceinline__ void load(int c0, int c_end) {
+  __device__ __forceinline__ void set(const T* b, int64_t l, int e) {
+    base = b;
+    ld = l;
+    ext = e;
+    whole = kAlong || ext >= kExt || ext % kV == 0;
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
       const int id = (int)threadIdx.x + 256 * u;
       if constexpr (kAlong) {
-        const int row = id >> 2, c = c0 + (id & 3) * kV;
+        const int row = id / kChunks;
+        at[u] = (row < ext ? row : ext - 1) * ld + (id % kChunks) * kV;
+      } else {
+        constexpr int kPer = kExt * kEs / 16;
+        const int row = (id % kPer) * kV;
+        at[u] = (id / kPer) * ld + (row < ext ? row : 0);
+      }
+    }
+  }
+  // pieces of a whole stage at c0
+  __device__ __forceinline__ void load(regs_t& reg, int c0) const {
+    const T* from = base + (kAlong ? c0 : c0 * ld);
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) __builtin_memcpy(&reg[u], from + at[u], 16);
+  }
+  // pieces of the stage at c0, where c exists below c_end
+  __device__ __forceinline__ void load_some(regs_t& reg, int c0, int c_end) const {
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int id = (int)threadIdx.x + 256 * u;
+      if constexpr (kAlong) {
+        const int row = id / kChunks, c = c0 + (id % kChunks) * kV;
         reg[u] = load16(base + row * ld + c, row < ext ? c_end - c : 0);
       } else {
         constexpr int kPer = kExt * kEs / 16;
@@ -118,13 +153,13 @@ struct Operand {
       }
     }
   }
-  __device__ __forceinline__ void store(char* lds) const {
+  __device__ static __forceinline__ void store(const regs_t& reg, char* lds) {
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
       const int id = (int)threadIdx.x + 256 * u;
       int off;
       if constexpr (kAlong) {
-        off = (id >> 2) * 80 + (id & 3) * 16;
+        off = (id / kChunks) * kPitch + (id % kChunks) * 16;
       } else {
         constexpr int kPer = kExt * kEs / 16;
         off = (id / kPer) * kPitch + (id % kPer) * 16;
@@ -139,10 +174,10 @@ struct Operand {
     typedef typename Mma<T>::frag_t frag_t;
     if constexpr (kEs == 4) {
       const int c = 2 * s + half;
-      return kAlong ? *reinterpret_cast<const float*>(lds + (row0 + l32) * 80 + c * 4)
+      return kAlong ? *reinterpret_cast<const float*>(lds + (row0 + l32) * kPitch + c * 4)
                     : *reinterpret_cast<const float*>(lds + c * kPitch + (row0 + l32) * 4);
     } else if constexpr (kAlong) {
-      return *reinterpret_cast<const frag_t*>(lds + (row0 + l32) * 80 + s * 32 + half * 16);
+      return *reinterpret_cast<const frag_t*>(lds + (row0 + l32) * kPitch + s * 32 + half * 16);
     } else {
       // transposing LDS read: in each group of 16 lanes, lane i receives
       // 16-bit element i % 4 of the 8 bytes addressed by lanes 4 j + i / 4,
@@ -175,9 +210,14 @@ __device__ __forceinline__ int slots_before(const int32_t* offsets, int e, int n
 }
 
 // General kernel: one workgroup per output tile of 64 W x 64 W, 2 x 2
-// wavefronts of W x W blocks of 32 x 32. Stages of 64 bytes of c go through
-// registers into two LDS buffers, the next stage's loads in flight while a
-// stage is multiplied. Takes every size, stride and element alignment.
+// wavefronts of W x W blocks of 32 x 32. Stages of 128 bytes of c go through
+// registers into two LDS buffers, the loads of the next two stages in flight
+// while one is multiplied. Takes every size, stride and element alignment.
+// The whole stages run without a bounds check; the last, partial one is loaded
+// element by element where it has to be. 32768 rows, N = K = 2049, 8 experts,
+// fp16: 540 us, 510 TFLOP/s (64-byte stages 608 us, one stage ahead 659 us);
+// what bounds it is LDS, which the 64 x 64 wavefront tiles read 1 KiB of per
+// 32 x 32 x 16 product, and the barrier of each stage.
 template <typename T, int kMode, int W>
 __global__ __launch_bounds__(256) void ragged_general_kernel(RaggedParams p) {
   constexpr int kTile = 64 * W;
@@ -216,21 +256,18 @@ __global__ __launch_bounds__(256) void ragged_general_kernel(RaggedParams p) {
     c_begin = part * p.chunk;
     c_end = u.rows - c_begin < p.chunk ? u.rows : c_begin + p.chunk;
     a_ext = p.A - a0;
-    P.base = static_cast<const T*>(p.p) + (int64_t)u.start * p.ldp + a0;
-    Q.base = static_cast<const T*>(p.q) + (int64_t)u.start * p.ldq + b0;
+    P.set(static_cast<const T*>(p.p) + (int64_t)u.start * p.ldp + a0, p.ldp, a_ext);
+    Q.set(static_cast<const T*>(p.q) + (int64_t)u.start * p.ldq + b0, p.ldq, p.B - b0);
   } else {
     a0 = local / p.tiles_b * kTile;
     b0 = local % p.tiles_b * kTile;
     c_end = p.C;
     a_ext = u.rows - a0;
-    P.base = static_cast<const T*>(p.p) + ((int64_t)u.start + a0) * p.ldp;
-    Q.base = static_cast<const T*>(p.q) + (int64_t)u.e * p.B * p.C +
-             (kMode == kForward ? (int64_t)b0 * p.ldq : (int64_t)b0);
+    P.set(static_cast<const T*>(p.p) + ((int64_t)u.start + a0) * p.ldp, p.ldp, a_ext);
+    Q.set(static_cast<const T*>(p.q) + (int64_t)u.e * p.B * p.C +
+              (kMode == kForward ? (int64_t)b0 * p.ldq : (int64_t)b0),
+          p.ldq, p.B - b0);
   }
-  P.ld = p.ldp;
-  Q.ld = p.ldq;
-  P.ext = a_ext;
-  Q.ext = p.B - b0;
 
   // weight gradient: the slot of this chunk (past the last one only if the
   // offsets overlap: then it is not stored)
@@ -249,32 +286,59 @@ __global__ __launch_bounds__(256) void ragged_general_kernel(RaggedParams p) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
 
-  if (c_begin < c_end) {
-    P.load(c_begin, c_end);
-    Q.load(c_begin, c_end);
-    int buf = 0;
-    for (int c = c_begin; c < c_end; c += kCk, buf ^= 1) {
-      // the buffer's last readers passed the previous stage's barrier
-      P.store(lds[buf]);
-      Q.store(lds[buf] + P_t::kBytes);
-      __syncthreads();
-      if (c + kCk < c_end) {
-        P.load(c + kCk, c_end);
-        Q.load(c + kCk, c_end);
-      }
+  auto multiply = [&](const char* buf) {
 #pragma unroll
-      for (int s = 0; s < Mma<T>::kSteps; ++s) {
-        typename Mma<T>::frag_t fa[W], fb[W];
+    for (int s = 0; s < kStage / Mma<T>::kStepBytes; ++s) {
+      typename Mma<T>::frag_t fa[W], fb[W];
 #pragma unroll
-        for (int i = 0; i < W; ++i) fa[i] = P_t::frag(lds[buf], wa + 32 * i, s);
+      for (int i = 0; i < W; ++i) fa[i] = P_t::frag(buf, wa + 32 * i, s);
 #pragma unroll
-        for (int j = 0; j < W; ++j) fb[j] = Q_t::frag(lds[buf] + P_t::kBytes, wb + 32 * j, s);
+      for (int j = 0; j < W; ++j) fb[j] = Q_t::frag(buf + P_t::kBytes, wb + 32 * j, s);
 #pragma unroll
-        for (int i = 0; i < W; ++i)
+      for (int i = 0; i < W; ++i)
 #pragma unroll
-          for (int j = 0; j < W; ++j) acc[i][j] = Mma<T>::mma(fa[i], fb[j], acc[i][j]);
-      }
+        for (int j = 0; j < W; ++j) acc[i][j] = Mma<T>::mma(fa[i], fb[j], acc[i][j]);
     }
+  };
+  // the whole stages; the rest is at most one more
+  const int count = c_end - c_begin;
+  int whole = count / kCk;
+  if (!(P.whole && Q.whole) && whole > 0 && whole * kCk == count) --whole;
+  typename P_t::regs_t p0, p1;
+  typename Q_t::regs_t q0, q1;
+  // stage i from its registers into LDS buffer i % 2, the loads of stage i +
+  // kAhead into them, and its products. The buffer's last readers passed the
+  // barrier of the stage between.
+  auto stage = [&](int i, int buf, typename P_t::regs_t& rp, typename Q_t::regs_t& rq) {
+    P_t::store(rp, lds[buf]);
+    Q_t::store(rq, lds[buf] + P_t::kBytes);
+    __syncthreads();
+    if (i + kAhead < whole) {
+      P.load(rp, c_begin + (i + kAhead) * kCk);
+      Q.load(rq, c_begin + (i + kAhead) * kCk);
+    }
+    multiply(lds[buf]);
+  };
+  if (whole > 0) {
+    P.load(p0, c_begin);
+    Q.load(q0, c_begin);
+  }
+  if (whole > 1) {
+    P.load(p1, c_begin + kCk);
+    Q.load(q1, c_begin + kCk);
+  }
+  for (int i = 0; i < whole; i += 2) {
+    stage(i, 0, p0, q0);
+    if (i + 1 < whole) stage(i + 1, 1, p1, q1);
+  }
+  if (whole * kCk < count) {
+    P.load_some(p0, c_begin + whole * kCk, c_end);
+    Q.load_some(q0, c_begin + whole * kCk, c_end);
+    char* buf = lds[whole & 1];
+    P_t::store(p0, buf);
+    Q_t::store(q0, buf + P_t::kBytes);
+    __syncthreads();
+    multiply(buf);
   }
 
   // lane: column b = l % 32 of a block, rows a = 8 (v / 4) + 4 (l / 32) + v % 4
@@ -314,6 +378,7 @@ __global__ __launch_bounds__(256) void ragged_add_slots_kernel(RaggedParams p) {
   const int64_t n = (int64_t)p.A * p.B / V;
   const int lane = threadIdx.x & 63;
   int before = 0;  // slots of the experts below
+  uint32_t turn = 0;  // experts with slots so far
   for (int base = 0; base < p.E; base += kWave) {
     int start, rows = 0, own = 0;
     if (base + lane < p.E) {
@@ -326,6 +391,7 @@ __global__ __launch_bounds__(256) void ragged_add_slots_kernel(RaggedParams p) {
     while (todo) {
       const int l = __builtin_ctzll(todo);
       todo &= todo - 1;
+      if (turn++ % gridDim.y != blockIdx.y) continue;
       const int last = __builtin_amdgcn_readlane(incl, l);
       const int first = last - __builtin_amdgcn_readlane(own, l);
       const int count = (last < p.n_slots ? last : p.n_slots) - first;
@@ -334,6 +400,7 @@ __global__ __launch_bounds__(256) void ragged_add_slots_kernel(RaggedParams p) {
       for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n;
            i += (int64_t)gridDim.x * 256) {
         vec_t r = o[i];
+#pragma unroll 4
         for (int k = 0; k < count; ++k) r += s[k * n + i];
         o[i] = r;
       }
@@ -344,7 +411,8 @@ __global__ __launch_bounds__(256) void ragged_add_slots_kernel(RaggedParams p) {
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 // Tile of the general kernel: 128 x 128 unless the outputs are too few to
-// give every CU one.
+// give every CU two.
+constexpr int kLargeJobs = 2;
 template <typename T, int kMode>
 hipError_t launch_general(RaggedParams p, int num_cus, hipStream_t st) {
   auto jobs = [&](int tile) -> int64_t {
@@ -356,13 +424,13 @@ hipError_t launch_general(RaggedParams p, int num_cus, hipStream_t st) {
     return ((int64_t)p.rows / tile + (p.rows < p.E ? p.rows : p.E)) * p.tiles_b;
   };
   const int64_t large = jobs(128);
-  if (large >= 2 * (int64_t)num_cus) {
-    hipLaunchKernelGGL((ragged_general_kernel<T, kMode, 2>), dim3((unsigned)large), dim3(256), 0,
-                       st, p);
+  if (large >= kLargeJobs * (int64_t)num_cus) {
+    hipLaunchKernelGGL((ragged_general_kernel<T, kMode, 2>),
+                       dim3((unsigned)large), dim3(256), 0, st, p);
   } else {
     const int64_t small = jobs(64);
-    hipLaunchKernelGGL((ragged_general_kernel<T, kMode, 1>), dim3((unsigned)small), dim3(256), 0,
-                       st, p);
+    hipLaunchKernelGGL((ragged_general_kernel<T, kMode, 1>), dim3((unsigned)small), dim3(256),
+                       0, st, p);
   }
   return hipGetLastError();
 }
@@ -417,15 +485,17 @@ RaggedParams base_params(const RaggedShape& s, const int32_t* offsets) {
 
 // Chunks: an expert's tiles run at once, so a chunk may hold half of the rows
 // that a CU sums in all (rows * tiles / 256), or an expert with many rows
-// holds up the launch; but at least
-// 512 rows each (a chunk past the first costs a write and a read of [N][K]
-// in fp32, its product 2 N K flops a row: below some hundred rows the
-// traffic would outweigh it). A function of the shape alone: it fixes the
-// order of the sums.
+// holds up the launch. A chunk past the first costs a write and a read of
+// [N][K] in fp32 against 2 N K flops a row: 512 rows at least, or 128 where
+// [N][K] is one tile and its slots are small (8192 rows of 8 experts with N =
+// K = 512: 46 us with chunks of 512, 59 with 128; 1024 rows with N = 256, K =
+// 64 in fp32: 15 us with 512, 9 with 128). A function of the shape alone: it
+// fixes the order of the sums.
 DwSplit dw_split(const RaggedShape& s) {
   const int64_t tiles = (int64_t)ceil_div(s.N, 256) * ceil_div(s.K, 256);
+  const int64_t least = tiles == 1 ? 128 : 512;
   int64_t chunk = (s.rows * tiles + 511) / 512;
-  chunk = chunk < 512 ? 512 : (chunk + 63) / 64 * 64;
+  chunk = chunk < least ? least : (chunk + 63) / 64 * 64;
   // a chunk's rows are addressed with 32-bit byte offsets
   const int64_t ld = (s.ld_x > s.ld_y ? s.ld_x : s.ld_y) * elem_bytes(s.type);
   const int64_t most = (((int64_t)1 << 31) - 1) / ld / 64 * 64;
@@ -500,7 +570,9 @@ hipError_t launch_ragged_dw(const RaggedShape& s, const int32_t* offsets, const 
   if (e != hipSuccess || split.slots == 0) return e;
   const bool vec = (int64_t)s.N * s.K % 4 == 0 && aligned16(dw);
   const int most = num_cus * 8, blocks = ceil_div((int64_t)s.N * s.K, vec ? 1024 : 256);
-  const dim3 grid(blocks < most ? blocks : most);
+  // and y over the experts with slots, where [N][K] is small
+  const int gx = blocks < most ? blocks : most;
+  const dim3 grid(gx, gx < num_cus ? (s.E < 8 ? s.E : 8) : 1);
   if (vec)
     hipLaunchKernelGGL((ragged_add_slots_kernel<4>), grid, dim3(256), 0, st, p);
   else

@@ -59,6 +59,39 @@ __device__ __forceinline__ bool find_unit(const int32_t* offsets, int E, int n, 
   return false;
 }
 
+// The unit of this workgroup when the units are dealt to the XCDs in
+// contiguous eighths (workgroup b runs on XCD b % 8): false where it has none.
+template <typename Units>
+__device__ __forceinline__ bool find_xcd_unit(const int32_t* offsets, int E, int n, Units units,
+                                              int* t, ExpertUnit* out) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int xcd = (int)(blockIdx.x % 8), place = (int)(blockIdx.x / 8);
+  int total = 0;
+  for (int base = 0; base < E; base += kWave) {
+    int start = 0, rows = 0, own = 0;
+    if (base + lane < E) {
+      expert_rows(offsets, base + lane, n, &start, &rows);
+      own = units(rows);
+    }
+    const int incl = wave_inclusive_scan(own);
+    total += __builtin_amdgcn_readlane(incl, kWave - 1);
+    if (E <= kWave) {  // one pass finds it
+      const int share = (total + 7) / 8;
+      *t = xcd * share + place;
+      if (place >= share || *t >= total) return false;
+      const int l = __builtin_popcountll(__builtin_amdgcn_ballot_w64(incl <= *t));
+      out->e = l;
+      out->start = __builtin_amdgcn_readlane(start, l);
+      out->rows = __builtin_amdgcn_readlane(rows, l);
+      out->first = __builtin_amdgcn_readlane(incl - own, l);
+      return true;
+    }
+  }
+  const int share = (total + 7) / 8;
+  *t = xcd * share + place;
+  return place < share && find_unit(offsets, E, n, *t, units, out);
+}
+
 // Rows that an elementwise call processes.
 __device__ __forceinline__ int64_t live_rows(int64_t rows, const int32_t* n_rows) {
   if (!n_rows) return rows;

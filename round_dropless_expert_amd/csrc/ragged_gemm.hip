@@ -229,21 +229,20 @@ __global__ __launch_bounds__(256) void ragged_general_kernel(RaggedParams p) {
   __shared__ __attribute__((aligned(16))) char lds[2][P_t::kBytes + Q_t::kBytes];
 
   const int per = kMode == kWeightGrad ? p.tiles_a * p.tiles_b : p.tiles_b;
+  auto units = [&](int rows) {
+    if constexpr (kMode == kWeightGrad) {
+      // an expert without rows still stores its zeros
+      const int n = (int)(((int64_t)rows + p.chunk - 1) / p.chunk);
+      return (n == 0 && !p.accumulate ? 1 : n) * per;
+    } else {
+      return (int)(((int64_t)rows + kTile - 1) / kTile) * per;
+    }
+  };
+  // Each XCD (workgroups b % 8) takes a contiguous eighth of the tiles: it
+  // then reads an eighth of the rows, and the weights of few experts.
   ExpertUnit u;
-  const int t = blockIdx.x;
-  const bool found = find_unit(
-      p.offsets, p.E, p.rows, t,
-      [&](int rows) {
-        if constexpr (kMode == kWeightGrad) {
-          // an expert without rows still stores its zeros
-          const int n = (int)(((int64_t)rows + p.chunk - 1) / p.chunk);
-          return (n == 0 && !p.accumulate ? 1 : n) * per;
-        } else {
-          return (int)(((int64_t)rows + kTile - 1) / kTile) * per;
-        }
-      },
-      &u);
-  if (!found) return;
+  int t = 0;
+  if (!find_xcd_unit(p.offsets, p.E, p.rows, units, &t, &u)) return;
   const int local = t - u.first;
 
   P_t P;
@@ -423,12 +422,13 @@ hipError_t launch_general(RaggedParams p, int num_cus, hipStream_t st) {
       return ((int64_t)p.rows / p.chunk + p.E) * p.tiles_a * p.tiles_b;
     return ((int64_t)p.rows / tile + (p.rows < p.E ? p.rows : p.E)) * p.tiles_b;
   };
-  const int64_t large = jobs(128);
+  // (rounded up to whole turns over the XCDs)
+  const int64_t large = (jobs(128) + 7) / 8 * 8;
   if (large >= kLargeJobs * (int64_t)num_cus) {
     hipLaunchKernelGGL((ragged_general_kernel<T, kMode, 2>),
                        dim3((unsigned)large), dim3(256), 0, st, p);
   } else {
-    const int64_t small = jobs(64);
+    const int64_t small = (jobs(64) + 7) / 8 * 8;
     hipLaunchKernelGGL((ragged_general_kernel<T, kMode, 1>), dim3((unsigned)small), dim3(256),
                        0, st, p);
   }

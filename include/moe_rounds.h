@@ -520,8 +520,8 @@ moe_status_t moe_backward(const moe_config_t *cfg, const void *x,
  * elem below is fp32, bf16 or fp16 (MOE_F32, MOE_BF16, MOE_F16). Products
  * run on the matrix cores with fp32 accumulation and round each output once.
  * Infinities and NaN follow the arithmetic: they reach exactly the outputs
- * whose sums contain them. Results do not depend on how rows are grouped
- * into tiles or calls, and repeat bit for bit. */
+ * whose sums contain them. Calls of the same shape (and alignment) repeat bit
+ * for bit; another shape may be summed in another order. */
 
 /* rows: rows of the buffers; w: E matrices [N][K] (out x in), contiguous;
  * x and dx: [rows][K] at ld_x; y and dy: [rows][N] at ld_y. Limits: rows <

@@ -26,6 +26,12 @@ __device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int n
   *rows = b > a ? b - a : 0;
 }
 
+// Units (tiles, jobs) of one launch at most. Offsets in order stay far below
+// (the ABI refuses larger shapes); overlapping ones can pass it, and are then
+// not worked on: every sum of 64 experts' units fits 32 bits, so a check
+// behind each keeps all of them exact.
+constexpr uint32_t kMaxUnits = 1u << 26;
+
 // The expert whose units hold unit t, when expert e owns units(rows_e)
 // consecutive units: every wavefront scans 64 experts at a time. All lanes
 // return the same values; false past the last unit.
@@ -46,6 +52,8 @@ __device__ __forceinline__ bool find_unit(const int32_t* offsets, int E, int n, 
       own = units(rows);
     }
     const int incl = wave_inclusive_scan(own) + carry;
+    carry = __builtin_amdgcn_readlane(incl, kWave - 1);
+    if ((uint32_t)carry > kMaxUnits) return false;
     const int before = __builtin_popcountll(__builtin_amdgcn_ballot_w64(incl <= t));
     if (before < kWave && base + before < E) {
       out->e = base + before;
@@ -54,7 +62,6 @@ __device__ __forceinline__ bool find_unit(const int32_t* offsets, int E, int n, 
       out->first = __builtin_amdgcn_readlane(incl - own, before);
       return true;
     }
-    carry = __builtin_amdgcn_readlane(incl, kWave - 1);
   }
   return false;
 }
@@ -75,6 +82,7 @@ __device__ __forceinline__ bool find_xcd_unit(const int32_t* offsets, int E, int
     }
     const int incl = wave_inclusive_scan(own);
     total += __builtin_amdgcn_readlane(incl, kWave - 1);
+    if ((uint32_t)total > kMaxUnits) return false;
     if (E <= kWave) {  // one pass finds it
       const int share = (total + 7) / 8;
       *t = xcd * share + place;

@@ -273,7 +273,7 @@ __global__ __launch_bounds__(256) void ragged_general_kernel(RaggedParams p) {
   int slot = 0;
   if (kMode == kWeightGrad && part > 0) {
     slot = slots_before(p.offsets, u.e, p.rows, p.chunk) + part - 1;
-    if (slot >= p.n_slots) return;
+    if ((uint32_t)slot >= (uint32_t)p.n_slots) return;
   }
   const int wave = threadIdx.x >> 6;
   const int wa = (wave >> 1) * 32 * W, wb = (wave & 1) * 32 * W;
@@ -386,6 +386,7 @@ __global__ __launch_bounds__(256) void ragged_add_slots_kernel(RaggedParams p) {
     }
     const int incl = wave_inclusive_scan(own) + before;
     before = __builtin_amdgcn_readlane(incl, kWave - 1);
+    if ((uint32_t)before > (uint32_t)p.n_slots) return;  // overlapping offsets
     uint64_t todo = __builtin_amdgcn_ballot_w64(own > 0);
     while (todo) {
       const int l = __builtin_ctzll(todo);
@@ -393,7 +394,7 @@ __global__ __launch_bounds__(256) void ragged_add_slots_kernel(RaggedParams p) {
       if (turn++ % gridDim.y != blockIdx.y) continue;
       const int last = __builtin_amdgcn_readlane(incl, l);
       const int first = last - __builtin_amdgcn_readlane(own, l);
-      const int count = (last < p.n_slots ? last : p.n_slots) - first;
+      const int count = last - first;
       vec_t* o = static_cast<vec_t*>(p.out) + (base + l) * n;
       const vec_t* s = reinterpret_cast<const vec_t*>(p.slots) + first * n;
       for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n;

@@ -264,6 +264,7 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(RingParams p) {
   __shared__ __attribute__((aligned(1024))) char slot2[kSlotBytes];
   __shared__ __attribute__((aligned(1024))) char slot3[kSlotBytes];
   __shared__ int32_t tiles_to[kRaggedMaxExperts];  // tiles of the experts up to e
+  __shared__ int32_t n_tiles;
   __shared__ int32_t first_row[kRaggedMaxExperts];
   __shared__ int32_t n_rows[kRaggedMaxExperts];
 
@@ -286,10 +287,12 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(RingParams p) {
         n_rows[base + lane] = rows;
       }
       carry = __builtin_amdgcn_readlane(incl, kWave - 1);
+      if ((uint32_t)carry > kMaxUnits) break;  // overlapping offsets: no tiles
     }
+    if (lane == 0) n_tiles = (uint32_t)carry > kMaxUnits ? 0 : carry;
   }
   __syncthreads();
-  const int total = __builtin_amdgcn_readfirstlane(tiles_to[p.E - 1]);
+  const int total = __builtin_amdgcn_readfirstlane(n_tiles);
 
   // XCD-contiguous walk: workgroup b runs on XCD b % 8.
   const int G = gridDim.x;
@@ -626,6 +629,7 @@ __global__ __launch_bounds__(256, 1) void wide_ring_kernel(RingParams p) {
   // scales of two slots: 16 bytes a row
   __shared__ __attribute__((aligned(1024))) char scales[kScaled ? 512 * 16 : 16];
   __shared__ int32_t tiles_to[kRaggedMaxExperts];  // tiles of the experts up to e
+  __shared__ int32_t n_tiles;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -641,10 +645,12 @@ __global__ __launch_bounds__(256, 1) void wide_ring_kernel(RingParams p) {
       const int incl = wave_inclusive_scan((rows + BM - 1) / BM * nt) + carry;
       if (base + lane < p.E) tiles_to[base + lane] = incl;
       carry = __builtin_amdgcn_readlane(incl, kWave - 1);
+      if ((uint32_t)carry > kMaxUnits) break;  // overlapping offsets: no tiles
     }
+    if (lane == 0) n_tiles = (uint32_t)carry > kMaxUnits ? 0 : carry;
   }
   __syncthreads();
-  const int total = __builtin_amdgcn_readfirstlane(tiles_to[p.E - 1]);
+  const int total = __builtin_amdgcn_readfirstlane(n_tiles);
 
   const int G = gridDim.x;
   int tile = (int)(blockIdx.x % 8) * (G / 8) + (int)(blockIdx.x / 8);
@@ -947,9 +953,6 @@ hipError_t choose(const RingParams& p, int num_cus, hipStream_t st) {
               small = cost(128, 64, 0.45f);
   const int grid = num_cus < 8 ? 8 : num_cus / 8 * 8;
   if (big <= medium && big <= small) {
-    // the transposed weights' loads read whole lines already: the narrow ring
-    // looks further ahead
-    if constexpr (kTransW) return launch<Op, Out, 4, 4, 1, kTransW>(p, grid, st);
     if (p.out_vec)
       hipLaunchKernelGGL((wide_ring_kernel<Op, Out, kTransW, true>), dim3((unsigned)grid),
                          dim3(256), 0, st, p);

@@ -120,7 +120,7 @@ __global__ __launch_bounds__(256, 1) void ragged_wgrad_kernel(WgradRingParams p)
   __shared__ int32_t order[kRaggedMaxExperts];      // experts by falling rows
   __shared__ int32_t blocks_to[kRaggedMaxExperts];  // blocks up to that place of the order
   __shared__ int32_t dealt[kDealt];                 // this group's among the first blocks
-  __shared__ int32_t n_dealt;
+  __shared__ int32_t n_dealt, n_blocks;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wa = wave & 1, wb = wave >> 1;  // this wavefront's 128 x 128 quarter
@@ -168,7 +168,9 @@ __global__ __launch_bounds__(256, 1) void ragged_wgrad_kernel(WgradRingParams p)
       }
       blocks = __builtin_amdgcn_readlane(incl, kWave - 1);
       slots = __builtin_amdgcn_readlane(sincl, kWave - 1);
+      if ((uint32_t)blocks > kMaxUnits) break;
     }
+    if ((uint32_t)blocks > kMaxUnits) blocks = 0;  // overlapping offsets: no jobs
     // the deal: lane g holds group g's work so far, in stages (a block's
     // store counts as eight)
     int mine = 0;
@@ -200,10 +202,13 @@ __global__ __launch_bounds__(256, 1) void ragged_wgrad_kernel(WgradRingParams p)
         }
       }
     }
-    if (lane == 0) n_dealt = mine;
+    if (lane == 0) {
+      n_dealt = mine;
+      n_blocks = blocks;
+    }
   }
   __syncthreads();
-  const int total = __builtin_amdgcn_readfirstlane(blocks_to[p.E - 1]);
+  const int total = __builtin_amdgcn_readfirstlane(n_blocks);
   const int mine = __builtin_amdgcn_readfirstlane(n_dealt);
   const int in_turn = groups < kDealt ? kDealt : 0;  // blocks from here on go in turn
 
@@ -247,7 +252,8 @@ __global__ __launch_bounds__(256, 1) void ragged_wgrad_kernel(WgradRingParams p)
   // piece. Chunk c of row r sits at c ^ 4 (r % 4): the transposing reads
   // then cover all banks. Columns past the matrix read the next row's (or
   // zeros past the last): they feed sums that are never stored. Rows past
-  // the chunk lie past the range and read as zeros.
+  // the chunk lie past the range and read as zeros. The range is checked by
+  // whole dwords, so an odd width is rounded up to one.
   const int op = wave >> 1;
   const uint32_t ld = (uint32_t)(op == 0 ? p.ldy : p.ldx);  // bytes
   const char* src = op == 0 ? p.dy : p.x;
@@ -267,7 +273,7 @@ __global__ __launch_bounds__(256, 1) void ragged_wgrad_kernel(WgradRingParams p)
     F.rs = __builtin_amdgcn_make_buffer_rsrc(
         (void*)(src + J.row * ld + (int64_t)col * 2), 0,
         J.cnt > 0 && col < width
-            ? (int)((uint32_t)(J.cnt - 1) * ld + (uint32_t)(width - col) * 2u)
+            ? (int)((uint32_t)(J.cnt - 1) * ld + (((uint32_t)(width - col) * 2u + 3u) & ~3u))
             : 0,
         kRsrcWord3);
     return F;
@@ -380,7 +386,7 @@ __global__ __launch_bounds__(256, 1) void ragged_wgrad_kernel(WgradRingParams p)
     asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
     if (J.part > 0) {
       const int slot = __builtin_amdgcn_readfirstlane(slots_to[J.e]) + J.part - 1;
-      if (slot >= p.n_slots) return;  // only if the offsets overlap
+      if ((uint32_t)slot >= (uint32_t)p.n_slots) return;  // overlapping offsets
       store_out(J, p.slots + (int64_t)slot * p.N * p.K, false, Policy<0>{});
     } else {
       store_out(J, p.dw + (int64_t)J.e * p.N * p.K, p.accumulate != 0, Policy<kNonTemporal>{});

@@ -613,3 +613,166 @@ def test_mxfp4_product_reads_no_scales_past_its_arrays(B, K):
     ref, s = R.product(off, torch.from_numpy(R.values_of(xc, xs)),
                        torch.from_numpy(R.values_of(wc, wsb)).view(1, N, K), rows)
     check(y, ref, R.sum_bound(ref, s, K, torch.float32), "y")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("N,K,ld_y,ld_x", [(777, 333, 784, 336), (65, 513, 72, 520),
+                                           (259, 261, 264, 264)])
+def test_odd_widths_in_aligned_rows(B, dt, N, K, ld_y, ld_x):
+    """Rows that start at 16 bytes and end at an odd element, in buffers that
+    end with the last row's last element."""
+    el, off = DT[dt], R.offsets_of([70, 0, 601, 30])
+    rows = int(off[-1])
+
+    def exact(rows, cols, ld, seed):
+        n = (rows - 1) * ld + cols
+        flat = torch.full((n,), float("nan"), dtype=el, device="cuda")
+        t = flat.as_strided((rows, cols), (ld, 1))
+        t.copy_(randn((rows, cols), el, seed))
+        return t
+
+    x, dy = exact(rows, K, ld_x, 1), exact(rows, N, ld_y, 2)
+    w = randn((4, N, K), el, 3, 0, K ** -0.5)
+    g = B.grouped(rows, 4, N, K, el, ld_x=ld_x, ld_y=ld_y)
+    ws = torch.empty(max(16, B.grouped_dw_workspace_size(g)), dtype=torch.uint8, device="cuda")
+    dw = torch.empty(4, N, K, device="cuda")
+    B.moe_grouped_gemm_dw(g, dev_off(off), x, dy, dw, ws)
+    ref, s = R.weight_grad(off, x, dy, 4)
+    check(dw, ref, R.sum_bound(ref, s, 601, torch.float32), "dw")
+    y, dx = exact(rows, N, ld_y, 4), exact(rows, K, ld_x, 5)
+    B.moe_grouped_gemm(g, dev_off(off), x, w, y)
+    ref, s = R.product(off, x, w, rows)
+    check(y, ref, R.sum_bound(ref, s, K, el), "y")
+    B.moe_grouped_gemm_dx(g, dev_off(off), dy, w, dx)
+    ref, s = R.product(off, dy, w, rows, transpose=True)
+    check(dx, ref, R.sum_bound(ref, s, N, el), "dx")
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("E,lo,hi", [(65, 0, 3), (200, 0, 40), (1024, 0, 9)])
+def test_many_experts(B, dt, E, lo, hi):
+    el, N, K = DT[dt], 192, 128
+    c = np.random.default_rng(E).integers(lo, hi, E)
+    c[[0, E // 2]] = 0
+    c[E - 1] = 300
+    off = R.offsets_of(c)
+    rows = int(off[-1])
+    x, dy = randn((rows, K), el, 1), randn((rows, N), el, 2)
+    w = randn((E, N, K), el, 3, 0, K ** -0.5)
+    g = B.grouped(rows, E, N, K, el)
+    d_off = dev_off(off)
+    y, dx = filled(rows, N, el, 0), filled(rows, K, el, 0)
+    dw = torch.full((E, N, K), float("nan"), device="cuda")
+    ws = torch.empty(max(16, B.grouped_dw_workspace_size(g)), dtype=torch.uint8, device="cuda")
+    B.moe_grouped_gemm(g, d_off, x, w, y)
+    B.moe_grouped_gemm_dx(g, d_off, dy, w, dx)
+    B.moe_grouped_gemm_dw(g, d_off, x, dy, dw, ws)
+    ref, s = R.product(off, x, w, rows)
+    check(y, ref, R.sum_bound(ref, s, K, el), "y")
+    ref, s = R.product(off, dy, w, rows, transpose=True)
+    check(dx, ref, R.sum_bound(ref, s, N, el), "dx")
+    ref, s = R.weight_grad(off, x, dy, E)
+    check(dw, ref, R.sum_bound(ref, s, 300, torch.float32), "dw")
+    xc, xs, xq, xsc = mx_operand(rows, K, 1, 3)
+    wc, wsb, wq, wsc = mx_operand(E * N, K, 2, 3)
+    B.moe_mxfp4_grouped_gemm(g, d_off, xq, xsc, wq, wsc, y)
+    ref, s = R.product(off, torch.from_numpy(R.values_of(xc, xs)),
+                       torch.from_numpy(R.values_of(wc, wsb)).view(E, N, K), rows)
+    check(y, ref, R.sum_bound(ref, s, K, el), "MXFP4 y")
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("rows", [1, 15, 16, 17, 31, 32, 33, 50])
+def test_one_expert_with_few_rows(B, dt, rows):
+    """Every split of a few rows into blocks of 16, at widths that end inside
+    a block and a K that ends inside a step and inside a scale group."""
+    el = DT[dt]
+    for N, K in [(40, 96), (264, 544), (1000, 2080)]:
+        off = R.offsets_of([0, rows, 0])
+        x, w = randn((rows, K), el, 1), randn((3, N, K), el, 2, 0, K ** -0.5)
+        w[0] = w[2] = float("nan")
+        g = B.grouped(rows, 3, N, K, el)
+        y = filled(rows, N, el, 0)
+        B.moe_grouped_gemm(g, dev_off(off), x, w, y)
+        ref, s = R.product(off, x, torch.nan_to_num(w.double()), rows)
+        check(y, ref, R.sum_bound(ref, s, K, el), (N, K))
+        xc, xs, xq, xsc = mx_operand(rows, K, 1, 3)
+        wc, wsb, wq, wsc = mx_operand(3 * N, K, 2, 3)
+        B.moe_mxfp4_grouped_gemm(g, dev_off(off), xq, xsc, wq, wsc, y)
+        ref, s = R.product(off, torch.from_numpy(R.values_of(xc, xs)),
+                           torch.from_numpy(R.values_of(wc, wsb)).view(3, N, K), rows)
+        check(y, ref, R.sum_bound(ref, s, K, el), ("MXFP4", N, K))
+
+
+def test_overlapping_offsets_on_a_large_buffer(B):
+    """Half of the experts claim all rows: far more tiles, chunks and slots than
+    the shape has. No result is promised; the calls stay inside their outputs."""
+    rows, E, N, K = 1 << 14, 1024, 64, 64
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[1::2] = rows
+    x = torch.zeros(rows, K, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(E, N, K, dtype=torch.bfloat16, device="cuda")
+    guard = torch.full((rows + 512, N), SENTINEL, dtype=torch.bfloat16, device="cuda")
+    y = guard[256:256 + rows]
+    g = B.grouped(rows, E, N, K, "bf16")
+    B.moe_grouped_gemm(g, off, x, w, y)
+    B.moe_grouped_gemm_dx(g, off, x, w, y)
+    dw = torch.full((E + 2, N, K), SENTINEL, device="cuda")
+    ws = torch.empty(B.grouped_dw_workspace_size(g), dtype=torch.uint8, device="cuda")
+    B.moe_grouped_gemm_dw(g, off, x, x, dw[1:1 + E], ws)
+    torch.cuda.synchronize()
+    assert (guard[:256] == SENTINEL).all() and (guard[256 + rows:] == SENTINEL).all()
+    assert (dw[0] == SENTINEL).all() and (dw[-1] == SENTINEL).all()
+
+
+def test_buffers_past_4_gib(B):
+    """Rows whose byte offsets pass 32 bits: products, gradients, SwiGLU and
+    quantisation, checked on rows at both ends."""
+    rows, E, N, K = 300_000, 3, 256, 8192
+    el = torch.bfloat16
+    off = R.offsets_of([5, rows - 135, 130])
+    x = torch.empty(rows, K, dtype=el, device="cuda")
+    for a in range(0, rows, 50_000):
+        x[a:a + 50_000] = randn((min(50_000, rows - a), K), el, a)
+    w = randn((E, N, K), el, 2, 0, K ** -0.5)
+    g, d_off = B.grouped(rows, E, N, K, el), dev_off(off)
+    y = torch.empty(rows, N, dtype=el, device="cuda")
+    B.moe_grouped_gemm(g, d_off, x, w, y)
+    pick = [0, 4, 5, 131_071, 131_072, 262_143, 262_144, rows - 131, rows - 130, rows - 1]
+    e_of = [0 if i < 5 else (1 if i < rows - 130 else 2) for i in pick]
+    for i, e in zip(pick, e_of):
+        ref, s = R.product(np.array([0, 1]), x[i:i + 1], w[e:e + 1], 1)
+        check(y[i:i + 1], ref, R.sum_bound(ref, s, K, el), i)
+    dx = torch.empty(rows, K, dtype=el, device="cuda")
+    B.moe_grouped_gemm_dx(g, d_off, y, w, dx)
+    for i, e in zip(pick, e_of):
+        ref, s = R.product(np.array([0, 1]), y[i:i + 1], w[e:e + 1], 1, transpose=True)
+        check(dx[i:i + 1], ref, R.sum_bound(ref, s, N, el), i)
+    # the last expert's rows are the buffer's end
+    ws = torch.empty(max(16, B.grouped_dw_workspace_size(g)), dtype=torch.uint8, device="cuda")
+    dw = torch.empty(E, N, K, device="cuda")
+    B.moe_grouped_gemm_dw(g, d_off, x, y, dw, ws)
+    last = R.offsets_of([130])
+    ref, s = R.weight_grad(last, x[-130:], y[-130:], 1)
+    check(dw[2:], ref, R.sum_bound(ref, s, 130, torch.float32), "dw")
+    # x as [g, u] of 4096 features each
+    h = torch.empty(rows, K // 2, dtype=el, device="cuda")
+    B.moe_swiglu(x, h)
+    B.moe_swiglu_backward(x, h, dx)
+    codes = torch.empty(rows, K // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(rows, K // 32, dtype=torch.uint8, device="cuda")
+    B.moe_mxfp4_quantize(x, codes, scales)
+    for i in pick:
+        gg, u = x[i, : K // 2].double().cpu(), x[i, K // 2:].double().cpu()
+        ref = gg * torch.sigmoid(gg) * u
+        check(h[i], ref, ref.abs() * 2.0 ** -20 + R.rounding(ref * (1 + 2.0 ** -20), el), i)
+        d = h[i].double().cpu()
+        ref = d * gg * torch.sigmoid(gg)
+        check(dx[i, K // 2:], ref, ref.abs() * 2.0 ** -20 + R.rounding(ref * (1 + 2.0 ** -20), el), i)
+        c, s = R.codes_of(x[i:i + 1].double().cpu().numpy())
+        assert np.array_equal(R.unpack(codes[i:i + 1].cpu().numpy()), c)
+        assert np.array_equal(scales[i:i + 1].cpu().numpy(), s)
+    B.moe_mxfp4_dequantize(codes, scales, dx)
+    for i in pick:
+        c, s = R.codes_of(x[i:i + 1].double().cpu().numpy())
+        assert torch.equal(dx[i:i + 1].double().cpu(), torch.from_numpy(R.values_of(c, s)))

@@ -153,6 +153,20 @@ __device__ __forceinline__ void mma_step(f32x16 (&acc)[WI][WJ], const Frags<WI, 
   }
 }
 
+// Row tile and feature tile of an expert's local tile, of mt x nt. An XCD
+// works on 32 consecutive tiles at a time; bands of up to eight row tiles,
+// walked feature by feature, make them about 8 x 4 (12 operand panels in its
+// L2) however many rows the expert has. (One expert of 16384 rows, 16384 x
+// 16384: bands of all 64 row tiles make it 32 x 1 and 33 panels.)
+__device__ __forceinline__ void place_tile(int local, int mt, int nt, int* m, int* n) {
+  const int bands = (mt + 7) / 8;
+  const int height = (mt + bands - 1) / bands;  // of a band; the last may be lower
+  const int band = local / (height * nt), in = local - band * (height * nt);
+  const int own = mt - band * height < height ? mt - band * height : height;
+  *n = in / own;
+  *m = band * height + in % own;
+}
+
 // Where a tile's operands live; uniform.
 template <int kScaleLoads>
 struct TileSrc {
@@ -315,8 +329,9 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(RingParams p) {
     const int mt = (T.m + BM - 1) / BM;
     const int local =
         t - (e > 0 ? __builtin_amdgcn_readfirstlane(tiles_to[e - 1]) : 0);
-    T.n0 = local / mt * BN;
-    T.m0 = local % mt * BM;
+    place_tile(local, mt, nt, &T.m0, &T.n0);
+    T.m0 *= BM;
+    T.n0 *= BN;
     return T;
   };
 
@@ -672,8 +687,9 @@ __global__ __launch_bounds__(256, 1) void wide_ring_kernel(RingParams p) {
     T.m = __builtin_amdgcn_readfirstlane(T.m);
     const int mt = (T.m + BM - 1) / BM;
     const int local = t - (e > 0 ? __builtin_amdgcn_readfirstlane(tiles_to[e - 1]) : 0);
-    T.n0 = local / mt * BN;
-    T.m0 = local % mt * BM;
+    place_tile(local, mt, nt, &T.m0, &T.n0);
+    T.m0 *= BM;
+    T.n0 *= BN;
     return T;
   };
 

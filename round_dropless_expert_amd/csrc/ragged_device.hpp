@@ -100,6 +100,21 @@ __device__ __forceinline__ bool find_xcd_unit(const int32_t* offsets, int E, int
   return place < share && find_unit(offsets, E, n, *t, units, out);
 }
 
+// Slots of the experts below e: an expert's chunks past its first.
+__device__ __forceinline__ int slots_before(const int32_t* offsets, int e, int n, int chunk) {
+  const int lane = threadIdx.x & 63;
+  int sum = 0;
+  for (int base = 0; base < e; base += kWave) {
+    int start, rows, own = 0;
+    if (base + lane < e) {
+      expert_rows(offsets, base + lane, n, &start, &rows);
+      own = rows > 0 ? (int)(((int64_t)rows + chunk - 1) / chunk) - 1 : 0;
+    }
+    sum += __builtin_amdgcn_readlane(wave_inclusive_scan(own), kWave - 1);
+  }
+  return sum;
+}
+
 // Rows that an elementwise call processes.
 __device__ __forceinline__ int64_t live_rows(int64_t rows, const int32_t* n_rows) {
   if (!n_rows) return rows;

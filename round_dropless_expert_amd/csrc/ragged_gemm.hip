@@ -194,21 +194,6 @@ struct Operand {
   }
 };
 
-// Slots of the experts below e: an expert's chunks past its first.
-__device__ __forceinline__ int slots_before(const int32_t* offsets, int e, int n, int chunk) {
-  const int lane = threadIdx.x & 63;
-  int sum = 0;
-  for (int base = 0; base < e; base += kWave) {
-    int start, rows, own = 0;
-    if (base + lane < e) {
-      expert_rows(offsets, base + lane, n, &start, &rows);
-      own = rows > 0 ? (int)(((int64_t)rows + chunk - 1) / chunk) - 1 : 0;
-    }
-    sum += __builtin_amdgcn_readlane(wave_inclusive_scan(own), kWave - 1);
-  }
-  return sum;
-}
-
 // General kernel: one workgroup per output tile of 64 W x 64 W, 2 x 2
 // wavefronts of W x W blocks of 32 x 32. Stages of 128 bytes of c go through
 // registers into two LDS buffers, the loads of the next two stages in flight

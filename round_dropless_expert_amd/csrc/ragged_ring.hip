@@ -24,69 +24,16 @@
 // Every output is one fixed sequence of MFMA steps over ascending c, so a
 // row's result does not depend on the tile, the tile's shape or the rows
 // around it.
-#include "ragged_device.hpp"
+#include "ragged_mma.hpp"
 #include "ragged_ring.hpp"
 
 namespace moe {
 namespace {
 
-typedef __attribute__((address_space(3))) char lds_char;
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kRsrcWord3 = 0x00020000;  // raw buffer
-constexpr int kNonTemporal = 2;
 constexpr int kSlots = 4;
 constexpr int kRowBytes = 64;  // bytes of c per row and stage
-// Past every buffer range (all below 2^31): loads return zeros, stores drop.
-constexpr uint32_t kOutOfRange = 0x80000000u;
-
-// LDS-direct loads of 16 or 4 bytes a lane: lane i's voff + soff of the
-// buffer to LDS at lds + size * i. In asm, so that the compiler neither
-// moves them nor waits on them: every wait is the kernel's own vmcnt count.
-// They have no register results.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void lds_load16(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff,
-                                           uint32_t soff, uint32_t lds) {
-  asm volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 0\n\t"
-      "buffer_load_dwordx4 %1, %2, %3 offen lds"
-      :
-      : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
-      : "m0");
-}
-__device__ __forceinline__ void lds_load4(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff,
-                                          uint32_t soff, uint32_t lds) {
-  asm volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 0\n\t"
-      "buffer_load_dword %1, %2, %3 offen lds"
-      :
-      : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
-      : "m0");
-}
-#pragma clang diagnostic pop
-
-// At most N of this wavefront's vector-memory operations outstanding, its
-// LDS reads done, then the workgroup barrier.
-template <int N>
-__device__ __forceinline__ void wait_vmem_barrier() {
-  static_assert(N >= 0 && N < 64, "vmcnt range");
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
-// An accumulator element, read from its AGPR at this point of the program.
-__device__ __forceinline__ float acc_read(float a) {
-  float v;
-  asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
-  return v;
-}
 
 // Operand kinds.
 struct OpBf16 {
@@ -173,78 +120,6 @@ struct TileSrc {
   __amdgpu_buffer_rsrc_t rw, ra;
   __amdgpu_buffer_rsrc_t rs[kScaleLoads > 0 ? kScaleLoads : 1];
 };
-
-// A wavefront's part of a tile's output: rows m0 .. of the expert's m (from
-// buffer row `start`), features n0 .. Lane (l32, half) holds, for token l32
-// of a 32-token block, features 8 q + 4 half + 0..3 of each 32-feature
-// block. The wavefront turns 32 tokens x 128 bytes of features around in 4
-// KiB of LDS and stores whole 128-byte row pieces. 16-byte chunk q of row r
-// sits at q ^ (r % 8), against bank conflicts. Non-temporal: the output is
-// next read when this launch has ended and should not displace operands in
-// L2. (The accumulators are read by asm: the caller gives the last MFMAs the
-// wait states that the compiler cannot see.)
-template <typename Out, int WI, int WJ, bool kOutVec>
-__device__ __forceinline__ void store_tile(const RingParams& p, const f32x16 (&acc)[WI][WJ],
-                                           char* stg, int start, int m, int n0, int m0, int wn,
-                                           int wm, int lane) {
-  constexpr int BN = 64 * WI, BM = 64 * WJ;
-  const int half = lane >> 5, l32 = lane & 31;
-
-  constexpr int kOs = sizeof(Out), kPerBlk = kOs == 2 ? 2 : 1;  // 32-feature blocks
-  const int mr = m - m0 < BM ? m - m0 : BM;
-  const uint32_t ldo = (uint32_t)p.ldo;
-  const __amdgpu_buffer_rsrc_t ro = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)(p.out + ((int64_t)start + m0) * p.ldo), 0,
-      (int)((uint32_t)(mr - 1) * ldo + (uint32_t)p.B * kOs), kRsrcWord3);
-  const int rrow = lane >> 3, rchunk = lane & 7;
-#pragma unroll
-  for (int jb = 0; jb < WJ; ++jb) {
-    const int row0 = wm * (BM / 2) + jb * 32;
-#pragma unroll
-    for (int ip = 0; ip < WI / kPerBlk; ++ip) {
-#pragma unroll
-      for (int u = 0; u < kPerBlk; ++u) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          typedef Out vec4_t __attribute__((ext_vector_type(4)));
-          vec4_t o;
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            o[v] = from_f32<Out>(acc_read(acc[kPerBlk * ip + u][jb][4 * q + v]));
-          if constexpr (kOs == 2) {
-            const int chunk = (u * 4 + q) ^ (l32 & 7);
-            *reinterpret_cast<u32x2*>(stg + l32 * 128 + chunk * 16 + half * 8) =
-                __builtin_bit_cast(u32x2, o);
-          } else {
-            const int chunk = (2 * q + half) ^ (l32 & 7);
-            *reinterpret_cast<u32x4*>(stg + l32 * 128 + chunk * 16) =
-                __builtin_bit_cast(u32x4, o);
-          }
-        }
-      }
-      const int feat = n0 + wn * (BN / 2) + ip * 32 * kPerBlk + rchunk * (16 / kOs);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + rrow;
-        const u32x4 v = *reinterpret_cast<const u32x4*>(
-            stg + r * 128 + ((rchunk ^ (r & 7)) * 16));
-        // rows past the expert's fall past the range
-        const uint32_t at = (uint32_t)(row0 + r) * ldo + (uint32_t)feat * kOs;
-        if constexpr (kOutVec) {
-          __builtin_amdgcn_raw_buffer_store_b128(v, ro, feat < p.B ? at : kOutOfRange, 0,
-                                                 kNonTemporal);
-        } else if (row0 + r < mr) {
-          Out* o = reinterpret_cast<Out*>(p.out + ((int64_t)start + m0) * p.ldo + at);
-          typedef Out vec_t __attribute__((ext_vector_type(16 / kOs)));
-          const vec_t e = __builtin_bit_cast(vec_t, v);
-#pragma unroll
-          for (int k = 0; k < 16 / kOs; ++k)
-            if (feat + k < p.B) o[k] = e[k];
-        }
-      }
-    }
-  }
-}
 
 template <typename Op, typename Out, int WI, int WJ, int SPB, bool kTransW, bool kOutVec>
 __global__ __launch_bounds__(256, 1) void ring_kernel(RingParams p) {
@@ -593,18 +468,15 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(RingParams p) {
     }
 #undef MOE_SLOT
 
-    // Epilogue. Lane (l32, half) holds, for token l32 of a 32-token block,
-    // features 8 q + 4 half + 0..3 of each 32-feature block. Each wavefront
-    // turns 32 tokens x 128 bytes of features around in its 4 KiB of slot 3
-    // (consumed by the last step; next filled after the barrier below) and
-    // stores whole 128-byte row pieces. 16-byte chunk q of row r sits at q ^
-    // (r % 8), against bank conflicts. Non-temporal: the output is next read
-    // when this launch has ended and should not displace operands in L2.
-    // (The accumulators are read by asm: give the last MFMAs the wait states
-    // that the compiler cannot see.)
+    // Epilogue, staged in slot 3 (consumed by the last step; next filled
+    // after the barrier below). Non-temporal: the output is next read when
+    // this launch has ended and should not displace operands in L2. (The
+    // accumulators are read by asm: the nops are the wait states the compiler
+    // cannot see.)
     asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
-    store_tile<Out, WI, WJ, kOutVec>(p, acc, slot3 + wave * 4096, T.start, T.m, T.n0, T.m0, wn, wm,
-                                     lane);
+    store_tile<Out, WI, WJ, kOutVec, false, kNonTemporal>(
+        acc, slot3 + wave * 4096, p.out + ((int64_t)T.start + T.m0) * p.ldo, (uint32_t)p.ldo,
+        T.m - T.m0 < BM ? T.m - T.m0 : BM, p.B, T.n0, wn, wm, lane);
     // every wavefront's staging reads are done before the next tile's ring
     // writes slot 3
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -924,8 +796,9 @@ __global__ __launch_bounds__(256, 1) void wide_ring_kernel(RingParams p) {
 
     // Epilogue, as the narrow ring's, through a staging area of its own.
     asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
-    store_tile<Out, WI, WJ, kOutVec>(p, acc, &staging[wave][0], T.start, T.m, T.n0, T.m0, wn, wm,
-                                     lane);
+    store_tile<Out, WI, WJ, kOutVec, false, kNonTemporal>(
+        acc, &staging[wave][0], p.out + ((int64_t)T.start + T.m0) * p.ldo, (uint32_t)p.ldo,
+        T.m - T.m0 < BM ? T.m - T.m0 : BM, p.B, T.n0, wn, wm, lane);
     if (!has_next) break;
     read_first();
     tile = tile_n;

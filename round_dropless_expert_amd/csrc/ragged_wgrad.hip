@@ -24,7 +24,7 @@
 // An expert with more rows than a chunk is summed in several tiles; those
 // past the first go to slots of the workspace and a second launch adds them
 // in chunk order.
-#include "ragged_device.hpp"
+#include "ragged_mma.hpp"
 #include "ragged_ring.hpp"
 
 namespace moe {
@@ -36,44 +36,6 @@ constexpr int kOpBytes = kStageRows * kTile * 2;  // one operand's stage
 constexpr int kSlotBytes = 2 * kOpBytes;          // dy, then x
 constexpr int kSlots = 4;
 constexpr int kLoads = kSlotBytes / (256 * 16);  // 16-byte loads per thread and stage
-constexpr int kRsrcWord3 = 0x00020000;
-constexpr uint32_t kOutOfRange = 0x80000000u;
-
-typedef __attribute__((address_space(3))) char lds_char;
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-
-// LDS-direct load: lane i's 16 bytes at voff + soff to LDS at lds + 16 i. In
-// asm: the compiler neither moves nor waits on it, every wait is the
-// kernel's own vmcnt count. No register results.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void lds_load16(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff,
-                                           uint32_t soff, uint32_t lds) {
-  asm volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 0\n\t"
-      "buffer_load_dwordx4 %1, %2, %3 offen lds"
-      :
-      : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
-      : "m0");
-}
-#pragma clang diagnostic pop
-
-template <int N>
-__device__ __forceinline__ void wait_vmem_barrier() {
-  static_assert(N >= 0 && N < 64, "vmcnt range");
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
-__device__ __forceinline__ float acc_read(float a) {
-  float v;
-  asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
-  return v;
-}
-
 template <typename T>
 __device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
   if constexpr (__is_same(T, bf16))
@@ -104,19 +66,14 @@ __device__ __forceinline__ uint32_t wave_min(uint32_t v) {
 
 constexpr int kDealt = 64;
 
-// Cache policy of a buffer store.
-constexpr int kNonTemporal = 2;
-template <int kValue>
-struct Policy {
-  static constexpr int value = kValue;
-};
-
-template <typename T>
+// kVec: rows of dw are 16-byte aligned and hold whole 16-byte chunks.
+template <typename T, bool kVec>
 __global__ __launch_bounds__(256, 1) void ragged_wgrad_kernel(WgradRingParams p) {
   __shared__ __attribute__((aligned(1024))) char lds[kSlots][kSlotBytes];
-  __shared__ int32_t first_row[kRaggedMaxExperts];
-  __shared__ int32_t n_rows[kRaggedMaxExperts];
-  __shared__ int32_t slots_to[kRaggedMaxExperts];   // slots of the experts below e
+  // 4 KiB a wavefront for its tile's store; while the deal is worked out,
+  // the experts' rows
+  __shared__ __attribute__((aligned(1024))) char staging[4][4096];
+  int32_t* const n_rows = reinterpret_cast<int32_t*>(&staging[0][0]);
   __shared__ int32_t order[kRaggedMaxExperts];      // experts by falling rows
   __shared__ int32_t blocks_to[kRaggedMaxExperts];  // blocks up to that place of the order
   __shared__ int32_t dealt[kDealt];                 // this group's among the first blocks
@@ -124,14 +81,12 @@ __global__ __launch_bounds__(256, 1) void ragged_wgrad_kernel(WgradRingParams p)
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wa = wave & 1, wb = wave >> 1;  // this wavefront's 128 x 128 quarter
-  const int l32 = lane & 31, half = lane >> 5;
 
   const int ta = (p.N + kTile - 1) / kTile, tb = (p.K + kTile - 1) / kTile;
   const int per = ta * tb;
   for (int e = tid; e < p.E; e += 256) {
     int start, rows;
     expert_rows(p.offsets, e, p.rows, &start, &rows);
-    first_row[e] = start;
     n_rows[e] = rows;
   }
   __syncthreads();
@@ -154,20 +109,13 @@ __global__ __launch_bounds__(256, 1) void ragged_wgrad_kernel(WgradRingParams p)
     return n == 0 && !p.accumulate ? 1 : n;  // without rows: its zeros are stored
   };
   if (wave == 0) {
-    int blocks = 0, slots = 0;
+    int blocks = 0;
     for (int base = 0; base < p.E; base += kWave) {
       const int i = base + lane;
       const int jobs = i < p.E ? parts_of(n_rows[order[i]]) : 0;
-      const int extra = i < p.E ? parts_of(n_rows[i]) - 1 : 0;
       const int incl = wave_inclusive_scan(jobs * per_blocks) + blocks;
-      const int own = extra > 0 ? extra : 0;
-      const int sincl = wave_inclusive_scan(own) + slots;
-      if (i < p.E) {
-        blocks_to[i] = incl;
-        slots_to[i] = sincl - own;
-      }
+      if (i < p.E) blocks_to[i] = incl;
       blocks = __builtin_amdgcn_readlane(incl, kWave - 1);
-      slots = __builtin_amdgcn_readlane(sincl, kWave - 1);
       if ((uint32_t)blocks > kMaxUnits) break;
     }
     if ((uint32_t)blocks > kMaxUnits) blocks = 0;  // overlapping offsets: no jobs
@@ -235,7 +183,10 @@ __global__ __launch_bounds__(256, 1) void ragged_wgrad_kernel(WgradRingParams p)
     }
     const int local = t - (i > 0 ? __builtin_amdgcn_readfirstlane(blocks_to[i - 1]) : 0);
     const int e = __builtin_amdgcn_readfirstlane(order[i]);
-    const int rows = __builtin_amdgcn_readfirstlane(n_rows[e]);
+    int start, rows;
+    expert_rows(p.offsets, e, p.rows, &start, &rows);
+    start = __builtin_amdgcn_readfirstlane(start);
+    rows = __builtin_amdgcn_readfirstlane(rows);
     const int tile = local % per_blocks * p.group + member;
     J->e = e;
     J->part = local / per_blocks;
@@ -243,7 +194,7 @@ __global__ __launch_bounds__(256, 1) void ragged_wgrad_kernel(WgradRingParams p)
     J->b0 = tile % tb * kTile;
     const int left = rows - J->part * p.chunk;
     J->cnt = tile < per ? (left < p.chunk ? left : p.chunk) : -1;
-    J->row = (int64_t)__builtin_amdgcn_readfirstlane(first_row[e]) + (int64_t)J->part * p.chunk;
+    J->row = (int64_t)start + (int64_t)J->part * p.chunk;
     return true;
   };
 
@@ -315,7 +266,7 @@ __global__ __launch_bounds__(256, 1) void ragged_wgrad_kernel(WgradRingParams p)
     return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
 
-  f32x16 acc[4][4];  // [k block][n block]
+  f32x16 acc[4][4];  // [k block][n block]: lanes are rows n
   u32x4 fb0[4], fa0[4], fb1[4], fa1[4];
   // in the order the MFMAs first use them
   auto read_one = [&](u32x4 (&fb)[4], u32x4 (&fa)[4], int slot, int ks, int x) {
@@ -331,65 +282,36 @@ __global__ __launch_bounds__(256, 1) void ragged_wgrad_kernel(WgradRingParams p)
 #pragma unroll
     for (int n = 0; n < 16; ++n) {
       const int i = n / 4, j = n % 4;
-      acc[i][j] = mma<T>(fa[j], fb[i], acc[i][j]);
+      acc[i][j] = mma<T>(fb[i], fa[j], acc[i][j]);
 #pragma unroll
       for (int x = n * kOps / 16; x < (n + 1) * kOps / 16; ++x) op_(x);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
 
-  // Lane: k = column l32 of a block, n = rows 8 (v / 4) + 4 half + v % 4:
-  // every store writes two 128-byte row pieces.
-  const uint32_t rowb = (uint32_t)p.K * 4u;
-  auto store_out = [&](const Tile& J, float* out, bool add, auto policy) {
-    constexpr int kPolicy = decltype(policy)::value;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int ab = J.a0 + wa * 128 + j * 32;
-      if (ab >= p.N) continue;
-      const int an = p.N - ab < 32 ? p.N - ab : 32;
-      const __amdgpu_buffer_rsrc_t ro = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(out + (int64_t)ab * p.K), 0, (int)((uint32_t)an * rowb), kRsrcWord3);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int b = J.b0 + wb * 128 + i * 32 + l32;
-        const uint32_t vo_o =
-            b < p.K ? (uint32_t)(4 * half) * rowb + (uint32_t)b * 4u : kOutOfRange;
-        auto so = [&](int v) { return (int)((uint32_t)(8 * (v / 4) + v % 4) * rowb); };
-        if (add) {
-          float o[16];
-#pragma unroll
-          for (int v = 0; v < 16; ++v)
-            o[v] = __builtin_bit_cast(
-                float, __builtin_amdgcn_raw_buffer_load_b32(ro, (int)vo_o, so(v), 0));
-#pragma unroll
-          for (int v = 0; v < 16; ++v)
-            __builtin_amdgcn_raw_buffer_store_b32(
-                __builtin_bit_cast(uint32_t, acc_read(acc[i][j][v]) + o[v]), ro, (int)vo_o, so(v),
-                kPolicy);
-        } else {
-#pragma unroll
-          for (int v = 0; v < 16; ++v)
-            __builtin_amdgcn_raw_buffer_store_b32(
-                __builtin_bit_cast(uint32_t, acc_read(acc[i][j][v])), ro, (int)vo_o, so(v),
-                kPolicy);
-        }
-      }
-    }
-  };
   // dw is next read when the backward has ended: non-temporal, so that its
   // lines do not displace operands in L2 (balanced gate/up, both gradients:
-  // 599 -> 584 us). Slots, and the chunk they are added to, are read again
-  // by the next launch. (The accumulators are read by asm: the nops are the
-  // wait states the compiler cannot see.)
+  // 599 -> 584 us). Slots are read again by the next launch. (The
+  // accumulators are read by asm: the nops are the wait states the compiler
+  // cannot see.)
   auto epilogue = [&](const Tile& J) {
     asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+    const int mr = p.N - J.a0 < kTile ? p.N - J.a0 : kTile;
+    const uint32_t ldo = (uint32_t)p.K * 4u;
+    char* stg = &staging[wave][0];
+    float* dw = p.dw + ((int64_t)J.e * p.N + J.a0) * p.K;
     if (J.part > 0) {
-      const int slot = __builtin_amdgcn_readfirstlane(slots_to[J.e]) + J.part - 1;
+      const int slot = slots_before(p.offsets, J.e, p.rows, p.chunk) + J.part - 1;
       if ((uint32_t)slot >= (uint32_t)p.n_slots) return;  // overlapping offsets
-      store_out(J, p.slots + (int64_t)slot * p.N * p.K, false, Policy<0>{});
+      float* out = p.slots + ((int64_t)slot * p.N + J.a0) * p.K;
+      store_tile<float, 4, 4, kVec, false, 0>(acc, stg, (char*)out, ldo, mr, p.K, J.b0, wb, wa,
+                                              lane);
+    } else if (p.accumulate) {
+      store_tile<float, 4, 4, kVec, true, kNonTemporal>(acc, stg, (char*)dw, ldo, mr, p.K, J.b0,
+                                                        wb, wa, lane);
     } else {
-      store_out(J, p.dw + (int64_t)J.e * p.N * p.K, p.accumulate != 0, Policy<kNonTemporal>{});
+      store_tile<float, 4, 4, kVec, false, kNonTemporal>(acc, stg, (char*)dw, ldo, mr, p.K, J.b0,
+                                                         wb, wa, lane);
     }
   };
 
@@ -452,10 +374,15 @@ hipError_t launch_wgrad_ring(bool is_bf16, const WgradRingParams& params, int nu
   const int tiles = ((p.N + kTile - 1) / kTile) * ((p.K + kTile - 1) / kTile);
   for (p.group = 32; p.group > 1; p.group /= 2)
     if ((tiles + p.group - 1) / p.group * p.group * 8 <= tiles * 9 && grid / 8 % p.group == 0) break;
-  if (is_bf16)
-    hipLaunchKernelGGL((ragged_wgrad_kernel<bf16>), dim3(grid), dim3(256), 0, st, p);
+  const bool vec = p.K % 4 == 0 && (reinterpret_cast<uintptr_t>(p.dw) & 15) == 0;
+  if (is_bf16 && vec)
+    hipLaunchKernelGGL((ragged_wgrad_kernel<bf16, true>), dim3(grid), dim3(256), 0, st, p);
+  else if (is_bf16)
+    hipLaunchKernelGGL((ragged_wgrad_kernel<bf16, false>), dim3(grid), dim3(256), 0, st, p);
+  else if (vec)
+    hipLaunchKernelGGL((ragged_wgrad_kernel<f16, true>), dim3(grid), dim3(256), 0, st, p);
   else
-    hipLaunchKernelGGL((ragged_wgrad_kernel<f16>), dim3(grid), dim3(256), 0, st, p);
+    hipLaunchKernelGGL((ragged_wgrad_kernel<f16, false>), dim3(grid), dim3(256), 0, st, p);
   return hipGetLastError();
 }
 

@@ -515,6 +515,8 @@ _get_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 def _call_stream(stream, dev):
     if stream is None and _get_raw_stream is not None:
         return _get_raw_stream(dev)
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
+        raise ValueError(f"stream: on {stream.device}, the current device is cuda:{dev}")
     return _stream(stream)
 
 

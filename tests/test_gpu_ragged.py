@@ -179,6 +179,22 @@ def test_weight_gradient_over_many_chunks(B, dt):
     ref, s = R.weight_grad(off, x, dy, 4)
     check(dw, ref, R.sum_bound(ref, s, 8000, torch.float32), "dw")
     assert (dw[1] == 0).all()
+    # added to what is there, at an address that is only four-byte aligned
+    buf = torch.full((4 * N * K + 1,), 2.0, device="cuda")
+    dw2 = buf[1:].view(4, N, K)
+    B.moe_grouped_gemm_dw(g, dev_off(off), x, dy, dw2, ws, accumulate=True)
+    check(dw2, ref + 2, R.sum_bound(ref + 2, s + 2, 8001, torch.float32), "dw added")
+    assert buf[0] == 2.0 and (dw2[1] == 2.0).all()
+    # a width that ends inside 16 bytes, and too small a workspace
+    g3 = B.grouped(rows, 4, N, 190, el, ld_x=K)
+    ws3 = torch.empty(B.grouped_dw_workspace_size(g3), dtype=torch.uint8, device="cuda")
+    dw3 = torch.empty(4, N, 190, device="cuda")
+    B.moe_grouped_gemm_dw(g3, dev_off(off), x[:, :190], dy, dw3, ws3)
+    check(dw3, ref[:, :, :190], R.sum_bound(ref, s, 8000, torch.float32)[:, :, :190], "dw narrow")
+    with pytest.raises(B.MoeError):
+        B.moe_grouped_gemm_dw(g, dev_off(off), x, dy, dw, ws[:-1])
+    with pytest.raises(B.MoeError):
+        B.moe_grouped_gemm_dw(g, dev_off(off), x, dy, dw)
 
 
 def test_no_rows(B):
@@ -200,11 +216,15 @@ def test_no_rows(B):
     B.moe_mxfp4_dequantize(q, q, torch.empty(0, 32, device="cuda"))
 
 
-@pytest.mark.parametrize("raw", [[-5, 3, 2, 9], [0, 100, 100, 100], [9, 4, 0, -1]])
-def test_wrong_offsets_stay_inside_the_buffers(B, raw):
+@pytest.mark.parametrize("rows,N,K,raw", [
+    (8, 64, 64, [-5, 3, 2, 9]), (8, 64, 64, [0, 100, 100, 100]), (8, 64, 64, [9, 4, 0, -1]),
+    (8, 64, 64, [-(2 ** 31), 2 ** 31 - 1, -(2 ** 31), 2 ** 31 - 1]),
+    (2000, 512, 512, [0, 2000, 0, 2000]), (2000, 512, 512, [2000, 0, 1500, 100]),
+    (2000, 512, 512, [-7, 5000, 3, 1999])])
+def test_wrong_offsets_stay_inside_the_buffers(B, rows, N, K, raw):
     """Offsets outside [0, rows] or out of order: no result is promised, but
     nothing outside the outputs is written (guard rows around them)."""
-    rows, N, K, E = 8, 64, 64, 3
+    E = 3
     off = torch.tensor(raw, dtype=torch.int32, device="cuda")
     x, w = randn((rows, K), torch.bfloat16, 1), randn((E, N, K), torch.bfloat16, 2)
     buf = torch.full((rows + 512, N), SENTINEL, dtype=torch.bfloat16, device="cuda")
@@ -214,8 +234,13 @@ def test_wrong_offsets_stay_inside_the_buffers(B, raw):
     B.moe_grouped_gemm_dx(g, off, x, w, y)
     assert (buf[:256] == SENTINEL).all() and (buf[256 + rows:] == SENTINEL).all()
     dw = torch.full((E + 2, N, K), SENTINEL, device="cuda")
-    B.moe_grouped_gemm_dw(g, off, x, x, dw[1:1 + E])
+    ws = torch.empty(B.grouped_dw_workspace_size(g), dtype=torch.uint8, device="cuda")
+    B.moe_grouped_gemm_dw(g, off, x, x, dw[1:1 + E], ws)
     assert (dw[0] == SENTINEL).all() and (dw[-1] == SENTINEL).all()
+    _, _, xq, xsc = mx_operand(rows, K, 1)
+    _, _, wq, wsc = mx_operand(E * N, K, 2)
+    B.moe_mxfp4_grouped_gemm(g, off, xq, xsc, wq, wsc, y)
+    assert (buf[:256] == SENTINEL).all() and (buf[256 + rows:] == SENTINEL).all()
 
 
 @pytest.mark.parametrize("dt", list(DT))
@@ -429,6 +454,9 @@ def test_streams_and_graph_replays(B):
     w1, w2 = randn((E, N, K), el, 1, 0, K ** -0.5), randn((E, K, f), el, 2, 0, f ** -0.5)
     mk = lambda n, dt=el: torch.zeros(rows, n, dtype=dt, device="cuda")
     S = B.mxfp4_scale_stride(K)
+    u8 = lambda *n: torch.zeros(*n, dtype=torch.uint8, device="cuda")
+    w1q, w1s = u8(E, N, K // 2), u8(E, N, S)
+    B.moe_mxfp4_quantize(w1.contiguous(), w1q, w1s)
 
     def bufs():
         return dict(x=mk(K), off=torch.zeros(E + 1, dtype=torch.int32, device="cuda"), gu=mk(N),
@@ -437,7 +465,8 @@ def test_streams_and_graph_replays(B):
                     ws=torch.zeros(max(1, B.grouped_dw_workspace_size(g1)), dtype=torch.uint8,
                                    device="cuda"),
                     q=torch.zeros(rows, K // 2, dtype=torch.uint8, device="cuda"),
-                    s=torch.zeros(rows, S, dtype=torch.uint8, device="cuda"), v=mk(K))
+                    s=torch.zeros(rows, S, dtype=torch.uint8, device="cuda"), v=mk(K),
+                    gu4=mk(N))
 
     def run(b):
         B.moe_grouped_gemm(g1, b["off"], b["x"], w1, b["gu"])
@@ -449,6 +478,7 @@ def test_streams_and_graph_replays(B):
         B.moe_grouped_gemm_dw(g1, b["off"], b["x"], b["dgu"], b["dw"], b["ws"])
         B.moe_mxfp4_quantize(b["y"], b["q"], b["s"], n_rows=b["off"][E:])
         B.moe_mxfp4_dequantize(b["q"], b["s"], b["v"], n_rows=b["off"][E:])
+        B.moe_mxfp4_grouped_gemm(g1, b["off"], b["q"], b["s"], w1q, w1s, b["gu4"])
 
     def fill(b, seed, counts):
         b["x"].copy_(randn((rows, K), el, seed))
@@ -464,7 +494,7 @@ def test_streams_and_graph_replays(B):
     torch.cuda.synchronize()
     with torch.cuda.graph(graph, stream=st):
         run(cap)
-    outs = ("gu", "h", "y", "dh", "dgu", "dx", "dw", "q", "s", "v")
+    outs = ("gu", "h", "y", "dh", "dgu", "dx", "dw", "q", "s", "v", "gu4")
     for seed, counts in ((2, [700, 0, 0, 0]), (3, [0, 0, 1, 0]), (4, [0, 0, 0, 0]),
                          (5, [5, 600, 5, 90])):
         for b in (cap, eager):
@@ -776,3 +806,51 @@ def test_buffers_past_4_gib(B):
     for i in pick:
         c, s = R.codes_of(x[i:i + 1].double().cpu().numpy())
         assert torch.equal(dx[i:i + 1].double().cpu(), torch.from_numpy(R.values_of(c, s)))
+
+
+def test_calls_on_a_given_stream_wait_for_it(B):
+    """stream= is where the work goes: it sees what was queued there before."""
+    st = torch.cuda.Stream()
+    x = torch.zeros(4096, 512, device="cuda")
+    y = torch.zeros(4096, 256, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(20_000_000)
+        x.fill_(1.0)
+    B.moe_swiglu(x, y, stream=st)
+    st.synchronize()
+    assert torch.allclose(y, torch.full_like(y, 1 / (1 + np.exp(-1.0))))
+    B.moe_swiglu(x, y, stream=st.cuda_stream)
+    st.synchronize()
+
+
+def test_wrong_tensors_are_refused(B):
+    el = torch.bfloat16
+    g = B.grouped(8, 2, 16, 32, el)
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    x, w = torch.zeros(8, 32, dtype=el, device="cuda"), torch.zeros(2, 16, 32, dtype=el, device="cuda")
+    y = torch.zeros(8, 16, dtype=el, device="cuda")
+    bad = [(off.long(), x, w, y), (off[:2], x, w, y), (off.cpu(), x, w, y), (off, x.float(), w, y),
+           (off, x[:7], w, y), (off, x[:, :16], w, y), (off, x.t(), w, y), (off, x, w[:1], y),
+           (off, x, w.transpose(1, 2), y), (off, x, w, y[:, :8]), (off, x, w, x),
+           (off, x[:1].expand(8, 32), w, y)]
+    for a in bad:
+        with pytest.raises(ValueError):
+            B.moe_grouped_gemm(g, *a)
+    with pytest.raises(ValueError):
+        B.moe_swiglu(x, y[:, :8])
+    with pytest.raises(ValueError):
+        B.moe_swiglu(x, y.float())
+    with pytest.raises(ValueError):
+        B.moe_swiglu(x, y[:1].expand(8, 16))
+    with pytest.raises(ValueError):
+        B.moe_mxfp4_quantize(x.int(), off, off)
+    u8 = torch.zeros(8, 16, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError):
+        B.moe_mxfp4_quantize(x, u8, u8[:1])
+    with pytest.raises(ValueError):
+        B.moe_mxfp4_quantize(x, u8, u8, index=off.long())
+    with pytest.raises(B.MoeError):
+        B.moe_mxfp4_quantize(x, u8, u8, index=off, index_div=0)
+    with pytest.raises(ValueError):
+        B.moe_mxfp4_quantize(x[:, :16], u8, u8)

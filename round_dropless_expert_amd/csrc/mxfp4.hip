@@ -13,7 +13,7 @@
 namespace moe {
 namespace {
 
-constexpr int kUnroll = 4;  // 16-byte vectors a lane has in flight
+constexpr int kUnroll = 8;  // 16-byte vectors a lane has in flight (581 us with 4, 557 with 8: below)
 
 // gfx950 converts two values at a time to and from the 4-bit format with a
 // scale (an fp32 power of two, of which it uses the exponent): to nearest,
@@ -242,7 +242,7 @@ __global__ __launch_bounds__(256) void mx_dequantize_kernel(DequantParams p) {
           for (int k = 0; k < V; ++k) y.t[k] = from_f32<T>(__builtin_nanf(""));
         }
         if constexpr (kVec)
-          *reinterpret_cast<u32x4*>(out + (int64_t)v * V) = y.v;
+          __builtin_nontemporal_store(y.v, reinterpret_cast<u32x4*>(out + (int64_t)v * V));
         else
           __builtin_memcpy(out + (int64_t)v * V, &y.v, 16);
       }

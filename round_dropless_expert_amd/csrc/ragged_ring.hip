@@ -809,12 +809,20 @@ __global__ __launch_bounds__(256, 1) void wide_ring_kernel(RingParams p) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
-// Mean rows of an expert up to which a product with few tiles goes to the
-// skinny kernel. One expert of 4096 x 4096 bf16, skinny against ring: 16 rows
-// 15 and 30 us, 32 rows 20 and 30 us, 64 rows 36 and 31 us. With a tile for
-// every CU the ring is the faster for single rows too (eight experts of 4096
-// x 1536, a row each: 17 against 24 us).
-constexpr int kSkinnyRows = 32;
+// Products that go to the skinny kernel: fewer tiles of the ring's smallest
+// shape than CUs, and at most 32 rows a (mean) expert or two of the skinny
+// kernel's 32 x 16 blocks a CU. Skinny against ring, bf16, one expert: 4096 x
+// 4096, a row 8.6 and 30 us, 32 rows 15 and 30, 64 rows (512 blocks) 20 and
+// 31, 128 rows (1024 blocks) 38 and 27; 1024 x 4096, 256 rows (512 blocks) 17
+// and 26. With a tile for every CU the ring is the faster for single rows too
+// (eight experts of 4096 x 1536, a row each: 17 against 24 us).
+bool skinny_takes(const RingParams& p, int num_cus) {
+  const int64_t active = p.rows < p.E ? p.rows : p.E;
+  const int64_t mean = (p.rows + active - 1) / active;
+  return active * ((mean + 63) / 64) * ((p.B + 127) / 128) < num_cus &&
+         (mean <= 32 ||
+          active * ((mean + 31) / 32) * ((p.B + 15) / 16) <= 2 * (int64_t)num_cus);
+}
 
 template <typename Op, typename Out, int WI, int WJ, int SPB, bool kTransW>
 hipError_t launch(const RingParams& p, int grid, hipStream_t st) {
@@ -857,11 +865,8 @@ hipError_t choose(const RingParams& p, int num_cus, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_ring(RingKind kind, const RingParams& p, int num_cus, hipStream_t st) {
-  const int64_t active = p.rows < p.E ? p.rows : p.E;
-  // Few rows, and fewer tiles of the ring's smallest shape than CUs: what
-  // counts is that every CU reads weights.
   if (kind != RingKind::kInputGradBF16 && kind != RingKind::kInputGradF16 &&
-      p.rows <= kSkinnyRows * active && active * ((p.B + 127) / 128) < num_cus)
+      skinny_takes(p, num_cus))
     return launch_skinny(kind, p, num_cus, st);
   switch (kind) {
     case RingKind::kForwardBF16: return choose<OpBf16, bf16, false>(p, num_cus, st);

@@ -13,7 +13,9 @@
 namespace moe {
 namespace {
 
-constexpr int kUnroll = 8;  // 16-byte vectors a lane has in flight (581 us with 4, 557 with 8: below)
+// 16-byte vectors a lane has in flight. 98304 rows of 7168 bf16, to 4 bits and
+// back: 581 us with 4, 557 with 8.
+constexpr int kUnroll = 8;
 
 // gfx950 converts two values at a time to and from the 4-bit format with a
 // scale (an fp32 power of two, of which it uses the exponent): to nearest,
@@ -127,6 +129,10 @@ struct QuantParams {
 // are 16-byte aligned), 32 / V neighbours a block: their maximum is exchanged
 // by DPP, and each stores V / 2 bytes of codes. kUnroll vectors of a row are
 // in flight per lane.
+//
+// Bound by memory: 98304 rows of 7168 bf16 gathered from 16384 tokens, 240 us
+// (1.41 GB asked for and 0.37 GB stored, 7.4 TB/s: a token's later reads come
+// from the caches).
 template <typename T, bool kVec>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(QuantParams p) {
   constexpr int V = 16 / sizeof(T);
@@ -197,6 +203,9 @@ struct DequantParams {
   int log_lanes;
 };
 
+// The inverse: a lane reads V / 2 bytes of codes and stores 16 bytes of
+// values, past the caches. Bound by the stores: 98304 rows of 7168 bf16, 317
+// us (0.37 GB read, 1.41 GB stored, 5.6 TB/s).
 template <typename T, bool kVec>
 __global__ __launch_bounds__(256) void mx_dequantize_kernel(DequantParams p) {
   constexpr int V = 16 / sizeof(T);

@@ -66,10 +66,11 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 // 16 bytes of a row of which `n` elements exist (n may be <= 0), the rest
-// zero. The address need only be aligned to an element: gfx950 loads 16
-// bytes from any address.
+// zero. `room`: if there are fewer than 16 bytes, so many more lie before
+// `at` in the row, and one load ending at the last element serves. The address
+// need only be aligned to an element: gfx950 loads 16 bytes from any address.
 template <typename T>
-__device__ __forceinline__ u32x4 load16(const T* at, int n) {
+__device__ __forceinline__ u32x4 load16(const T* at, int n, bool room) {
   constexpr int kV = 16 / sizeof(T);
   union {
     T e[kV];
@@ -78,6 +79,14 @@ __device__ __forceinline__ u32x4 load16(const T* at, int n) {
   r.v = u32x4{0, 0, 0, 0};
   if (n >= kV) {
     __builtin_memcpy(&r.v, at, 16);
+    return r.v;
+  }
+  if (n <= 0) return r.v;
+  if (room) {
+    unsigned __int128 w;
+    __builtin_memcpy(&w, at - (kV - n), 16);
+    w >>= (kV - n) * 8 * (int)sizeof(T);
+    __builtin_memcpy(&r.v, &w, 16);
     return r.v;
   }
 #pragma unroll
@@ -113,11 +122,14 @@ struct Operand {
   // matrix's last row does not have.
   int64_t at[kPieces];
   bool whole;
+  bool room;  // down: a row has 16 bytes up to the tile's last column
 
-  __device__ __forceinline__ void set(const T* b, int64_t l, int e) {
+  // `before`: rows of the output index before the tile's
+  __device__ __forceinline__ void set(const T* b, int64_t l, int e, int before) {
     base = b;
     ld = l;
     ext = e;
+    room = before + e >= kV;
     whole = kAlong || ext >= kExt || ext % kV == 0;
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
@@ -145,11 +157,11 @@ struct Operand {
       const int id = (int)threadIdx.x + 256 * u;
       if constexpr (kAlong) {
         const int row = id / kChunks, c = c0 + (id % kChunks) * kV;
-        reg[u] = load16(base + row * ld + c, row < ext ? c_end - c : 0);
+        reg[u] = load16(base + row * ld + c, row < ext ? c_end - c : 0, c_end >= kV);
       } else {
         constexpr int kPer = kExt * kEs / 16;
         const int c = c0 + id / kPer, row = (id % kPer) * kV;
-        reg[u] = load16(base + c * ld + row, c < c_end ? ext - row : 0);
+        reg[u] = load16(base + c * ld + row, c < c_end ? ext - row : 0, room);
       }
     }
   }
@@ -198,13 +210,16 @@ struct Operand {
 // wavefronts of W x W blocks of 32 x 32. Stages of 128 bytes of c go through
 // registers into two LDS buffers, the loads of the next two stages in flight
 // while one is multiplied. Takes every size, stride and element alignment.
-// The whole stages run without a bounds check; the last, partial one is loaded
-// element by element where it has to be. 32768 rows, N = K = 2049, 8 experts,
-// fp16: 540 us, 510 TFLOP/s (64-byte stages 608 us, one stage ahead 659 us);
-// what bounds it is LDS, which the 64 x 64 wavefront tiles read 1 KiB of per
-// 32 x 32 x 16 product, and the barrier of each stage.
+// The whole stages run without a bounds check; the partial one goes first and
+// shifts what it loads at the ends of rows. 32768 rows, N = K = 2049, 8
+// experts, fp16: 495 us, 555 TFLOP/s (with 64-byte stages or one stage ahead
+// 10-20% more); what bounds it is LDS, which the 64 x 64 wavefront tiles read 1
+// KiB of per 32 x 32 x 16 product, and the barrier of each stage. 5002 rows, N
+// = 777, K = 1111, fp16: 31 us (35 with the partial stage last and its ends
+// loaded an element at a time); there rows that start at any 2 bytes cost the
+// loads (K = 1104: 25 us).
 template <typename T, int kMode, int W>
-__global__ __launch_bounds__(256) void ragged_general_kernel(RaggedParams p) {
+__global__ __launch_bounds__(256, W == 2 ? 2 : 4) void ragged_general_kernel(RaggedParams p) {
   constexpr int kTile = 64 * W;
   constexpr bool kPAlong = kMode != kWeightGrad;
   constexpr bool kQAlong = kMode == kForward;
@@ -240,17 +255,17 @@ __global__ __launch_bounds__(256) void ragged_general_kernel(RaggedParams p) {
     c_begin = part * p.chunk;
     c_end = u.rows - c_begin < p.chunk ? u.rows : c_begin + p.chunk;
     a_ext = p.A - a0;
-    P.set(static_cast<const T*>(p.p) + (int64_t)u.start * p.ldp + a0, p.ldp, a_ext);
-    Q.set(static_cast<const T*>(p.q) + (int64_t)u.start * p.ldq + b0, p.ldq, p.B - b0);
+    P.set(static_cast<const T*>(p.p) + (int64_t)u.start * p.ldp + a0, p.ldp, a_ext, a0);
+    Q.set(static_cast<const T*>(p.q) + (int64_t)u.start * p.ldq + b0, p.ldq, p.B - b0, b0);
   } else {
     a0 = local / p.tiles_b * kTile;
     b0 = local % p.tiles_b * kTile;
     c_end = p.C;
     a_ext = u.rows - a0;
-    P.set(static_cast<const T*>(p.p) + ((int64_t)u.start + a0) * p.ldp, p.ldp, a_ext);
+    P.set(static_cast<const T*>(p.p) + ((int64_t)u.start + a0) * p.ldp, p.ldp, a_ext, a0);
     Q.set(static_cast<const T*>(p.q) + (int64_t)u.e * p.B * p.C +
               (kMode == kForward ? (int64_t)b0 * p.ldq : (int64_t)b0),
-          p.ldq, p.B - b0);
+          p.ldq, p.B - b0, b0);
   }
 
   // weight gradient: the slot of this chunk (past the last one only if the
@@ -284,12 +299,18 @@ __global__ __launch_bounds__(256) void ragged_general_kernel(RaggedParams p) {
         for (int j = 0; j < W; ++j) acc[i][j] = Mma<T>::mma(fa[i], fb[j], acc[i][j]);
     }
   };
-  // the whole stages; the rest is at most one more
+  // the whole stages; the rest is at most one more, which goes first, so that
+  // its loads are as far ahead as the others'
   const int count = c_end - c_begin;
   int whole = count / kCk;
   if (!(P.whole && Q.whole) && whole > 0 && whole * kCk == count) --whole;
+  const int rest = whole * kCk < count ? 1 : 0, stages = whole + rest;
   typename P_t::regs_t p0, p1;
   typename Q_t::regs_t q0, q1;
+  auto load = [&](int i, typename P_t::regs_t& rp, typename Q_t::regs_t& rq) {
+    P.load(rp, c_begin + (i - rest) * kCk);
+    Q.load(rq, c_begin + (i - rest) * kCk);
+  };
   // stage i from its registers into LDS buffer i % 2, the loads of stage i +
   // kAhead into them, and its products. The buffer's last readers passed the
   // barrier of the stage between.
@@ -297,32 +318,19 @@ __global__ __launch_bounds__(256) void ragged_general_kernel(RaggedParams p) {
     P_t::store(rp, lds[buf]);
     Q_t::store(rq, lds[buf] + P_t::kBytes);
     __syncthreads();
-    if (i + kAhead < whole) {
-      P.load(rp, c_begin + (i + kAhead) * kCk);
-      Q.load(rq, c_begin + (i + kAhead) * kCk);
-    }
+    if (i + kAhead < stages) load(i + kAhead, rp, rq);
     multiply(lds[buf]);
   };
-  if (whole > 0) {
-    P.load(p0, c_begin);
-    Q.load(q0, c_begin);
-  }
-  if (whole > 1) {
-    P.load(p1, c_begin + kCk);
-    Q.load(q1, c_begin + kCk);
-  }
-  for (int i = 0; i < whole; i += 2) {
-    stage(i, 0, p0, q0);
-    if (i + 1 < whole) stage(i + 1, 1, p1, q1);
-  }
-  if (whole * kCk < count) {
+  if (rest) {
     P.load_some(p0, c_begin + whole * kCk, c_end);
     Q.load_some(q0, c_begin + whole * kCk, c_end);
-    char* buf = lds[whole & 1];
-    P_t::store(p0, buf);
-    Q_t::store(q0, buf + P_t::kBytes);
-    __syncthreads();
-    multiply(buf);
+  } else if (whole > 0) {
+    load(0, p0, q0);
+  }
+  if (stages > 1) load(1, p1, q1);
+  for (int i = 0; i < stages; i += 2) {
+    stage(i, 0, p0, q0);
+    if (i + 1 < stages) stage(i + 1, 1, p1, q1);
   }
 
   // lane: column b = l % 32 of a block, rows a = 8 (v / 4) + 4 (l / 32) + v % 4

@@ -8,6 +8,13 @@
 // and operand: 16x16x32 for 16-bit types, 16x16x128 for MXFP4) and their sums
 // are joined in LDS, in wavefront order: the order of the sum is fixed. A
 // batch's loads are issued while the one before is multiplied.
+//
+// Splitting K over the wavefronts makes four times as many loads in flight as
+// one wavefront a tile would, and row blocks are workgroups of their own: the
+// weights come from the L2 after the first. One token through four of 32
+// experts, N = K = 2048, bf16: 8.4 us for 33.6 MB (4.0 TB/s; 7.6 us, 4.4 TB/s
+// back to back), of which about 3 us are the launch. One expert of 64 rows,
+// N = K = 4096: 20 us bf16, 8 us MXFP4.
 #include "ragged_device.hpp"
 #include "ragged_ring.hpp"
 

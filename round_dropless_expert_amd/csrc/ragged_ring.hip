@@ -511,10 +511,10 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(RingParams p) {
 // steps (1024 MFMA cycles) and more to land.
 //
 // 98304 rows over 64 experts, N = 4096, K = 7168: bf16 4.59 ms, 1.26 PFLOP/s,
-// MFMA pipes busy 76% of the cycles at 1.5 GHz (of 2.4: the chip's power
-// limit); MXFP4 1.44 ms, 4.0 PFLOP/s, busy 60% at 1.6 GHz, the rest waits for
-// a slot's loads (95 requests to the L2 of 128 bytes per thousand cycles and
-// CU). The same on 64-byte stages in four slots: 5.01 and 2.02 ms. Input
+// MFMA pipes busy 76% of the cycles at 1.7 GHz (of 2.4: the chip's power
+// limit); MXFP4 1.44 ms, 4.0 PFLOP/s, busy 60% at 1.7 GHz, the rest waits for
+// a slot's loads (1.4e8 requests to the L2: one a CU every 4.6 cycles). The
+// same on 64-byte stages in four slots: 5.01 and 2.02 ms. Input
 // gradient, 32768 rows over 32 experts, N = K = 2048, bf16: 264 us, 1.04
 // PFLOP/s.
 template <typename Op, typename Out, bool kTransW, bool kOutVec>

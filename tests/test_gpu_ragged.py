@@ -854,3 +854,44 @@ def test_wrong_tensors_are_refused(B):
         B.moe_mxfp4_quantize(x, u8, u8, index=off, index_div=0)
     with pytest.raises(ValueError):
         B.moe_mxfp4_quantize(x[:, :16], u8, u8)
+
+
+# around 16 bytes and a 128-byte stage of every type, where the ends of rows
+# are loaded in another way than the rest
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("N,K", [(2, 3), (3, 9), (9, 2), (8, 7), (33, 31), (65, 71), (66, 130),
+                                 (129, 63), (135, 129), (5, 1031)])
+def test_widths_around_vectors_and_stages(B, dt, N, K):
+    el, c = DT[dt], [70, 0, 1, 131, 8]
+    off = R.offsets_of(c, 1)
+    rows, E, nan = int(off[-1]) + 2, len(c), float("nan")
+
+    def framed(shape, seed, scale=1.0):  # NaN around every row and matrix
+        n = int(np.prod(shape))
+        flat = torch.full((n + 64,), nan, dtype=el, device="cuda")
+        t = flat[33:33 + n].view(shape)
+        t.copy_(randn((n // shape[-1], shape[-1]), el, seed, 0, scale).view(shape))
+        return t
+
+    def rows_of(width, seed):  # behind every row, and before it, NaN
+        t = torch.full((rows, width + 11), nan, dtype=el, device="cuda")[:, 5:5 + width]
+        t[1:int(off[-1])] = randn((int(off[-1]) - 1, width), el, seed)
+        return t
+
+    x, dy, w = rows_of(K, 1), rows_of(N, 2), framed((E, N, K), 3, K ** -0.5)
+    g = B.grouped(rows, E, N, K, el, ld_x=K + 11, ld_y=N + 11)
+    d_off, live = dev_off(off), slice(1, int(off[-1]))
+    y, dx = filled(rows, N, el, 11), filled(rows, K, el, 11)
+    dw = torch.empty(E, N, K, device="cuda")
+    ws = torch.empty(B.grouped_dw_workspace_size(g), dtype=torch.uint8, device="cuda")
+    B.moe_grouped_gemm(g, d_off, x, w, y)
+    B.moe_grouped_gemm_dx(g, d_off, dy, w, dx)
+    B.moe_grouped_gemm_dw(g, d_off, x, dy, dw, ws)
+    ref, s = R.product(off, x, w, rows)
+    check(y[live], ref[live], R.sum_bound(ref, s, K, el)[live], "y")
+    ref, s = R.product(off, dy, w, rows, transpose=True)
+    check(dx[live], ref[live], R.sum_bound(ref, s, N, el)[live], "dx")
+    ref, s = R.weight_grad(off, x, dy, E)
+    check(dw, ref, R.sum_bound(ref, s, max(c), torch.float32), "dw")
+    for t in (y, dx):
+        assert (t[0] == SENTINEL).all() and (t[int(off[-1]):] == SENTINEL).all()

@@ -33,12 +33,13 @@ struct RaggedParams {
   int tiles_a;   // weight gradient: tiles along a
 };
 
-// One MFMA step of a type: 32 x 32 outputs, lane l supplies row l % 32.
+// One step of a type over 32 bytes of c: 32 x 32 outputs, lane l supplies row
+// l % 32 and 16 bytes of c, the first half of the step's for l < 32.
 template <typename T>
 struct Mma;
+constexpr int kStepBytes = 32;
 template <>
 struct Mma<bf16> {
-  static constexpr int kStepBytes = 32;  // of c
   typedef bf16x8 frag_t;
   __device__ static __forceinline__ f32x16 mma(frag_t a, frag_t b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
@@ -46,7 +47,6 @@ struct Mma<bf16> {
 };
 template <>
 struct Mma<f16> {
-  static constexpr int kStepBytes = 32;
   typedef f16x8 frag_t;
   __device__ static __forceinline__ f32x16 mma(frag_t a, frag_t b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
@@ -54,10 +54,13 @@ struct Mma<f16> {
 };
 template <>
 struct Mma<float> {
-  static constexpr int kStepBytes = 8;
-  typedef float frag_t;
+  typedef f32x4 frag_t;
+  // instruction i takes c = i and 4 + i: a lane's values then are 16 adjacent
+  // bytes, one LDS read where c lies along the row
   __device__ static __forceinline__ f32x16 mma(frag_t a, frag_t b, f32x16 c) {
-    return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, c, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
+    return c;
   }
 };
 
@@ -184,12 +187,16 @@ struct Operand {
                                                                  int s) {
     const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5;
     typedef typename Mma<T>::frag_t frag_t;
-    if constexpr (kEs == 4) {
-      const int c = 2 * s + half;
-      return kAlong ? *reinterpret_cast<const float*>(lds + (row0 + l32) * kPitch + c * 4)
-                    : *reinterpret_cast<const float*>(lds + c * kPitch + (row0 + l32) * 4);
-    } else if constexpr (kAlong) {
-      return *reinterpret_cast<const frag_t*>(lds + (row0 + l32) * kPitch + s * 32 + half * 16);
+    if constexpr (kAlong) {
+      return *reinterpret_cast<const frag_t*>(lds + (row0 + l32) * kPitch + s * kStepBytes +
+                                              half * 16);
+    } else if constexpr (kEs == 4) {
+      frag_t f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        f[i] = *reinterpret_cast<const float*>(lds + (8 * s + 4 * half + i) * kPitch +
+                                               (row0 + l32) * 4);
+      return f;
     } else {
       // transposing LDS read: in each group of 16 lanes, lane i receives
       // 16-bit element i % 4 of the 8 bytes addressed by lanes 4 j + i / 4,
@@ -287,7 +294,7 @@ __global__ __launch_bounds__(256, W == 2 ? 2 : 4) void ragged_general_kernel(Rag
 
   auto multiply = [&](const char* buf) {
 #pragma unroll
-    for (int s = 0; s < kStage / Mma<T>::kStepBytes; ++s) {
+    for (int s = 0; s < kStage / kStepBytes; ++s) {
       typename Mma<T>::frag_t fa[W], fb[W];
 #pragma unroll
       for (int i = 0; i < W; ++i) fa[i] = P_t::frag(buf, wa + 32 * i, s);

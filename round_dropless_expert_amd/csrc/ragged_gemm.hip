@@ -98,13 +98,12 @@ __device__ __forceinline__ u32x4 load16(const T* at, int n, bool room) {
   return r.v;
 }
 
-constexpr int kStage = 128;  // bytes of c
 constexpr int kAhead = 2;    // stages of loads in flight
 
 // One operand's share of a stage: `kExt` rows of its output index by kStage
 // bytes of c. Along: one LDS row per row, 16 bytes of padding. Down: one LDS
 // row per c, kExt elements and 16 bytes of padding.
-template <typename T, bool kAlong, int kExt>
+template <typename T, bool kAlong, int kExt, int kStage>
 struct Operand {
   static constexpr int kEs = sizeof(T);
   static constexpr int kV = 16 / kEs;
@@ -213,8 +212,8 @@ struct Operand {
   }
 };
 
-// General kernel: one workgroup per output tile of 64 W x 64 W, 2 x 2
-// wavefronts of W x W blocks of 32 x 32. Stages of 128 bytes of c go through
+// General kernel: one workgroup per output tile, of 128 x 128 or 64 x 64 with 2
+// x 2 wavefronts of W x W blocks of 32 x 32. Stages of 128 bytes of c go through
 // registers into two LDS buffers, the loads of the next two stages in flight
 // while one is multiplied. Takes every size, stride and element alignment.
 // The whole stages run without a bounds check; the partial one goes first and
@@ -225,13 +224,19 @@ struct Operand {
 // = 777, K = 1111, fp16: 31 us (35 with the partial stage last and its ends
 // loaded an element at a time); there rows that start at any 2 bytes cost the
 // loads (K = 1104: 25 us).
-template <typename T, int kMode, int W>
-__global__ __launch_bounds__(256, W == 2 ? 2 : 4) void ragged_general_kernel(RaggedParams p) {
-  constexpr int kTile = 64 * W;
+//
+// Where there are few outputs a tile is 32 x 32, so that more CUs have one, and
+// its four wavefronts share c: each takes every fourth step of a stage (of
+// 512 bytes), and their sums are joined in LDS, in wavefront order.
+template <typename T, int kMode, int kTile>
+__global__ __launch_bounds__(256, kTile == 64 ? 4 : 2) void ragged_general_kernel(RaggedParams p) {
+  constexpr bool kSplit = kTile == 32;
+  constexpr int W = kSplit ? 1 : kTile / 64;
+  constexpr int kStage = kSplit ? 512 : 128;  // bytes of c
   constexpr bool kPAlong = kMode != kWeightGrad;
   constexpr bool kQAlong = kMode == kForward;
-  typedef Operand<T, kPAlong, kTile> P_t;
-  typedef Operand<T, kQAlong, kTile> Q_t;
+  typedef Operand<T, kPAlong, kTile, kStage> P_t;
+  typedef Operand<T, kQAlong, kTile, kStage> Q_t;
   constexpr int kCk = P_t::kCk;
   __shared__ __attribute__((aligned(16))) char lds[2][P_t::kBytes + Q_t::kBytes];
 
@@ -283,7 +288,7 @@ __global__ __launch_bounds__(256, W == 2 ? 2 : 4) void ragged_general_kernel(Rag
     if ((uint32_t)slot >= (uint32_t)p.n_slots) return;
   }
   const int wave = threadIdx.x >> 6;
-  const int wa = (wave >> 1) * 32 * W, wb = (wave & 1) * 32 * W;
+  const int wa = kSplit ? 0 : (wave >> 1) * 32 * W, wb = kSplit ? 0 : (wave & 1) * 32 * W;
   f32x16 acc[W][W];
 #pragma unroll
   for (int i = 0; i < W; ++i)
@@ -292,18 +297,25 @@ __global__ __launch_bounds__(256, W == 2 ? 2 : 4) void ragged_general_kernel(Rag
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
 
+  auto step = [&](const char* buf, int s) {
+    typename Mma<T>::frag_t fa[W], fb[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) fa[i] = P_t::frag(buf, wa + 32 * i, s);
+#pragma unroll
+    for (int j = 0; j < W; ++j) fb[j] = Q_t::frag(buf + P_t::kBytes, wb + 32 * j, s);
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+#pragma unroll
+      for (int j = 0; j < W; ++j) acc[i][j] = Mma<T>::mma(fa[i], fb[j], acc[i][j]);
+  };
+  constexpr int kSteps = kStage / kStepBytes;
   auto multiply = [&](const char* buf) {
+    if constexpr (kSplit) {
 #pragma unroll
-    for (int s = 0; s < kStage / kStepBytes; ++s) {
-      typename Mma<T>::frag_t fa[W], fb[W];
+      for (int s = 0; s < kSteps; s += 4) step(buf, s + wave);
+    } else {
 #pragma unroll
-      for (int i = 0; i < W; ++i) fa[i] = P_t::frag(buf, wa + 32 * i, s);
-#pragma unroll
-      for (int j = 0; j < W; ++j) fb[j] = Q_t::frag(buf + P_t::kBytes, wb + 32 * j, s);
-#pragma unroll
-      for (int i = 0; i < W; ++i)
-#pragma unroll
-        for (int j = 0; j < W; ++j) acc[i][j] = Mma<T>::mma(fa[i], fb[j], acc[i][j]);
+      for (int s = 0; s < kSteps; ++s) step(buf, s);
     }
   };
   // the whole stages; the rest is at most one more, which goes first, so that
@@ -342,27 +354,45 @@ __global__ __launch_bounds__(256, W == 2 ? 2 : 4) void ragged_general_kernel(Rag
 
   // lane: column b = l % 32 of a block, rows a = 8 (v / 4) + 4 (l / 32) + v % 4
   const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5;
+  auto put = [&](int da, int b, float r) {
+    if (da >= a_ext) return;
+    if constexpr (kMode == kWeightGrad) {
+      if (part == 0) {
+        float* o = static_cast<float*>(p.out) + ((int64_t)u.e * p.A + a0 + da) * p.B + b;
+        *o = p.accumulate ? *o + r : r;
+      } else {
+        p.slots[((int64_t)slot * p.A + a0 + da) * p.B + b] = r;
+      }
+    } else {
+      static_cast<T*>(p.out)[((int64_t)u.start + a0 + da) * p.ldo + b] = from_f32<T>(r);
+    }
+  };
+  if constexpr (kSplit) {
+    // wavefront w joins and stores rows 8 w .. 8 w + 7: values 4 w .. 4 w + 3
+    float(*joined)[16][64] = reinterpret_cast<float(*)[16][64]>(&lds[0][0]);
+    static_assert(sizeof(lds) >= 4 * 16 * 64 * 4, "");
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < W; ++i) {
+    for (int v = 0; v < 16; ++v) joined[wave][v][lane] = acc[0][0][v];
+    __syncthreads();
+    if (b0 + l32 >= p.B) return;
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-      const int b = b0 + wb + 32 * j + l32;
-      if (b >= p.B) continue;
+    for (int v = 0; v < 4; ++v) {
+      float r = 0.f;
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int da = wa + 32 * i + 8 * (v >> 2) + 4 * half + (v & 3);
-        if (da >= a_ext) continue;
-        const float r = acc[i][j][v];
-        if constexpr (kMode == kWeightGrad) {
-          if (part == 0) {
-            float* o = static_cast<float*>(p.out) + ((int64_t)u.e * p.A + a0 + da) * p.B + b;
-            *o = p.accumulate ? *o + r : r;
-          } else {
-            p.slots[((int64_t)slot * p.A + a0 + da) * p.B + b] = r;
-          }
-        } else {
-          static_cast<T*>(p.out)[((int64_t)u.start + a0 + da) * p.ldo + b] = from_f32<T>(r);
-        }
+      for (int w = 0; w < 4; ++w) r += joined[w][4 * wave + v][lane];
+      put(8 * wave + 4 * half + v, b0 + l32, r);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        const int b = b0 + wb + 32 * j + l32;
+        if (b >= p.B) continue;
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          put(wa + 32 * i + 8 * (v >> 2) + 4 * half + (v & 3), b, acc[i][j][v]);
       }
     }
   }
@@ -411,8 +441,12 @@ __global__ __launch_bounds__(256) void ragged_add_slots_kernel(RaggedParams p) {
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 // Tile of the general kernel: 128 x 128 unless the outputs are too few to
-// give every CU two.
-constexpr int kLargeJobs = 2;
+// give every CU two; 32 x 32 where all tiles run at once (two fit a CU).
+// 32 x 32 against 64 x 64: fp32, 1024 rows of 4 experts, N = 256, K = 2047
+// (288 tiles of 32 x 32) 30 and 48 us, 846 rows of one expert, N = 128, K =
+// 2496 (108) 21 and 54; fp16, 300 rows of 4, N = 2001, K = 1500 (819) 20 and
+// 16, 64 rows of 4, N = 512, K = 511 (96) 7 and 7.
+constexpr int kLargeJobs = 2, kSmallJobs = 2;
 template <typename T, int kMode>
 hipError_t launch_general(RaggedParams p, int num_cus, hipStream_t st) {
   auto jobs = [&](int tile) -> int64_t {
@@ -426,13 +460,19 @@ hipError_t launch_general(RaggedParams p, int num_cus, hipStream_t st) {
   // (rounded up to whole turns over the XCDs)
   const int64_t large = (jobs(128) + 7) / 8 * 8;
   if (large >= kLargeJobs * (int64_t)num_cus) {
-    hipLaunchKernelGGL((ragged_general_kernel<T, kMode, 2>),
-                       dim3((unsigned)large), dim3(256), 0, st, p);
-  } else {
-    const int64_t small = (jobs(64) + 7) / 8 * 8;
-    hipLaunchKernelGGL((ragged_general_kernel<T, kMode, 1>), dim3((unsigned)small), dim3(256),
+    hipLaunchKernelGGL((ragged_general_kernel<T, kMode, 128>), dim3((unsigned)large), dim3(256),
                        0, st, p);
+    return hipGetLastError();
   }
+  const int64_t small = (jobs(32) + 7) / 8 * 8;
+  if (small <= kSmallJobs * (int64_t)num_cus) {
+    hipLaunchKernelGGL((ragged_general_kernel<T, kMode, 32>), dim3((unsigned)small), dim3(256),
+                       0, st, p);
+    return hipGetLastError();
+  }
+  const int64_t medium = (jobs(64) + 7) / 8 * 8;
+  hipLaunchKernelGGL((ragged_general_kernel<T, kMode, 64>), dim3((unsigned)medium), dim3(256), 0,
+                     st, p);
   return hipGetLastError();
 }
 

@@ -895,3 +895,31 @@ def test_widths_around_vectors_and_stages(B, dt, N, K):
     check(dw, ref, R.sum_bound(ref, s, max(c), torch.float32), "dw")
     for t in (y, dx):
         assert (t[0] == SENTINEL).all() and (t[int(off[-1]):] == SENTINEL).all()
+
+
+# few outputs with long sums, where a tile's wavefronts share the sum
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("N,K", [(40, 1031), (1031, 40), (129, 4095), (32, 128), (33, 127)])
+def test_few_outputs_with_long_sums(B, dt, N, K):
+    el, c = DT[dt], [3, 33, 0, 300]
+    off = R.offsets_of(c, 2)
+    rows, E = int(off[-1]) + 1, len(c)
+    x, dy = randn((rows, K), el, 1, 3), randn((rows, N), el, 2, 3)
+    w = randn((E, N, K), el, 3, 0, K ** -0.5)
+    g = B.grouped(rows, E, N, K, el, ld_x=K + 3, ld_y=N + 3)
+    d_off, live = dev_off(off), slice(2, int(off[-1]))
+    y, dx = filled(rows, N, el, 3), filled(rows, K, el, 3)
+    dw = randn((E, N, K), torch.float32, 4)
+    was = dw.double().cpu()
+    ws = torch.empty(B.grouped_dw_workspace_size(g), dtype=torch.uint8, device="cuda")
+    B.moe_grouped_gemm(g, d_off, x, w, y)
+    B.moe_grouped_gemm_dx(g, d_off, dy, w, dx)
+    B.moe_grouped_gemm_dw(g, d_off, x, dy, dw, ws, accumulate=True)
+    ref, s = R.product(off, x, w, rows)
+    check(y[live], ref[live], R.sum_bound(ref, s, K, el)[live], "y")
+    ref, s = R.product(off, dy, w, rows, transpose=True)
+    check(dx[live], ref[live], R.sum_bound(ref, s, N, el)[live], "dx")
+    ref, s = R.weight_grad(off, x, dy, E)
+    check(dw, ref + was, R.sum_bound(ref + was, s + was.abs(), max(c) + 1, torch.float32), "dw")
+    for t in (y, dx):
+        assert (t[:2] == SENTINEL).all() and (t[int(off[-1]):] == SENTINEL).all()

@@ -125,9 +125,19 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[WI][WJ], char* st
                                                  kPolicy);
         } else if (row0 + r < mr) {
           Out* o = reinterpret_cast<Out*>(out + at);
+          if (col + kChunk <= B) {
+            // gfx950 stores 16 bytes to any address
+            if constexpr (kAdd) {
+              vec_t was;
+              __builtin_memcpy(&was, o, 16);
+              v += was;
+            }
+            __builtin_memcpy(o, &v, 16);
+          } else {
 #pragma unroll
-          for (int k = 0; k < kChunk; ++k)
-            if (col + k < B) o[k] = kAdd ? o[k] + v[k] : v[k];
+            for (int k = 0; k < kChunk; ++k)
+              if (col + k < B) o[k] = kAdd ? o[k] + v[k] : v[k];
+          }
         }
       }
     }

@@ -599,8 +599,15 @@ hipError_t launch_ragged_dw(const RaggedShape& s, const int32_t* offsets, const 
   p.n_slots = (int)split.slots;
   p.accumulate = accumulate ? 1 : 0;
   hipError_t e;
-  if (s.type != ElemType::kF32 && s.rows > 0 && s.ld_x % 8 == 0 && s.ld_y % 8 == 0 &&
-      aligned16(x) && aligned16(dy)) {
+  // The ring where it has a 256 x 256 tile for every CU (at the mean rows of an
+  // expert); fewer go to the general kernel's smaller ones. bf16, ring against
+  // general: 16384 rows, E 64, N = K = 512 (256 tiles) 27 and 32 us, E 4 (128)
+  // 45 and 34, 4096 rows, E 8, N = K = 1024 (128) 32 and 26, 2792 rows, E 4,
+  // N = 448, K = 128 (10) 23 and 11.
+  const int64_t chunks = s.rows / split.chunk;
+  const int64_t tiles = (chunks > s.E ? chunks : s.E) * ceil_div(s.N, 256) * ceil_div(s.K, 256);
+  if (s.type != ElemType::kF32 && s.rows > 0 && tiles >= num_cus && s.ld_x % 8 == 0 &&
+      s.ld_y % 8 == 0 && aligned16(x) && aligned16(dy)) {
     const WgradRingParams r{static_cast<const char*>(dy), static_cast<const char*>(x), dw, slots,
                             offsets, s.ld_y * 2, s.ld_x * 2, (int)s.rows, s.E, s.N, s.K,
                             p.chunk, p.n_slots, p.accumulate, 1};

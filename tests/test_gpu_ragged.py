@@ -923,3 +923,55 @@ def test_few_outputs_with_long_sums(B, dt, N, K):
     check(dw, ref + was, R.sum_bound(ref + was, s + was.abs(), max(c) + 1, torch.float32), "dw")
     for t in (y, dx):
         assert (t[:2] == SENTINEL).all() and (t[int(off[-1]):] == SENTINEL).all()
+
+
+# a 256 x 256 tile for every CU: the weight gradient's ring
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("E,hi,N,K,ld_y,ld_x", [
+    (64, 40, 520, 264, 520, 264), (130, 5, 264, 72, 272, 72), (4, 700, 2048, 2048, 2048, 2056),
+    (60, 33, 777, 333, 784, 336), (300, 3, 65, 130, 72, 136), (5, 1, 1921, 2050, 1928, 2056)])
+def test_weight_gradient_with_many_tiles(B, dt, E, hi, N, K, ld_y, ld_x):
+    el = DT[dt]
+    c = np.random.default_rng(E + hi).integers(0, hi + 1, E).tolist()
+    c[E // 2] = 0
+    off = R.offsets_of(c, 3)
+    rows, nan = int(off[-1]) + 5, float("nan")
+    x, dy = randn((rows, K), el, 1, ld_x - K), randn((rows, N), el, 2, ld_y - N)
+    for t in (x, dy):
+        t[:3] = nan
+        t[int(off[-1]):] = nan
+    g = B.grouped(rows, E, N, K, el, ld_x=ld_x, ld_y=ld_y)
+    ws = torch.full((B.grouped_dw_workspace_size(g),), 255, dtype=torch.uint8, device="cuda")
+    dw = torch.full((E, N, K), nan, device="cuda")
+    B.moe_grouped_gemm_dw(g, dev_off(off), x, dy, dw, ws)
+    ref, s = R.weight_grad(off, x, dy, E)
+    bound = R.sum_bound(ref, s, max(c), torch.float32)
+    check(dw, ref, bound, "dw")
+    dw0 = dw.clone()
+    B.moe_grouped_gemm_dw(g, dev_off(off), x, dy, dw, ws, accumulate=True)
+    check(dw, 2 * ref, R.sum_bound(2 * ref, 2 * s, 2 * max(c) + 1, torch.float32), "dw added")
+    dw1 = torch.empty_like(dw0)
+    B.moe_grouped_gemm_dw(g, dev_off(off), x, dy, dw1, ws)
+    assert torch.equal(dw0, dw1)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_weight_gradient_with_many_chunks_and_tiles(B, dt):
+    """Experts of very different sizes over many chunks of 128 rows, their
+    sums joined from the slots; overlapping offsets store no slot twice."""
+    el, N, K = DT[dt], 200, 256
+    c = [20000, 0, 1, 129, 14000, 640]
+    off = R.offsets_of(c)
+    rows, E = int(off[-1]), len(c)
+    x, dy = randn((rows, K), el, 1), randn((rows, N), el, 2)
+    g = B.grouped(rows, E, N, K, el)
+    size = B.grouped_dw_workspace_size(g)
+    ws = torch.full((size + 4096,), 255, dtype=torch.uint8, device="cuda")
+    dw = torch.empty(E, N, K, device="cuda")
+    B.moe_grouped_gemm_dw(g, dev_off(off), x, dy, dw, ws)
+    ref, s = R.weight_grad(off, x, dy, E)
+    check(dw, ref, R.sum_bound(ref, s, max(c), torch.float32), "dw")
+    raw = torch.tensor([0, rows, -5, rows + 9, 7, rows, 0], dtype=torch.int32, device="cuda")
+    B.moe_grouped_gemm_dw(g, raw, x, dy, dw, ws)
+    torch.cuda.synchronize()
+    assert (ws[size:] == 255).all()

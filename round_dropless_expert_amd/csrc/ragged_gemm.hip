@@ -447,15 +447,21 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 // 2496 (108) 21 and 54; fp16, 300 rows of 4, N = 2001, K = 1500 (819) 20 and
 // 16, 64 rows of 4, N = 512, K = 511 (96) 7 and 7.
 constexpr int kLargeJobs = 2, kSmallJobs = 2;
+
+// Tiles of the forward or the input gradient at most, over B outputs a row:
+// every expert's last one may be partial.
+int64_t product_tiles(int64_t rows, int64_t E, int B, int tile) {
+  return (rows / tile + (rows < E ? rows : E)) * ceil_div(B, tile);
+}
 template <typename T, int kMode>
 hipError_t launch_general(RaggedParams p, int num_cus, hipStream_t st) {
   auto jobs = [&](int tile) -> int64_t {
     p.tiles_b = ceil_div(p.B, tile);
     p.tiles_a = ceil_div(p.A, tile);
-    // the most units that offsets can make: every expert's last one partial
+    // the most units that offsets can make
     if (kMode == kWeightGrad)
       return ((int64_t)p.rows / p.chunk + p.E) * p.tiles_a * p.tiles_b;
-    return ((int64_t)p.rows / tile + (p.rows < p.E ? p.rows : p.E)) * p.tiles_b;
+    return product_tiles(p.rows, p.E, p.B, tile);
   };
   // (rounded up to whole turns over the XCDs)
   const int64_t large = (jobs(128) + 7) / 8 * 8;
@@ -566,7 +572,11 @@ hipError_t launch_ragged_gemm(const RaggedShape& s, const int32_t* offsets, cons
 hipError_t launch_ragged_dx(const RaggedShape& s, const int32_t* offsets, const void* dy,
                             const void* w, void* dx, int num_cus, hipStream_t st) {
   if (s.rows == 0) return hipSuccess;
-  if (ring_takes(s, dy, s.ld_y, w, s.N))
+  // few outputs: the general kernel's 32 x 32 tiles. bf16, ring against them: 8
+  // rows, E 4, N = K = 2048 17 and 9 us, 1024 rows of one expert, N = 4096, K =
+  // 256 (264 tiles) 23 and 13; 512 rows, E 64, N = K = 512 (1280) 7.8 and 8.0.
+  if (ring_takes(s, dy, s.ld_y, w, s.N) &&
+      product_tiles(s.rows, s.E, s.K, 32) > kSmallJobs * (int64_t)num_cus)
     return launch_ring(
         s.type == ElemType::kBF16 ? RingKind::kInputGradBF16 : RingKind::kInputGradF16,
         ring_params(s, offsets, dy, s.ld_y, w, dx, s.ld_x, s.N, s.K), num_cus, st);

@@ -975,3 +975,27 @@ def test_weight_gradient_with_many_chunks_and_tiles(B, dt):
     B.moe_grouped_gemm_dw(g, raw, x, dy, dw, ws)
     torch.cuda.synchronize()
     assert (ws[size:] == 255).all()
+
+
+# outputs enough for the input gradient's ring: every one of its tiles
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("E,hi,N,K,pad", [
+    (130, 5, 264, 1000, 0), (4, 700, 72, 1000, 8), (3, 2000, 40, 2056, 8), (2, 3000, 520, 520, 0),
+    (60, 33, 1032, 333 * 8, 3), (8, 400, 8, 1032, 0)])
+def test_input_gradient_with_many_tiles(B, dt, E, hi, N, K, pad):
+    el, nan = DT[dt], float("nan")
+    c = np.random.default_rng(E + hi).integers(hi // 2, hi + 1, E).tolist()
+    c[E // 2] = 0
+    off = R.offsets_of(c, 3)
+    rows = int(off[-1]) + 5
+    dy, w = randn((rows, N), el, 1, 8), randn((E, N, K), el, 2, 0, N ** -0.5)
+    dy[:3] = nan
+    dy[int(off[-1]):] = nan
+    w[E // 2] = nan
+    dx = filled(rows, K, el, pad)
+    B.moe_grouped_gemm_dx(B.grouped(rows, E, N, K, el, ld_x=K + pad, ld_y=N + 8), dev_off(off), dy,
+                          w, dx)
+    live = slice(3, int(off[-1]))
+    ref, s = R.product(off, dy, torch.nan_to_num(w.double()), rows, transpose=True)
+    check(dx[live], ref[live], R.sum_bound(ref, s, N, el)[live], "dx")
+    assert (dx[:3] == SENTINEL).all() and (dx[int(off[-1]):] == SENTINEL).all()

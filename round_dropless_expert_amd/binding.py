@@ -481,6 +481,13 @@ _DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_
 _TORCH_DTYPES = {v: k for k, v in _DTYPES.items()}
 
 
+def _int32(v, name):
+    # ctypes keeps the low 32 bits of a larger int
+    if not -2**31 <= int(v) < 2**31:
+        raise ValueError(f"{name} = {v} does not fit 32 bits")
+    return int(v)
+
+
 def grouped(rows, E, N, K, dtype, ld_x=0, ld_y=0) -> MoeGrouped:
     """Shape of a grouped product: weights [E, N, K], buffers of `rows` rows
     with row strides ld_x and ld_y in elements (0: K and N)."""
@@ -488,6 +495,8 @@ def grouped(rows, E, N, K, dtype, ld_x=0, ld_y=0) -> MoeGrouped:
         dtype = {"f32": MOE_F32, "bf16": MOE_BF16, "f16": MOE_F16}[dtype]
     elif isinstance(dtype, torch.dtype):
         dtype = _DTYPES[dtype]
+    for v, name in ((E, "E"), (N, "N"), (K, "K")):
+        _int32(v, name)
     return MoeGrouped(int(rows), int(E), int(N), int(K), int(dtype), int(ld_x),
                       int(ld_y))
 
@@ -678,7 +687,7 @@ def moe_mxfp4_quantize(x, codes, scales, index=None, index_div=1, n_rows=None,
         index_ptr = _dense(index, "index", torch.int32, rows, dev)
     u8 = torch.uint8
     _check(load().moe_mxfp4_quantize(
-        _DTYPES[dt], rows, K, x.data_ptr(), ld_x, src, index_ptr, int(index_div),
+        _DTYPES[dt], rows, K, x.data_ptr(), ld_x, src, index_ptr, _int32(index_div, "index_div"),
         _n_rows(n_rows, dev), _dense(codes, "codes", u8, rows * (K // 2), dev),
         _dense(scales, "scales", u8, rows * mxfp4_scale_stride(K), dev),
         _call_stream(stream, dev)))

@@ -188,3 +188,9 @@ def test_plain_codes_are_the_definition():
     assert (v == 3.0).all()
     q = np.arange(32, dtype=np.uint8).reshape(1, 32) % 16
     assert np.array_equal(R.unpack(R.pack(q)), q)
+
+
+@pytest.mark.parametrize("kw", [dict(E=2**32 + 1), dict(N=2**31), dict(K=-2**31 - 1)])
+def test_sizes_past_32_bits_are_refused(B, kw):
+    with pytest.raises(ValueError, match="32 bits"):
+        B.grouped(**{**dict(rows=4, E=1, N=8, K=8, dtype="bf16"), **kw})

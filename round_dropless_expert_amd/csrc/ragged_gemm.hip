@@ -223,7 +223,8 @@ struct Operand {
 // KiB of per 32 x 32 x 16 product, and the barrier of each stage. 5002 rows, N
 // = 777, K = 1111, fp16: 31 us (35 with the partial stage last and its ends
 // loaded an element at a time); there rows that start at any 2 bytes cost the
-// loads (K = 1104: 25 us).
+// loads (K = 1104: 25 us). fp32, 20480 rows, 5 experts, N = 192, K = 2240: 166
+// us, 106 TFLOP/s.
 //
 // Where there are few outputs a tile is 32 x 32, so that more CUs have one, and
 // its four wavefronts share c: each takes every fourth step of a stage (of
@@ -453,6 +454,7 @@ constexpr int kLargeJobs = 2, kSmallJobs = 2;
 int64_t product_tiles(int64_t rows, int64_t E, int B, int tile) {
   return (rows / tile + (rows < E ? rows : E)) * ceil_div(B, tile);
 }
+
 template <typename T, int kMode>
 hipError_t launch_general(RaggedParams p, int num_cus, hipStream_t st) {
   auto jobs = [&](int tile) -> int64_t {

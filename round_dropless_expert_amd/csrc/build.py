@@ -26,7 +26,7 @@ SOURCES = ["route_plan.hip", "dispatch_combine.hip", "grouped_gemm.hip",
            "ragged_skinny.hip", "ragged_wgrad.hip", "swiglu.hip", "mxfp4.hip",
            "ragged_api.hip"]
 HEADERS = ["device_common.hpp", "launch.hpp", "api_common.hpp", "ragged.hpp",
-           "ragged_device.hpp", "ragged_mma.hpp", "ragged_ring.hpp"]
+           "ragged_device.hpp", "ragged_mma.hpp", "ragged_operand.hpp", "ragged_ring.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -10,6 +10,7 @@
 // contracted index c along its rows (x and w of the forward, dy of the input
 // gradient) or down its columns (the others).
 #include "ragged_device.hpp"
+#include "ragged_operand.hpp"
 #include "ragged_ring.hpp"
 
 namespace moe {
@@ -68,105 +69,21 @@ typedef __attribute__((address_space(3))) char lds_char;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-// 16 bytes of a row of which `n` elements exist (n may be <= 0), the rest
-// zero. `room`: if there are fewer than 16 bytes, so many more lie before
-// `at` in the row, and one load ending at the last element serves. The address
-// need only be aligned to an element: gfx950 loads 16 bytes from any address.
-template <typename T>
-__device__ __forceinline__ u32x4 load16(const T* at, int n, bool room) {
-  constexpr int kV = 16 / sizeof(T);
-  union {
-    T e[kV];
-    u32x4 v;
-  } r;
-  r.v = u32x4{0, 0, 0, 0};
-  if (n >= kV) {
-    __builtin_memcpy(&r.v, at, 16);
-    return r.v;
-  }
-  if (n <= 0) return r.v;
-  if (room) {
-    unsigned __int128 w;
-    __builtin_memcpy(&w, at - (kV - n), 16);
-    w >>= (kV - n) * 8 * (int)sizeof(T);
-    __builtin_memcpy(&r.v, &w, 16);
-    return r.v;
-  }
-#pragma unroll
-  for (int i = 0; i < kV; ++i)
-    if (i < n) r.e[i] = at[i];
-  return r.v;
-}
-
 constexpr int kAhead = 2;    // stages of loads in flight
 
-// One operand's share of a stage: `kExt` rows of its output index by kStage
-// bytes of c. Along: one LDS row per row, 16 bytes of padding. Down: one LDS
-// row per c, kExt elements and 16 bytes of padding.
+// One operand's share of a stage in LDS. Along: one LDS row per row, 16 bytes of
+// padding. Down: one LDS row per c, kExt elements and 16 bytes of padding.
 template <typename T, bool kAlong, int kExt, int kStage>
-struct Operand {
-  static constexpr int kEs = sizeof(T);
-  static constexpr int kV = 16 / kEs;
-  static constexpr int kCk = kStage / kEs;
-  static constexpr int kChunks = kStage / 16;  // of a row along c
+struct Operand : OperandLoads<T, kAlong, kExt, kStage> {
+  typedef OperandLoads<T, kAlong, kExt, kStage> Loads;
+  using Loads::kChunks;
+  using Loads::kCk;
+  using Loads::kEs;
+  using Loads::kPieces;
+  using typename Loads::regs_t;
   static constexpr int kPitch = (kAlong ? kStage : kExt * kEs) + 16;
   static constexpr int kBytes = kAlong ? kExt * kPitch : kCk * kPitch;
-  static constexpr int kPieces = kExt * kChunks / 256;  // 16-byte pieces per thread
-  typedef u32x4 regs_t[kPieces];
 
-  const T* base;  // c = 0 of the tile's first row
-  int64_t ld;
-  int ext;  // rows of the output index that exist
-  // Where this thread's pieces of a whole stage lie, from the stage's first
-  // c: rows past ext read the last one instead (they feed outputs that are
-  // never stored). `whole`: no such load leaves its row; otherwise (a last,
-  // partial chunk of columns) it reads on into the next row, which the
-  // matrix's last row does not have.
-  int64_t at[kPieces];
-  bool whole;
-  bool room;  // down: a row has 16 bytes up to the tile's last column
-
-  // `before`: rows of the output index before the tile's
-  __device__ __forceinline__ void set(const T* b, int64_t l, int e, int before) {
-    base = b;
-    ld = l;
-    ext = e;
-    room = before + e >= kV;
-    whole = kAlong || ext >= kExt || ext % kV == 0;
-#pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      const int id = (int)threadIdx.x + 256 * u;
-      if constexpr (kAlong) {
-        const int row = id / kChunks;
-        at[u] = (row < ext ? row : ext - 1) * ld + (id % kChunks) * kV;
-      } else {
-        constexpr int kPer = kExt * kEs / 16;
-        const int row = (id % kPer) * kV;
-        at[u] = (id / kPer) * ld + (row < ext ? row : 0);
-      }
-    }
-  }
-  // pieces of a whole stage at c0
-  __device__ __forceinline__ void load(regs_t& reg, int c0) const {
-    const T* from = base + (kAlong ? c0 : c0 * ld);
-#pragma unroll
-    for (int u = 0; u < kPieces; ++u) __builtin_memcpy(&reg[u], from + at[u], 16);
-  }
-  // pieces of the stage at c0, where c exists below c_end
-  __device__ __forceinline__ void load_some(regs_t& reg, int c0, int c_end) const {
-#pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      const int id = (int)threadIdx.x + 256 * u;
-      if constexpr (kAlong) {
-        const int row = id / kChunks, c = c0 + (id % kChunks) * kV;
-        reg[u] = load16(base + row * ld + c, row < ext ? c_end - c : 0, c_end >= kV);
-      } else {
-        constexpr int kPer = kExt * kEs / 16;
-        const int c = c0 + id / kPer, row = (id % kPer) * kV;
-        reg[u] = load16(base + c * ld + row, c < c_end ? ext - row : 0, room);
-      }
-    }
-  }
   __device__ static __forceinline__ void store(const regs_t& reg, char* lds) {
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
@@ -216,8 +133,8 @@ struct Operand {
 // x 2 wavefronts of W x W blocks of 32 x 32. Stages of 128 bytes of c go through
 // registers into two LDS buffers, the loads of the next two stages in flight
 // while one is multiplied. Takes every size, stride and element alignment.
-// The whole stages run without a bounds check; the partial one goes first and
-// shifts what it loads at the ends of rows. 32768 rows, N = K = 2049, 8
+// Whole stages run without a bounds check; the partial one (split_stages) goes
+// first and shifts what it loads at the ends of rows. 32768 rows, N = K = 2049, 8
 // experts, fp16: 495 us, 555 TFLOP/s (with 64-byte stages or one stage ahead
 // 10-20% more); what bounds it is LDS, which the 64 x 64 wavefront tiles read 1
 // KiB of per 32 x 32 x 16 product, and the barrier of each stage. 5002 rows, N
@@ -256,7 +173,7 @@ __global__ __launch_bounds__(256, kTile == 64 ? 4 : 2) void ragged_general_kerne
   ExpertUnit u;
   int t = 0;
   if (!find_xcd_unit(p.offsets, p.E, p.rows, units, &t, &u)) return;
-  const int local = t - u.first;
+  const int local = t - u.first, tid = threadIdx.x;
 
   P_t P;
   Q_t Q;
@@ -268,17 +185,18 @@ __global__ __launch_bounds__(256, kTile == 64 ? 4 : 2) void ragged_general_kerne
     c_begin = part * p.chunk;
     c_end = u.rows - c_begin < p.chunk ? u.rows : c_begin + p.chunk;
     a_ext = p.A - a0;
-    P.set(static_cast<const T*>(p.p) + (int64_t)u.start * p.ldp + a0, p.ldp, a_ext, a0);
-    Q.set(static_cast<const T*>(p.q) + (int64_t)u.start * p.ldq + b0, p.ldq, p.B - b0, b0);
+    P.set(static_cast<const T*>(p.p) + (int64_t)u.start * p.ldp + a0, p.ldp, a_ext, a0, tid);
+    Q.set(static_cast<const T*>(p.q) + (int64_t)u.start * p.ldq + b0, p.ldq, p.B - b0, b0, tid);
   } else {
     a0 = local / p.tiles_b * kTile;
     b0 = local % p.tiles_b * kTile;
     c_end = p.C;
     a_ext = u.rows - a0;
-    P.set(static_cast<const T*>(p.p) + ((int64_t)u.start + a0) * p.ldp, p.ldp, a_ext, a0);
+    P.set(static_cast<const T*>(p.p) + ((int64_t)u.start + a0) * p.ldp, p.ldp, a_ext, a0,
+          tid);
     Q.set(static_cast<const T*>(p.q) + (int64_t)u.e * p.B * p.C +
               (kMode == kForward ? (int64_t)b0 * p.ldq : (int64_t)b0),
-          p.ldq, p.B - b0, b0);
+          p.ldq, p.B - b0, b0, tid);
   }
 
   // weight gradient: the slot of this chunk (past the last one only if the
@@ -319,17 +237,20 @@ __global__ __launch_bounds__(256, kTile == 64 ? 4 : 2) void ragged_general_kerne
       for (int s = 0; s < kSteps; ++s) step(buf, s);
     }
   };
-  // the whole stages; the rest is at most one more, which goes first, so that
-  // its loads are as far ahead as the others'
-  const int count = c_end - c_begin;
-  int whole = count / kCk;
-  if (!(P.whole && Q.whole) && whole > 0 && whole * kCk == count) --whole;
-  const int rest = whole * kCk < count ? 1 : 0, stages = whole + rest;
+  // the stages that are checked go first, so that their loads are as far ahead
+  // as the others'
+  const StageSplit split = split_stages(c_end - c_begin, kCk, P.keep > Q.keep ? P.keep : Q.keep);
+  const int rest = split.checked, stages = split.whole + rest;
+  static_assert(kAhead == 2, "the checked stages' loads are the first two");
   typename P_t::regs_t p0, p1;
   typename Q_t::regs_t q0, q1;
   auto load = [&](int i, typename P_t::regs_t& rp, typename Q_t::regs_t& rq) {
     P.load(rp, c_begin + (i - rest) * kCk);
     Q.load(rq, c_begin + (i - rest) * kCk);
+  };
+  auto load_some = [&](int i, typename P_t::regs_t& rp, typename Q_t::regs_t& rq) {
+    P.load_some(rp, c_begin + (split.whole + i) * kCk, c_end, tid);
+    Q.load_some(rq, c_begin + (split.whole + i) * kCk, c_end, tid);
   };
   // stage i from its registers into LDS buffer i % 2, the loads of stage i +
   // kAhead into them, and its products. The buffer's last readers passed the
@@ -341,13 +262,14 @@ __global__ __launch_bounds__(256, kTile == 64 ? 4 : 2) void ragged_general_kerne
     if (i + kAhead < stages) load(i + kAhead, rp, rq);
     multiply(lds[buf]);
   };
-  if (rest) {
-    P.load_some(p0, c_begin + whole * kCk, c_end);
-    Q.load_some(q0, c_begin + whole * kCk, c_end);
-  } else if (whole > 0) {
+  if (rest > 0)
+    load_some(0, p0, q0);
+  else if (stages > 0)
     load(0, p0, q0);
-  }
-  if (stages > 1) load(1, p1, q1);
+  if (rest > 1)
+    load_some(1, p1, q1);
+  else if (stages > 1)
+    load(1, p1, q1);
   for (int i = 0; i < stages; i += 2) {
     stage(i, 0, p0, q0);
     if (i + 1 < stages) stage(i + 1, 1, p1, q1);

@@ -49,3 +49,109 @@ def test_rows_shorter_than_16_bytes(B, dt, rows, narrow):
         assert torch.equal(y.cpu(), R.product(off, x, w, rows)[0].to(el)), (N, K)
         assert torch.equal(dx.cpu(), R.product(off, dy, w, rows, transpose=True)[0].to(el)), (N, K)
         assert torch.equal(dw.double().cpu(), R.weight_grad(off, x, dy, 1)[0]), (N, K)
+
+
+def mm(a, b):
+    """fp64 product on the device: exact for these numbers."""
+    return torch.mm(a.double().contiguous(), b.double().contiguous())
+
+
+def expect(off, a, w, el):
+    """a[i] w[e]^T, rounded once; rows of nobody are 0."""
+    y = torch.zeros(a.shape[0], w.shape[1], dtype=el, device="cuda")
+    for e, b, t in R.segments(off):
+        if t > b:
+            y[b:t] = mm(a[b:t], w[e].t()).to(el)
+    return y
+
+
+# experts of many rows over many chunks, whose sums a bound over all their terms
+# could not tell from one with a row lost: rows of 16 bytes (the ring for 16-bit
+# types, a chunk of 128 rows and then of 512) and of any alignment
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("counts,N,K", [
+    ([20000, 0, 1, 129, 14000, 640], 200, 256), ([127, 128, 9000, 513, 0, 8191], 520, 264),
+    ([3000, 1, 0, 2000], 1024, 2048)])
+def test_weight_gradient_misses_and_doubles_no_row(B, dt, pad, counts, N, K):
+    el, off = DT[dt], R.offsets_of(counts, 2)
+    rows, E = int(off[-1]) + 3, len(counts)
+    x, dy = whole((rows, K + pad), el, 1)[:, :K], whole((rows, N + pad), el, 2)[:, :N]
+    g = B.grouped(rows, E, N, K, el, ld_x=K + pad, ld_y=N + pad)
+    ws = torch.full((B.grouped_dw_workspace_size(g),), 255, dtype=torch.uint8, device="cuda")
+    dw = torch.full((E, N, K), float("nan"), device="cuda")
+    ref = torch.stack([mm(dy[b:t].t(), x[b:t]) for _, b, t in R.segments(off)])
+    B.moe_grouped_gemm_dw(g, dev_off(off), x, dy, dw, ws)
+    assert torch.equal(dw.double(), ref)
+    was = whole((E, N, K), torch.float32, 3)
+    dw.copy_(was)
+    B.moe_grouped_gemm_dw(g, dev_off(off), x, dy, dw, ws, accumulate=True)
+    assert torch.equal(dw.double(), ref + was.double())
+
+
+def test_weight_gradient_past_4_gib_misses_and_doubles_no_row(B):
+    """One expert with nearly all rows of a buffer of 4.9 GB, in many chunks:
+    columns at both ends and in the middle."""
+    rows, N, K, el = 300_000, 256, 8192, torch.bfloat16
+    off = R.offsets_of([5, rows - 135, 130])
+    x, dy = whole((rows, K), torch.int8, 1).to(el), whole((rows, N), el, 2)
+    g = B.grouped(rows, 3, N, K, el)
+    ws = torch.full((B.grouped_dw_workspace_size(g),), 255, dtype=torch.uint8, device="cuda")
+    dw = torch.empty(3, N, K, device="cuda")
+    B.moe_grouped_gemm_dw(g, dev_off(off), x, dy, dw, ws)
+    cols = [0, 1, 255, 256, 4095, 8190, 8191]
+    for e, b, t in R.segments(off):
+        assert torch.equal(dw[e][:, cols].double(), mm(dy[b:t].t(), x[b:t][:, cols])), e
+
+
+# every tile of the products, with sums too long for a bound to see one term:
+# the ring's 256 x 256, 256 x 128 and 128 x 64, the skinny kernel, and (3 more
+# elements a row) the general kernel; K ends inside a stage and inside a slot
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("counts,N,K,pad", [
+    ([4000, 0, 4192], 4096, 2088, 0), ([1500, 260], 2048, 4104, 0), ([70, 0, 300, 64], 2000, 7168, 0),
+    ([1], 4096, 4112, 0), ([3, 0, 30], 1000, 7160, 0), ([700, 0, 33], 520, 4099, 3),
+    ([2], 300, 4099, 3)])
+def test_products_miss_and_double_no_term(B, dt, counts, N, K, pad):
+    el, off = DT[dt], R.offsets_of(counts, 1)
+    rows, E = int(off[-1]) + 2, len(counts)
+    x, dy = whole((rows, K + pad), el, 1)[:, :K], whole((rows, N + pad), el, 2)[:, :N]
+    w = whole((E, N, K), el, 3)
+    g = B.grouped(rows, E, N, K, el, ld_x=K + pad, ld_y=N + pad)
+    y = torch.zeros(rows, N + pad, dtype=el, device="cuda")[:, :N]
+    dx = torch.zeros(rows, K + pad, dtype=el, device="cuda")[:, :K]
+    B.moe_grouped_gemm(g, dev_off(off), x, w, y)
+    assert torch.equal(y, expect(off, x, w, el))
+    B.moe_grouped_gemm_dx(g, dev_off(off), dy, w, dx)
+    assert torch.equal(dx, expect(off, dy, w.transpose(1, 2), el))
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("counts,N,K", [
+    ([4000, 0, 4192], 4096, 2080), ([1500, 260], 2048, 4128), ([70, 0, 300, 64], 2000, 7168),
+    ([1], 4096, 4096), ([3, 0, 30], 1000, 7136)])
+def test_mxfp4_products_miss_and_double_no_term(B, dt, counts, N, K):
+    """Values of 1/4 to 12 in steps that make every product a multiple of 1/16
+    of at most 144: sums of 7168 of them are exact in fp32."""
+    el, off = DT[dt], R.offsets_of(counts, 1)
+    rows, E, S = int(off[-1]) + 2, len(counts), B.mxfp4_scale_stride(K)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    levels = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float64)
+    levels = torch.cat([levels, -levels]).cuda()
+
+    def operand(n):
+        c = torch.randint(0, 16, (n, K), generator=gen, device="cuda", dtype=torch.uint8)
+        s = torch.randint(126, 129, (n, S), generator=gen, device="cuda", dtype=torch.uint8)
+        f = torch.exp2(s[:, : K // 32].double() - 127).repeat_interleave(32, dim=1)
+        s[:, K // 32:] = 255  # the padding is never used
+        return c[:, 0::2] | (c[:, 1::2] << 4), s, levels[c.int()] * f
+
+    xq, xs, xv = operand(rows)
+    wq, wsc, wv = operand(E * N)
+    y = torch.zeros(rows, N, dtype=el, device="cuda")
+    B.moe_mxfp4_grouped_gemm(B.grouped(rows, E, N, K, el), dev_off(off), xq, xs, wq, wsc, y)
+    ref = torch.zeros(rows, N, dtype=torch.float64, device="cuda")
+    for e, b, t in R.segments(off):
+        if t > b:
+            ref[b:t] = mm(xv[b:t], wv.view(E, N, K)[e].t())
+    assert torch.equal(y, ref.float().to(el))

@@ -11,15 +11,16 @@
 // (2.01 GB, 6.2 TB/s); a 4 GiB copy moves 4.8 TB/s. A row's lanes are a power
 // of two, so no lane divides, and outputs are stored past the caches, which
 // leaves those to the inputs (648 us for both passes without either, 514
-// with).
+// with). Rows that 16-byte vectors do not fit (2047 features, or 4099 elements
+// apart) go element by element: 231 and 440 us.
 #include "ragged_device.hpp"
 
 namespace moe {
 namespace {
 
-// s(g) and 1 - s(g), both to a few ulp for every g: with a = e^-|g| they
-// are 1 / (1 + a) and a / (1 + a), in the order of g's sign, so neither
-// cancels and no exponential overflows.
+// s(g) and 1 - s(g), both to a few ulp for every g of at least kTail: with a =
+// e^-|g| they are 1 / (1 + a) and a / (1 + a), in the order of g's sign, so
+// neither cancels and no exponential overflows.
 struct Gate {
   float s, rest;
 };
@@ -40,10 +41,57 @@ __device__ __forceinline__ Gate gate(float g) {
   return g >= 0.f ? Gate{r, q} : Gate{q, r};
 }
 
+// Below kTail s(g) leaves fp32's normal numbers (e^-87.3 = 2^-126; the hardware
+// exponential returns 0 there), while its products with u and dh need not. It
+// is e^g to 2^-124 then, kept as a value and a power of two, and so are the
+// products (Scaled). Below kZero every product is 0 in fp32, and fp16 values are
+// too small for one to reach fp16's least subnormal. One comparison per vector
+// finds these features; their outputs are stored a second time, from operands
+// that are read again behind the row's others, so that those hold no registers
+// for them. The comparison costs nothing that can be measured (191 and 325 us
+// with and without it); with such a feature in every row the passes above take
+// 486 and 706 us.
+constexpr float kTail = -86.f, kZero = -1024.f;
+template <typename T>
+constexpr bool kHasTail = !__is_same(T, f16);
+
+struct Scaled {  // m 2^e
+  float m;
+  int e;
+  __device__ __forceinline__ Scaled times(float v) const {
+    return Scaled{m * __builtin_amdgcn_frexp_mantf(v), e + __builtin_amdgcn_frexp_expf(v)};
+  }
+  __device__ __forceinline__ float value() const { return __builtin_ldexpf(m, e); }
+};
+// e^g for kZero < g < 0: g log2 e less its nearest integer to fp32's precision
+// by log2 e in two parts.
+__device__ __forceinline__ Scaled scaled_exp(float g) {
+  constexpr double kLog2e = 1.44269504088896340736;
+  constexpr float kHigh = (float)kLog2e, kLow = (float)(kLog2e - kHigh);
+  const float n = __builtin_rintf(g * kHigh);
+  const float r = __builtin_fmaf(g, kLow, __builtin_fmaf(g, kHigh, -n));
+  return Scaled{__builtin_amdgcn_exp2f(r), (int)n};
+}
+
 template <typename T, int V>
 struct Vec {
   T e[V];
 };
+
+// Whether any g may lie below kTail: of negative values, as unsigned numbers
+// the larger are further from zero (and of NaN, which store_tail leaves out).
+template <typename T, int V>
+__device__ __forceinline__ bool in_tail(const Vec<T, V>& g) {
+  if constexpr (!kHasTail<T>) return false;
+  constexpr uint32_t kBits = __builtin_bit_cast(uint32_t, kTail);
+  if constexpr (sizeof(T) == 4) {
+    typedef uint32_t uint_t __attribute__((ext_vector_type(V)));
+    return __builtin_reduce_max(__builtin_bit_cast(uint_t, g)) > kBits;
+  } else {
+    typedef uint16_t uint_t __attribute__((ext_vector_type(V)));
+    return __builtin_reduce_max(__builtin_bit_cast(uint_t, g)) > kBits >> 16;
+  }
+}
 
 template <typename T, int V>
 __device__ __forceinline__ Vec<T, V> load(const T* p) {
@@ -60,6 +108,25 @@ __device__ __forceinline__ void store(T* p, const Vec<T, V>& v) {
     *p = v.e[0];
   else
     __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(p));
+}
+
+template <typename T, int V, bool kBackward>
+__device__ __forceinline__ void store_tail(const T* gu, const T* dh, T* out, int64_t f,
+                                           int64_t at) {
+#pragma unroll 1
+  for (int v = 0; v < V; ++v, ++at) {
+    const float g = to_f32(gu[at]);
+    if (!(g < kTail && g > kZero)) continue;
+    const Scaled s = scaled_exp(g), gs = s.times(g);
+    const float u = to_f32(gu[f + at]);
+    if constexpr (!kBackward) {
+      out[at] = from_f32<T>(gs.times(u).value());
+    } else {  // 1 - s is 1
+      const float d = to_f32(dh[at]);
+      out[at] = from_f32<T>(s.times(1.0f + g).times(u).times(d).value());
+      out[f + at] = from_f32<T>(gs.times(d).value());
+    }
+  }
 }
 
 struct SwigluParams {
@@ -87,6 +154,7 @@ __global__ __launch_bounds__(256) void swiglu_kernel(SwigluParams p) {
     const T* gu = static_cast<const T*>(p.gu) + row * p.ld_gu;
     const T* dh = static_cast<const T*>(p.dh) + row * p.ld_dh;
     T* out = static_cast<T*>(p.out) + row * p.ld_out;
+    bool tail = false;
     for (int c = c0; c < per; c += lanes * kUnroll) {
       Vec<T, V> g[kUnroll], u[kUnroll], d[kUnroll];
 #pragma unroll
@@ -102,6 +170,7 @@ __global__ __launch_bounds__(256) void swiglu_kernel(SwigluParams p) {
       for (int k = 0; k < kUnroll; ++k) {
         if (c + k * lanes >= per) break;
         const int64_t at = (int64_t)(c + k * lanes) * V;
+        tail |= in_tail(g[k]);
         if constexpr (!kBackward) {
           Vec<T, V> h;
 #pragma unroll
@@ -123,6 +192,11 @@ __global__ __launch_bounds__(256) void swiglu_kernel(SwigluParams p) {
           store<T, V>(out + p.f + at, du);
         }
       }
+    }
+    if (tail) {
+#pragma unroll 1
+      for (int c = c0; c < per; c += lanes)
+        store_tail<T, V, kBackward>(gu, dh, out, p.f, (int64_t)c * V);
     }
   }
 }

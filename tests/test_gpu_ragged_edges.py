@@ -155,3 +155,58 @@ def test_mxfp4_products_miss_and_double_no_term(B, dt, counts, N, K):
         if t > b:
             ref[b:t] = mm(xv[b:t], wv.view(E, N, K)[e].t())
     assert torch.equal(y, ref.float().to(el))
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("f,pad", [(2048, 0), (37, 3)])
+def test_swiglu_where_the_gate_is_below_fp32(B, dt, f, pad):
+    """s(g) down to and below 2^-126 against u and dh that bring the outputs back
+    into range: nothing is flushed."""
+    el = DT[dt]
+    fi = torch.finfo(el)
+    gs = [-60.0, -80.0, -85.5, -86.0, -86.5, -87.0, -87.5, -88.0, -90.0, -100.0, -103.5, -104.0,
+          -120.0, -150.0, -200.0, -250.0, -280.0, -300.0, -500.0, -1000.0, -1023.0, -1024.0,
+          -1032.0, -3000.0]
+    gs = gs + [30.0, 100.0, -1.0, 0.0]
+    vals = [1.0, -1e30, 3e38, -1e36, 1e4, 1e-3]
+    rows = len(vals) ** 2
+    gen = torch.Generator().manual_seed(1)
+    g = torch.tensor(gs)[torch.randint(0, len(gs), (rows, f), generator=gen)].to(el)
+    u = torch.tensor(vals).clamp(-fi.max, fi.max).repeat_interleave(len(vals))
+    d = torch.tensor(vals).clamp(-fi.max, fi.max).repeat(len(vals))
+    u, d = (v.to(el).unsqueeze(1).expand(rows, f) for v in (u, d))
+
+    def padded(t):
+        b = torch.zeros(rows, t.shape[1] + pad, dtype=el, device="cuda")[:, :t.shape[1]]
+        b.copy_(t)
+        return b
+
+    gu, dh = padded(torch.cat([g, u], dim=1)), padded(d)
+    h, dgu = padded(torch.zeros_like(d)), padded(torch.zeros(rows, 2 * f, dtype=el))
+    B.moe_swiglu(gu, h)
+    B.moe_swiglu_backward(gu, dh, dgu)
+    g, u, d = g.double(), u.double(), d.double()
+    s, r = torch.sigmoid(g), torch.sigmoid(-g)
+    # exponential, reciprocal and products, each within an ulp or two (2^-21
+    # covers eight roundings); of 16-bit types the exponent's argument from -86
+    # on is rounded to fp32, off by |g| 2^-24 in all
+    rel = 2.0 ** -21 + (0.0 if dt == "f32" else torch.where(g < -86, 0.0, g.abs() * 2.0 ** -23))
+
+    def near(got, ref, tol, what):
+        ok = ref.abs() < fi.max / 4  # no partial product overflows either
+        # fp32 subnormals on the way to the output: 2^-149
+        bound = tol + R.rounding(ref.abs() + tol, el) + 2.0 ** -149
+        err = (got.double().cpu() - ref).abs()
+        bad = ok & ~(err <= bound)
+        assert not bad.any(), (what, int(bad.sum()), g[bad][0], u[bad][0], d[bad][0],
+                               got.double().cpu()[bad][0], ref[bad][0])
+
+    href = g * s * u
+    near(h, href, href.abs() * rel, "h")
+    du = d * g * s
+    near(dgu[:, f:], du, du.abs() * rel, "du")
+    # from -86 on dh s (1 + g (1 - s)) is fp32 before u comes in, so that half a
+    # step of its subnormals counts u times
+    dg = d * u * s * (1 + g * r)
+    tol = (d * u).abs() * s * (1 + (g * r).abs()) * 2 * rel
+    near(dgu[:, :f], dg, tol + torch.where(g < -86, 0.0, u.abs() * 2.0 ** -149), "dg")

@@ -8,6 +8,9 @@ has not been built this module raises at load time: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import itertools
+import math
+import operator
 import os
 
 import numpy as np
@@ -549,6 +552,22 @@ def _dense(t, name, dtype, numel, dev):
     return _arg(t, name, dtype, numel)  # raises
 
 
+def _matrices(t, name, dtype, shape, dev):
+    """Address of a contiguous tensor of at least the elements of shape (...,
+    height, width) whose trailing dimensions make rows of that width or whole
+    matrices (a plain buffer has none): a transposed layout is refused."""
+    if t is None or isinstance(t, int):
+        return t
+    _on_device(t, name, dev)
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    address = _arg(t, name, dtype, math.prod(shape))
+    groups = list(itertools.accumulate(reversed(t.shape[1:]), operator.mul))
+    if shape[-1] not in groups and any(n < shape[-2] * shape[-1] for n in groups):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    return address
+
+
 def _mat(t, name, dtype, rows, cols, ld, dev):
     """Address of a [rows, cols] matrix whose rows are ld elements apart."""
     if t is None or isinstance(t, int):
@@ -616,7 +635,7 @@ def moe_grouped_gemm(g, offsets, x, w, y, stream=None):
     rows, E, N, K, dev = g.rows, g.E, g.N, g.K, torch.cuda.current_device()
     _check(load().moe_grouped_gemm(
         g, _offsets(offsets, E, dev), _mat(x, "x", el, rows, K, ld_x, dev),
-        _dense(w, "w", el, E * N * K, dev), _mat(y, "y", el, rows, N, ld_y, dev),
+        _matrices(w, "w", el, (E, N, K), dev), _mat(y, "y", el, rows, N, ld_y, dev),
         _call_stream(stream, dev)))
 
 
@@ -626,7 +645,7 @@ def moe_grouped_gemm_dx(g, offsets, dy, w, dx, stream=None):
     rows, E, N, K, dev = g.rows, g.E, g.N, g.K, torch.cuda.current_device()
     _check(load().moe_grouped_gemm_dx(
         g, _offsets(offsets, E, dev), _mat(dy, "dy", el, rows, N, ld_y, dev),
-        _dense(w, "w", el, E * N * K, dev), _mat(dx, "dx", el, rows, K, ld_x, dev),
+        _matrices(w, "w", el, (E, N, K), dev), _mat(dx, "dx", el, rows, K, ld_x, dev),
         _call_stream(stream, dev)))
 
 
@@ -645,7 +664,7 @@ def moe_grouped_gemm_dw(g, offsets, x, dy, dw, ws=None, accumulate=False, stream
     _check(load().moe_grouped_gemm_dw(
         g, _offsets(offsets, E, dev), _mat(x, "x", el, rows, K, ld_x, dev),
         _mat(dy, "dy", el, rows, N, ld_y, dev),
-        _dense(dw, "dw", torch.float32, E * N * K, dev), 1 if accumulate else 0, w_ptr,
+        _matrices(dw, "dw", torch.float32, (E, N, K), dev), 1 if accumulate else 0, w_ptr,
         w_bytes, _call_stream(stream, dev)))
 
 
@@ -688,8 +707,8 @@ def moe_mxfp4_quantize(x, codes, scales, index=None, index_div=1, n_rows=None,
     u8 = torch.uint8
     _check(load().moe_mxfp4_quantize(
         _DTYPES[dt], rows, K, x.data_ptr(), ld_x, src, index_ptr, _int32(index_div, "index_div"),
-        _n_rows(n_rows, dev), _dense(codes, "codes", u8, rows * (K // 2), dev),
-        _dense(scales, "scales", u8, rows * mxfp4_scale_stride(K), dev),
+        _n_rows(n_rows, dev), _matrices(codes, "codes", u8, (rows, K // 2), dev),
+        _matrices(scales, "scales", u8, (rows, mxfp4_scale_stride(K)), dev),
         _call_stream(stream, dev)))
 
 
@@ -699,8 +718,8 @@ def moe_mxfp4_dequantize(codes, scales, y, n_rows=None, stream=None):
     dt, rows, K, ld_y = _rows_of(y, "y", dev)
     u8 = torch.uint8
     _check(load().moe_mxfp4_dequantize(
-        _DTYPES[dt], rows, K, _dense(codes, "codes", u8, rows * (K // 2), dev),
-        _dense(scales, "scales", u8, rows * mxfp4_scale_stride(K), dev),
+        _DTYPES[dt], rows, K, _matrices(codes, "codes", u8, (rows, K // 2), dev),
+        _matrices(scales, "scales", u8, (rows, mxfp4_scale_stride(K)), dev),
         y.data_ptr(), ld_y, _n_rows(n_rows, dev), _call_stream(stream, dev)))
 
 
@@ -711,10 +730,10 @@ def moe_mxfp4_grouped_gemm(g, offsets, x_codes, x_scales, w_codes, w_scales, y,
     rows, E, N, K, dev = g.rows, g.E, g.N, g.K, torch.cuda.current_device()
     S, u8 = mxfp4_scale_stride(K), torch.uint8
     _check(load().moe_mxfp4_grouped_gemm(
-        g, _offsets(offsets, E, dev), _dense(x_codes, "x_codes", u8, rows * (K // 2), dev),
-        _dense(x_scales, "x_scales", u8, rows * S, dev),
-        _dense(w_codes, "w_codes", u8, E * N * (K // 2), dev),
-        _dense(w_scales, "w_scales", u8, E * N * S, dev),
+        g, _offsets(offsets, E, dev), _matrices(x_codes, "x_codes", u8, (rows, K // 2), dev),
+        _matrices(x_scales, "x_scales", u8, (rows, S), dev),
+        _matrices(w_codes, "w_codes", u8, (E, N, K // 2), dev),
+        _matrices(w_scales, "w_scales", u8, (E, N, S), dev),
         _mat(y, "y", el, rows, N, ld_y, dev), _call_stream(stream, dev)))
 
 

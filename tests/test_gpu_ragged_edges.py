@@ -210,3 +210,31 @@ def test_swiglu_where_the_gate_is_below_fp32(B, dt, f, pad):
     dg = d * u * s * (1 + g * r)
     tol = (d * u).abs() * s * (1 + (g * r).abs()) * 2 * rel
     near(dgu[:, :f], dg, tol + torch.where(g < -86, 0.0, u.abs() * 2.0 ** -149), "dg")
+
+
+def test_transposed_weights_are_refused(B):
+    """Layouts that have the right number of elements and other rows."""
+    el, rows, E, N, K = torch.bfloat16, 8, 2, 16, 64
+    zeros = lambda *n, dtype=el: torch.zeros(*n, dtype=dtype, device="cuda")
+    g, off = B.grouped(rows, E, N, K, el), torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    x, y, S = zeros(rows, K), zeros(rows, N), B.mxfp4_scale_stride(K)
+    u8 = lambda *n: zeros(*n, dtype=torch.uint8)
+    ops = [u8(rows, K // 2), u8(rows, S), u8(E, N, K // 2), u8(E, N, S)]
+    calls = [
+        lambda w: B.moe_grouped_gemm(g, off, x, w, y),
+        lambda w: B.moe_grouped_gemm_dx(g, off, y, w, x),
+        lambda w: B.moe_grouped_gemm_dw(g, off, x, y, w.float()),
+        lambda w: B.moe_mxfp4_quantize(w, u8(E, K, N // 2), u8(E, N, S)),
+        lambda w: B.moe_mxfp4_quantize(w, u8(E, N, K // 2), u8(E, S, N)),
+    ]
+    for i in range(4):
+        t = [*ops]
+        t[i] = t[i].reshape(*t[i].shape[:-2], t[i].shape[-1], t[i].shape[-2])
+        calls.append(lambda w, t=t: B.moe_mxfp4_grouped_gemm(g, off, *t, y))
+    for f in calls[:3]:
+        f(zeros(E, N, K)), f(zeros(E * N, K)), f(zeros(E, 2, N // 2, K)), f(zeros(E * N * K))
+        with pytest.raises(ValueError, match="shape"):
+            f(zeros(E, K, N))
+    for f in calls[3:]:
+        with pytest.raises(ValueError, match="shape"):
+            f(zeros(E, N, K))

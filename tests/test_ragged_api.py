@@ -194,3 +194,28 @@ def test_plain_codes_are_the_definition():
 def test_sizes_past_32_bits_are_refused(B, kw):
     with pytest.raises(ValueError, match="32 bits"):
         B.grouped(**{**dict(rows=4, E=1, N=8, K=8, dtype="bf16"), **kw})
+
+
+@pytest.mark.parametrize("shape,have,ok", [
+    ((4, 16, 8), (4, 16, 8), True), ((4, 16, 8), (5, 16, 8), True), ((4, 16, 8), (64, 8), True),
+    ((4, 16, 8), (4, 128), True), ((4, 16, 8), (512,), True), ((4, 16, 8), (4, 2, 8, 8), True),
+    ((4, 16, 8), (4, 16, 2, 4), True), ((8, 4), (2, 4, 4), True), ((3, 4), (8, 16), True),
+    ((0, 4), (0, 16), True), ((4, 16, 8), (4, 8, 16), False), ((4, 4, 16), (4, 16, 4), False),
+    ((4, 16, 8), (8, 64), False), ((4, 16, 8), (3, 16, 8), False), ((8, 12), (8, 16), False),
+    ((8, 12), (24, 4), False)])
+def test_layouts_of_matrices_are_checked(B, monkeypatch, shape, have, ok):
+    """Tensors of other shapes are taken where their rows are the shape's."""
+    monkeypatch.setattr(B, "_on_device", lambda t, name, dev: None)
+
+    def address(t, name, dtype, numel):
+        if t.numel() < numel:
+            raise ValueError(name)
+        return t.data_ptr()
+
+    monkeypatch.setattr(B, "_arg", address)
+    t = torch.zeros(have)
+    if ok:
+        assert B._matrices(t, "w", torch.float32, shape, 0) == t.data_ptr()
+    else:
+        with pytest.raises(ValueError, match="w"):
+            B._matrices(t, "w", torch.float32, shape, 0)

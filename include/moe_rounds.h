@@ -598,7 +598,9 @@ moe_status_t moe_mxfp4_quantize(int32_t dtype, int64_t rows, int64_t K,
                                 const int32_t *n_rows, uint8_t *codes,
                                 uint8_t *scales, void *stream);
 
-/* The values, rounded to elem (bf16 and fp32 hold every one of them). */
+/* The values, rounded to elem. bf16 and fp32 hold every one of them but 4 and 6
+ * under scale byte 253 and 2, 3, 4 and 6 under 254, which become infinite
+ * (moe_mxfp4_quantize's bytes end at 252); so do, in fp16, those past 65504. */
 moe_status_t moe_mxfp4_dequantize(int32_t dtype, int64_t rows, int64_t K,
                                   const uint8_t *codes, const uint8_t *scales,
                                   void *y, int64_t ld_y, const int32_t *n_rows,

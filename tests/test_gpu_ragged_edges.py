@@ -238,3 +238,25 @@ def test_transposed_weights_are_refused(B):
     for f in calls[3:]:
         with pytest.raises(ValueError, match="shape"):
             f(zeros(E, N, K))
+
+
+def test_dequantised_values_are_exact_or_infinite(B):
+    """Every code under every scale byte against fp64: bf16 and fp32 hold all
+    values but those past their largest, which are infinite; fp16 rounds."""
+    import numpy as np
+    c = np.tile(np.arange(16, dtype=np.uint8), (255, 2))
+    codes = torch.from_numpy(R.pack(c)).cuda()
+    scales = torch.zeros(255, 4, dtype=torch.uint8, device="cuda")
+    scales[:, 0] = torch.arange(255, dtype=torch.uint8)
+    ref = torch.from_numpy(R.values_of(c, np.arange(255, dtype=np.uint8)[:, None]))
+    for el in DT.values():
+        y = torch.empty(255, 32, dtype=el, device="cuda")
+        B.moe_mxfp4_dequantize(codes, scales, y)
+        y = y.double().cpu()
+        past = ref.abs() > torch.finfo(el).max
+        if el != torch.float16:
+            assert past.nonzero()[:, 0].unique().tolist() == [253, 254]
+            assert torch.equal(y[~past], ref[~past])
+        else:
+            assert torch.equal(y[~past], ref[~past].to(el).double())
+        assert torch.equal(y[past], torch.copysign(torch.full_like(ref[past], torch.inf), ref[past]))

@@ -457,14 +457,18 @@ RaggedParams base_params(const RaggedShape& s, const int32_t* offsets) {
 // Chunks: an expert's tiles run at once, so a chunk may hold half of the rows
 // that a CU sums in all (rows * tiles / 256), or an expert with many rows
 // holds up the launch. A chunk past the first costs a write and a read of
-// [N][K] in fp32 against 2 N K flops a row: 512 rows at least, or 128 where
-// [N][K] is one tile and its slots are small (8192 rows of 8 experts with N =
-// K = 512: 46 us with chunks of 512, 59 with 128; 1024 rows with N = 256, K =
-// 64 in fp32: 15 us with 512, 9 with 128). A function of the shape alone: it
-// fixes the order of the sums.
+// [N][K] in fp32 against 2 N K flops a row: 512 rows at least (8192 rows of 8
+// experts with N = K = 512: 46 us with chunks of 512, 59 with 128; 65536 rows of
+// 64 with N = K = 256: 36 and 63). Few rows in fp32, whose products take eight
+// times as long, may go down to 128 where [N][K] is one tile: 2048 rows of 16
+// uneven experts with N = K = 256 take 22 us with 512 and 13 with 128, 4096 of 64
+// 32 and 25, 4096 of 8 even ones 17 and 18; but 16384 of 64 even ones 27 and 40,
+// and bf16 at 2048 of 16 uneven ones 10.3 and 9.6, at 2048 of 4 even ones 7.1 and
+// 10.1. A function of the shape alone: it fixes the order of the sums.
 DwSplit dw_split(const RaggedShape& s) {
   const int64_t tiles = (int64_t)ceil_div(s.N, 256) * ceil_div(s.K, 256);
-  const int64_t least = tiles == 1 ? 128 : 512;
+  const bool few = s.type == ElemType::kF32 && tiles == 1 && s.rows <= 4096;
+  const int64_t least = few ? 128 : 512;
   int64_t chunk = (s.rows * tiles + 511) / 512;
   chunk = chunk < least ? least : (chunk + 63) / 64 * 64;
   // a chunk's rows are addressed with 32-bit byte offsets

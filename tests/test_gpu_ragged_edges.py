@@ -66,8 +66,8 @@ def expect(off, a, w, el):
 
 
 # experts of many rows over many chunks, whose sums a bound over all their terms
-# could not tell from one with a row lost: rows of 16 bytes (the ring for 16-bit
-# types, a chunk of 128 rows and then of 512) and of any alignment
+# could not tell from one with a row lost, in rows that start at 16 bytes (the
+# ring for 16-bit types where it has the tiles) and in others
 @pytest.mark.parametrize("dt", list(DT))
 @pytest.mark.parametrize("pad", [0, 3])
 @pytest.mark.parametrize("counts,N,K", [

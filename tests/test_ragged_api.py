@@ -219,3 +219,13 @@ def test_layouts_of_matrices_are_checked(B, monkeypatch, shape, have, ok):
     else:
         with pytest.raises(ValueError, match="w"):
             B._matrices(t, "w", torch.float32, shape, 0)
+
+
+def test_weight_gradient_workspace_is_small_beside_the_operands(B):
+    """Few slots where many rows meet small matrices: a chunk has 512 rows, or in
+    fp32 128 where there are at most 4096."""
+    size = lambda rows, dt: B.grouped_dw_workspace_size(B.grouped(rows, 64, 256, 256, dt))
+    for rows in (4097, 65536, 131072):
+        for dt in ("bf16", "f16", "f32"):
+            assert size(rows, dt) <= rows // 512 * 256 * 256 * 4
+    assert size(4096, "bf16") == 8 * 256 * 256 * 4 and size(4096, "f32") == 32 * 256 * 256 * 4

@@ -619,6 +619,9 @@ def _offsets(offsets, E, dev):
 
 
 def _n_rows(n_rows, dev):
+    # every number of rows is below 2^31, every device address far above
+    if isinstance(n_rows, int) and n_rows < 2**32:
+        raise TypeError(f"n_rows = {n_rows}: expected a one-element int32 device tensor")
     return None if n_rows is None else _dense(n_rows, "n_rows", torch.int32, 1, dev)
 
 

@@ -229,3 +229,10 @@ def test_weight_gradient_workspace_is_small_beside_the_operands(B):
         for dt in ("bf16", "f16", "f32"):
             assert size(rows, dt) <= rows // 512 * 256 * 256 * 4
     assert size(4096, "bf16") == 8 * 256 * 256 * 4 and size(4096, "f32") == 32 * 256 * 256 * 4
+
+
+@pytest.mark.parametrize("n", [0, 8, 64, 2**31 - 1, True])
+def test_numbers_of_rows_are_not_taken_for_addresses(B, n):
+    with pytest.raises(TypeError, match="n_rows"):
+        B._n_rows(n, 0)
+    assert B._n_rows(None, 0) is None and B._n_rows(1 << 46, 0) == 1 << 46

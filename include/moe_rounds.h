@@ -512,10 +512,12 @@ moe_status_t moe_backward(const moe_config_t *cfg, const void *x,
  * launches on `stream` and can be captured into a graph. The sizes that
  * shape a launch are on the host, the offsets only on the device; offsets
  * are clamped to [0, rows], so wrong ones give wrong results but no access
- * outside the buffers. Outputs must not overlap inputs. Matrices are
- * row-major with a row stride of ld elements (0 means the width); unlike in
- * the layer's calls, addresses only need the alignment of an element (16
- * bytes for the 4-bit format). 16-byte aligned rows are faster.
+ * outside the buffers (16-bit rows of odd width at 16-byte addresses are read
+ * in whole aligned 4-byte words, the last element's included). Outputs must
+ * not overlap inputs. Matrices are row-major with a row stride of ld elements
+ * (0 means the width); unlike in the layer's calls, addresses only need the
+ * alignment of an element (16 bytes for the 4-bit format). 16-byte aligned
+ * rows are faster.
  *
  * elem below is fp32, bf16 or fp16 (MOE_F32, MOE_BF16, MOE_F16). Products
  * run on the matrix cores with fp32 accumulation and round each output once.

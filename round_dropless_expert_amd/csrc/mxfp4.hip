@@ -130,9 +130,9 @@ struct QuantParams {
 // by DPP, and each stores V / 2 bytes of codes. kUnroll vectors of a row are
 // in flight per lane.
 //
-// Bound by memory: 98304 rows of 7168 bf16 gathered from 16384 tokens, 240 us
-// (1.41 GB asked for and 0.37 GB stored, 7.4 TB/s: a token's later reads come
-// from the caches).
+// Bound by memory: 98304 rows of 7168 bf16 gathered from 16384 tokens, 237-243
+// us (1.41 GB asked for and 0.37 GB stored, 7.4 TB/s: a token's later reads come
+// from the caches; read once it would be 0.6 GB in all).
 template <typename T, bool kVec>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(QuantParams p) {
   constexpr int V = 16 / sizeof(T);
@@ -204,7 +204,7 @@ struct DequantParams {
 };
 
 // The inverse: a lane reads V / 2 bytes of codes and stores 16 bytes of
-// values, past the caches. Bound by the stores: 98304 rows of 7168 bf16, 317
+// values, past the caches. Bound by the stores: 98304 rows of 7168 bf16, 317-320
 // us (0.37 GB read, 1.41 GB stored, 5.6 TB/s).
 template <typename T, bool kVec>
 __global__ __launch_bounds__(256) void mx_dequantize_kernel(DequantParams p) {

@@ -135,13 +135,14 @@ struct Operand : OperandLoads<T, kAlong, kExt, kStage> {
 // while one is multiplied. Takes every size, stride and element alignment.
 // Whole stages run without a bounds check; the partial one (split_stages) goes
 // first and shifts what it loads at the ends of rows. 32768 rows, N = K = 2049, 8
-// experts, fp16: 495 us, 555 TFLOP/s (with 64-byte stages or one stage ahead
-// 10-20% more); what bounds it is LDS, which the 64 x 64 wavefront tiles read 1
+// experts, fp16: 490-532 us, 515-560 TFLOP/s (with 64-byte stages or one stage
+// ahead 10-20% more); what bounds it is LDS, which the 64 x 64 wavefront tiles read 1
 // KiB of per 32 x 32 x 16 product, and the barrier of each stage. 5002 rows, N
-// = 777, K = 1111, fp16: 31 us (35 with the partial stage last and its ends
-// loaded an element at a time); there rows that start at any 2 bytes cost the
-// loads (K = 1104: 25 us). fp32, 20480 rows, 5 experts, N = 192, K = 2240: 166
-// us, 106 TFLOP/s.
+// = 777, K = 1111, fp16: 31-33 us by how unevenly the rows fall (with the
+// partial stage last and its ends loaded an element at a time 35.5, where this
+// takes 31.1); K = 1104 in aligned rows, on the ring, takes 27. fp32, 20480 rows,
+// 5 experts, N = 192, K = 2240: 161 us, 109 TFLOP/s; 8192 rows of 4 of 2048 x
+// 2048: 527 us, 130 TFLOP/s.
 //
 // Where there are few outputs a tile is 32 x 32, so that more CUs have one, and
 // its four wavefronts share c: each takes every fourth step of a stage (of

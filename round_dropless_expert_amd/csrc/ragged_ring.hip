@@ -29,10 +29,10 @@
 // of many rows; 256 x 128 and 128 x 64 (ring_kernel) where experts have few
 // rows and a larger tile would multiply rows that do not exist. The small
 // tiles are bound by reading the weights once: 512 rows over 64 experts, N =
-// 4096, K = 1536, bf16 (805 MB of weights) 157 us, 5.2 TB/s; in MXFP4 (214
-// MB) 42 us, 5.2 TB/s. 64-byte stages and four slots there, since three
-// stages in flight cover the memory's latency; the L2's request rate does not
-// matter yet.
+// 4096, K = 1536, bf16 (805 MB of weights) 152-157 us, 5.2 TB/s; in MXFP4 (214
+// MB) 54 us, 4.0 TB/s, and 42 where the last-level cache holds them. 64-byte
+// stages and four slots there, since three stages in flight cover the memory's
+// latency; the L2's request rate does not matter yet.
 #include "ragged_mma.hpp"
 #include "ragged_ring.hpp"
 
@@ -510,12 +510,12 @@ __global__ __launch_bounds__(256, 1) void ring_kernel(RingParams p) {
 // the slot's last step, half in the first step of the next, and have two
 // steps (1024 MFMA cycles) and more to land.
 //
-// 98304 rows over 64 experts, N = 4096, K = 7168: bf16 4.59 ms, 1.26 PFLOP/s,
-// MFMA pipes busy 76% of the cycles at 1.7 GHz (of 2.4: the chip's power
-// limit); MXFP4 1.44 ms, 4.0 PFLOP/s, busy 60% at 1.7 GHz, the rest waits for
-// a slot's loads (1.4e8 requests to the L2: one a CU every 4.6 cycles). The
-// same on 64-byte stages in four slots: 5.01 and 2.02 ms. Input
-// gradient, 32768 rows over 32 experts, N = K = 2048, bf16: 264 us, 1.04
+// 98304 rows over 64 experts, N = 4096, K = 7168: bf16 4.6-4.8 ms, 1.20-1.25
+// PFLOP/s, MFMA pipes busy 76% of the cycles at 1.7 GHz (of 2.4: the chip's
+// power limit); MXFP4 1.44-1.55 ms, 3.7-4.0 PFLOP/s, busy 60% at 1.7 GHz, the
+// rest waits for a slot's loads (1.4e8 requests to the L2: one a CU every 4.6
+// cycles). The same on 64-byte stages in four slots: 5.01 and 2.02 ms. Input
+// gradient, 32768 rows over 32 experts, N = K = 2048, bf16: 264-291 us, 0.94-1.04
 // PFLOP/s.
 template <typename Op, typename Out, bool kTransW, bool kOutVec>
 __global__ __launch_bounds__(256, 1) void wide_ring_kernel(RingParams p) {

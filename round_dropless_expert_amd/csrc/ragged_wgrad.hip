@@ -25,11 +25,15 @@
 // past the first go to slots of the workspace and a second launch adds them
 // in chunk order.
 //
-// 32768 rows over 32 experts, N = K = 2048, bf16: 316 us, 870 TFLOP/s; the
-// slots' addition 13 us more. The MFMA pipes are busy 45% of the cycles. By
+// 32768 rows over 32 experts, N = K = 2048, bf16: 316-349 us, 790-870 TFLOP/s;
+// the slots' addition 13 us more. The MFMA pipes are busy 45% of the cycles. By
 // variants that left work out: the loads cost 85 us (each stage is 32 rows of
 // 512 bytes from two operands, and a tile has only some 32 stages), the
 // store of the fp32 tile 64 us (537 MB of dw in all), the fragment reads 16.
+//
+// Every workgroup orders the experts by E^2 comparisons in LDS, which counts at
+// the most experts: 16384 rows, N = K = 256, 512 experts (134 MB of dw) 64 us,
+// 1024 (268 MB, 56 us at a copy's rate) 177; the general kernel takes 73 and 211.
 #include "ragged_mma.hpp"
 #include "ragged_ring.hpp"
 

@@ -556,11 +556,12 @@ def _matrices(t, name, dtype, shape, dev):
     """Address of a contiguous tensor of at least the elements of shape (...,
     height, width) whose trailing dimensions make rows of that width or whole
     matrices (a plain buffer has none): a transposed layout is refused."""
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype
+            and t.shape == shape and t.is_contiguous()):
+        return t.data_ptr()
     if t is None or isinstance(t, int):
         return t
     _on_device(t, name, dev)
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
     address = _arg(t, name, dtype, math.prod(shape))
     groups = list(itertools.accumulate(reversed(t.shape[1:]), operator.mul))
     if shape[-1] not in groups and any(n < shape[-2] * shape[-1] for n in groups):

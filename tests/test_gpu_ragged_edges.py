@@ -260,3 +260,147 @@ def test_dequantised_values_are_exact_or_infinite(B):
         else:
             assert torch.equal(y[~past], ref[~past].to(el).double())
         assert torch.equal(y[past], torch.copysign(torch.full_like(ref[past], torch.inf), ref[past]))
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("N,K,pad", [(16, 2 ** 20, 0), (2 ** 20, 16, 0), (5, 2 ** 20 - 3, 3),
+                                     (2 ** 20 - 8, 3, 8)])
+def test_the_widest_rows(B, dt, N, K, pad):
+    """Rows of 2^20 elements, the limit: a few of two experts, every product."""
+    el, off = DT[dt], R.offsets_of([2, 0, 70])
+    rows, E = int(off[-1]), 3
+    ld_x, ld_y = (K + pad, N) if K > N else (K, N + pad)
+    x = whole((rows, ld_x), torch.int8, 1).to(el)[:, :K]
+    dy = whole((rows, ld_y), torch.int8, 2).to(el)[:, :N]
+    w = whole((E, N, K), torch.int8, 3).to(el)
+    g = B.grouped(rows, E, N, K, el, ld_x=ld_x, ld_y=ld_y)
+    y = torch.zeros(rows, ld_y, dtype=el, device="cuda")[:, :N]
+    dx = torch.zeros(rows, ld_x, dtype=el, device="cuda")[:, :K]
+    dw = torch.empty(E, N, K, device="cuda")
+    ws = torch.empty(B.grouped_dw_workspace_size(g), dtype=torch.uint8, device="cuda")
+    B.moe_grouped_gemm(g, dev_off(off), x, w, y)
+    B.moe_grouped_gemm_dx(g, dev_off(off), dy, w, dx)
+    B.moe_grouped_gemm_dw(g, dev_off(off), x, dy, dw, ws)
+    assert torch.equal(y, expect(off, x, w, el))
+    assert torch.equal(dx, expect(off, dy, w.transpose(1, 2), el))
+    for e, b, t in R.segments(off):
+        assert torch.equal(dw[e].double(), mm(dy[b:t].t(), x[b:t])), e
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_the_widest_rows_elementwise(B, dt):
+    el, rows, K = DT[dt], 3, 2 ** 20
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    gu = torch.randn(rows, K, generator=gen, device="cuda").to(el)
+    dh = torch.randn(rows, K // 2, generator=gen, device="cuda").to(el)
+    h, dgu = torch.empty_like(dh), torch.empty_like(gu)
+    B.moe_swiglu(gu, h)
+    B.moe_swiglu_backward(gu, dh, dgu)
+    g, u, d = gu[:, : K // 2].double(), gu[:, K // 2:].double(), dh.double()
+    s, r = torch.sigmoid(g), torch.sigmoid(-g)
+    # as for narrow rows: 2^-20 covers the fp32 arithmetic of |g| < 8
+    for got, ref, size in ((h, g * s * u, g * s * u), (dgu[:, K // 2:], d * g * s, d * g * s),
+                           (dgu[:, : K // 2], d * u * s * (1 + g * r),
+                            d * u * s * (1 + (g * r).abs()))):
+        tol = size.abs() * 2.0 ** -20
+        assert ((got.double() - ref).abs() <= tol + R.rounding(ref.abs() + tol, el)).all()
+    codes = torch.empty(rows, K // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(rows, K // 32, dtype=torch.uint8, device="cuda")
+    B.moe_mxfp4_quantize(gu, codes, scales)
+    c, sc = R.codes_of(gu.double().cpu().numpy())
+    assert (R.unpack(codes.cpu().numpy()) == c).all() and (scales.cpu().numpy() == sc).all()
+
+
+def test_three_hundred_million_rows(B):
+    """Row numbers past 2^28 and element numbers past 2^31 in every operator."""
+    rows, K, N, el = 300_000_007, 8, 8, torch.bfloat16
+    off = R.offsets_of([5, 0, rows - 1000, 990], 2)
+    d_off, E, end = dev_off(off), 4, int(off[-1])
+    x = whole((rows, K), torch.int8, 1).to(el)
+    w = whole((E, N, K), el, 2)
+    y = torch.full((rows, N), 77.0, dtype=el, device="cuda")
+    g = B.grouped(rows, E, N, K, el)
+
+    def same(got, a, m):  # got[i] = a[i] m[e]^T, in parts
+        for e, b, t in R.segments(off):
+            for i in range(b, t, 1 << 24):
+                j = min(t, i + (1 << 24))
+                assert torch.equal(got[i:j], (a[i:j].float() @ m[e].float().t()).to(el)), (e, i)
+        assert (got[:2] == 77.0).all() and (got[end:] == 77.0).all()
+
+    B.moe_grouped_gemm(g, d_off, x, w, y)
+    same(y, x, w)
+    y.fill_(77.0)
+    B.moe_grouped_gemm_dx(g, d_off, x, w, y)
+    same(y, x, w.transpose(1, 2).contiguous())
+    # a few rows of dy that are not 0, at both ends of every expert and between
+    y.zero_()
+    some = [2, 6, 7, 8, 2 ** 28 - 1, 2 ** 28, end - 991, end - 990, end - 1]
+    y[some] = whole((len(some), N), el, 3)
+    y[:2] = y[end:] = float("nan")
+    dw = torch.empty(E, N, K, device="cuda")
+    ws = torch.empty(B.grouped_dw_workspace_size(g), dtype=torch.uint8, device="cuda")
+    B.moe_grouped_gemm_dw(g, d_off, x, y, dw, ws)
+    ref = torch.zeros(E, N, K, dtype=torch.float64, device="cuda")
+    for i in some:
+        e = 0 if i < 7 else 2 if i < end - 990 else 3
+        ref[e] += y[i].double().unsqueeze(1) * x[i].double()
+    assert torch.equal(dw.double(), ref)
+    # x as [g, u] of four features
+    h = torch.full((rows, 4), 77.0, dtype=el, device="cuda")
+    B.moe_swiglu(x, h, n_rows=d_off[E:])
+    B.moe_swiglu_backward(x, h, y, n_rows=d_off[E:])
+    for i in (0, 2 ** 28 - 2, end - 64):
+        gg, u, d = (t[i:i + 64].double().cpu() for t in (x[:, :4], x[:, 4:], h))
+        href, du = gg * torch.sigmoid(gg) * u, d * gg * torch.sigmoid(gg)
+        for got, want in ((d, href), (y[i:i + 64, 4:].double().cpu(), du)):
+            tol = want.abs() * 2.0 ** -20
+            assert ((got - want).abs() <= tol + R.rounding(want.abs() + tol, el)).all(), i
+    assert (h[end:] == 77.0).all() and torch.isnan(y[end:]).all()
+    del h, y
+    # the same values as rows of 32, in four bits and back
+    n = rows * K // 32
+    xq = torch.empty(n, 16, dtype=torch.uint8, device="cuda")
+    xs = torch.empty(n, 4, dtype=torch.uint8, device="cuda")
+    x = x.view(-1)[: n * 32].view(n, 32)
+    B.moe_mxfp4_quantize(x, xq, xs)
+    back = torch.empty_like(x)
+    B.moe_mxfp4_dequantize(xq, xs, back)
+    assert torch.equal(back, x)  # -2 to 2 are 4-bit values under the scale 2^-1
+
+
+def test_two_threads_on_two_streams(B):
+    """Calls that overlap in time, each with outputs and a workspace of its own."""
+    import threading
+    el, c, N, K = torch.bfloat16, [3000, 0, 1500, 4], 264, 520
+    off = R.offsets_of(c)
+    rows, E, d_off = int(off[-1]), len(c), dev_off(off)
+    g = B.grouped(rows, E, N, K, el)
+    size = B.grouped_dw_workspace_size(g)
+    sets = []
+    for seed in (1, 2):
+        sets.append(dict(
+            x=whole((rows, K), el, seed), dy=whole((rows, N), el, seed + 2),
+            w=whole((E, N, K), el, seed + 4), y=torch.zeros(rows, N, dtype=el, device="cuda"),
+            dx=torch.zeros(rows, K, dtype=el, device="cuda"), dw=torch.zeros(E, N, K, device="cuda"),
+            ws=torch.empty(size, dtype=torch.uint8, device="cuda"), st=torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def calls(s):
+        with torch.cuda.stream(s["st"]):
+            for _ in range(20):
+                B.moe_grouped_gemm(g, d_off, s["x"], s["w"], s["y"])
+                B.moe_grouped_gemm_dx(g, d_off, s["dy"], s["w"], s["dx"])
+                B.moe_grouped_gemm_dw(g, d_off, s["x"], s["dy"], s["dw"], s["ws"])
+
+    threads = [threading.Thread(target=calls, args=(s,)) for s in sets]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for s in sets:
+        assert torch.equal(s["y"], expect(off, s["x"], s["w"], el))
+        assert torch.equal(s["dx"], expect(off, s["dy"], s["w"].transpose(1, 2), el))
+        for e, b, t in R.segments(off):
+            assert torch.equal(s["dw"][e].double(), mm(s["dy"][b:t].t(), s["x"][b:t]))

@@ -618,6 +618,145 @@ moe_status_t moe_mxfp4_grouped_gemm(const moe_grouped_t *g,
                                     const uint8_t *w_scales, void *y,
                                     void *stream);
 
+/* ------------------------------------------------------------------------
+ * Around the experts' products: routing to up to 1024 experts with its
+ * gradient, the sort of its assignments into expert order, the sum of the
+ * experts' outputs back to tokens with its gradients, rows and products in
+ * 8-bit integers, and the orthogonalised update of the experts' matrices.
+ * As the ragged operators: no call allocates, waits or keeps state, each can
+ * be captured into a graph, and calls of the same shape repeat bit for bit.
+ * Calls that may overlap in time need a workspace each. */
+
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
+
+/* A router. logits: elem [T][E], rows ld elements apart (0: E). Limits: E <=
+ * 1024, k <= 64, groups <= 64, T*k < 2^31, ld <= 2^20. */
+typedef struct {
+  int64_t T;           /* tokens */
+  int32_t E, k;        /* experts, experts per token */
+  int32_t dtype;       /* moe_dtype_t of logits (and of dlogits) */
+  int32_t score;       /* moe_score_t */
+  int32_t groups;      /* groups of E / groups neighbouring experts (0: 1) */
+  int32_t top_groups;  /* groups a token may choose from (0: all) */
+  int32_t group_top;   /* 1 or 2: best experts that make a group's score (0: 2) */
+  int32_t renormalize; /* 1: a token's weights are divided by their sum */
+  float scale;         /* factor of the weights, finite */
+  int64_t ld;
+} moe_router_t;
+
+/* Scores s_e = softmax(l)_e or 1 / (1 + exp(-l_e)); choice c_e = s_e +
+ * bias[e] (bias: float [E], or NULL for none: it steers the choice and is no
+ * part of the weights). With groups > 1 a group's score is the sum of its
+ * group_top best c, and only experts of the top_groups best groups can be
+ * chosen. idx[t][j]: the expert of the j-th largest c, weight[t][j] = scale
+ * s_j, or scale s_j / sum of the token's chosen s. Both are contiguous [T][k].
+ * Equal ones go to the lower index, among groups too; c and the groups' sums
+ * are compared as fp64 arithmetic gives them, and without a bias experts rank
+ * by their logits. An expert whose logit is -inf or NaN, or whose c is -inf or
+ * NaN, ranks behind all others; its score is 0 where the logit is -inf or NaN.
+ * A token always gets k distinct experts; weights that nothing is left for
+ * (all k scores 0) are 0. k <= top_groups * (E / groups). */
+moe_status_t moe_route(const moe_router_t *r, const void *logits,
+                       const float *bias, int32_t *idx, float *weight,
+                       void *stream);
+
+/* The gradient of the weights with respect to the logits, for the choice idx
+ * (which passes none), given dweight [T][k]: dlogits, elem [T][E] at r->ld,
+ * written in full. A token's experts are distinct, as moe_route gives them; an
+ * idx outside [0, E) counts as not chosen. */
+moe_status_t moe_route_backward(const moe_router_t *r, const void *logits,
+                                const int32_t *idx, const float *dweight,
+                                void *dlogits, void *stream);
+
+/* Assignments into expert order: idx [n] (n = T*k, assignment a = t*k + j) is
+ * sorted by expert, stably. perm [n]: assignment ids in that order; pos [n]:
+ * its inverse; offsets [E + 1]: where each expert's begin, as the ragged
+ * operators take them. An assignment whose idx lies outside [0, E) is nobody's
+ * (the padding of a batch): its pos is -1, and perm ends with a -1 for each.
+ * ws: moe_sort_workspace_size bytes (may be 0), 16-byte aligned. n < 2^31, E <=
+ * 1024. */
+moe_status_t moe_sort_workspace_size(int64_t n, int32_t E, size_t *bytes);
+moe_status_t moe_sort(int64_t n, int32_t E, const int32_t *idx, int32_t *perm,
+                      int32_t *pos, int32_t *offsets, void *ws, size_t ws_bytes,
+                      void *stream);
+
+/* y[t] = sum over j of weight[t][j] z[pos[t][j]], j ascending, in fp32, rounded
+ * once: the experts' outputs back to tokens. z: elem [rows][d] at ld_z; y: elem
+ * [T][d] at ld_y; pos int32 [T][k], weight float [T][k] (NULL: all 1: the
+ * gradient of a gather into expert order). A pos outside [0, rows) adds
+ * nothing. d, ld <= 2^20, T*k < 2^31, rows < 2^31. */
+moe_status_t moe_collect(int32_t dtype, int64_t T, int32_t k, int64_t rows,
+                         int64_t d, const void *z, int64_t ld_z,
+                         const int32_t *pos, const float *weight, void *y,
+                         int64_t ld_y, void *stream);
+
+/* Its gradients: dz[pos[t][j]] = weight[t][j] dy[t] and dweight[t][j] = <z[pos[t]
+ * [j]], dy[t]> (0 where pos names no row; summed in fp32). Either may be NULL;
+ * z is read for dweight alone. Rows of dz that no pos names keep what they
+ * held, so with weight NULL this gathers tokens into expert order; positions
+ * are distinct. */
+moe_status_t moe_collect_backward(int32_t dtype, int64_t T, int32_t k,
+                                  int64_t rows, int64_t d, const void *dy,
+                                  int64_t ld_dy, const void *z, int64_t ld_z,
+                                  const int32_t *pos, const float *weight,
+                                  void *dz, int64_t ld_dz, float *dweight,
+                                  void *stream);
+
+/* 8-bit integers. A row of K values is
+ *   codes  int8, moe_int8_stride(K) of them (K rounded up to 16; -1 for an
+ *          invalid K); those past K are written as 0 and have to be 0
+ *   scale  one float: the values are the codes times it
+ * Code rows are contiguous, their arrays 16-byte aligned. */
+int64_t moe_int8_stride(int64_t K);
+
+/* elem rows to 8 bits: scale = max|x| / 127 (rounded to fp32), codes 127 x /
+ * max|x| rounded to the nearest integer, ties to even, without an error before
+ * that rounding; a row of zeros has scale 0. A row with an infinity or a NaN
+ * gets a NaN scale and codes 0. index, index_div, src_rows and n_rows as for
+ * moe_mxfp4_quantize (a row of no source: zeros, scale 0). Weights [E][N][K]
+ * are E*N rows: a scale for each output channel. */
+moe_status_t moe_int8_quantize(int32_t dtype, int64_t rows, int64_t K,
+                               const void *x, int64_t ld_x, int64_t src_rows,
+                               const int32_t *index, int32_t index_div,
+                               const int32_t *n_rows, int8_t *codes,
+                               float *scales, void *stream);
+
+/* The values, rounded to elem. */
+moe_status_t moe_int8_dequantize(int32_t dtype, int64_t rows, int64_t K,
+                                 const int8_t *codes, const float *scales,
+                                 void *y, int64_t ld_y, const int32_t *n_rows,
+                                 void *stream);
+
+/* moe_grouped_gemm on such rows: x of g->rows rows, w of E*N. The products are
+ * summed exactly (int32), then y[i][n] = sum * x_scale[i] * w_scale[e][n] in fp32,
+ * rounded to g->dtype; a NaN scale makes its row or column NaN. K < 2^17; g->ld_x
+ * 0 or K. */
+moe_status_t moe_int8_grouped_gemm(const moe_grouped_t *g,
+                                   const int32_t *offsets,
+                                   const int8_t *x_codes, const float *x_scales,
+                                   const int8_t *w_codes, const float *w_scales,
+                                   void *y, void *stream);
+
+/* Orthogonalised updates: the step that the Muon optimiser takes from a
+ * matrix's gradient (or its momentum), for E matrices g elem [E][N][K] at once,
+ * such as the fp32 weight gradients of moe_grouped_gemm_dw and moe_backward.
+ * Each is divided by its Frobenius norm plus 1e-20, then `steps` times replaced
+ * by a X + b (X X^T) X + c (X X^T)^2 X; y = scale times the result, bfloat16
+ * [E][N][K] (may not overlap g). coefficients: host memory, steps x {a, b, c},
+ * or NULL for {3.4445, -4.7750, 2.0315} in every step. The products run on the
+ * matrix cores on fp16 values (11 bits), scaled where they are small, with fp32
+ * accumulation: each element's error stays below the rounding of y for
+ * gradients of usual spectra. A matrix of zeros gives zeros; one with an
+ * infinity or a NaN gives NaN throughout. Limits: steps <= 32, N, K <= 16384,
+ * E <= 1024; coefficients that let the singular values grow past 32 can leave
+ * fp16's range. ws: moe_orthogonalize_workspace_size bytes, 16-byte aligned. */
+moe_status_t moe_orthogonalize_workspace_size(int32_t E, int32_t N, int32_t K,
+                                              size_t *bytes);
+moe_status_t moe_orthogonalize(int32_t dtype, int32_t E, int32_t N, int32_t K,
+                               const void *g, void *y, int32_t steps,
+                               const float *coefficients, float scale, void *ws,
+                               size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

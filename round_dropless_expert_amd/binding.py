@@ -30,6 +30,9 @@ MOE_F32 = 0
 MOE_BF16 = 1
 MOE_F16 = 2  # ragged expert operators only
 
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+
 MOE_WEIGHTS_ROW_MAJOR = 0
 MOE_WEIGHTS_TILED = 1
 
@@ -45,7 +48,11 @@ EXPORTS = ("moe_status_string", "moe_last_error", "moe_hip_runtime_version",
            "moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw",
            "moe_grouped_dw_workspace_size", "moe_swiglu", "moe_swiglu_backward",
            "moe_mxfp4_scale_stride", "moe_mxfp4_quantize", "moe_mxfp4_dequantize",
-           "moe_mxfp4_grouped_gemm")
+           "moe_mxfp4_grouped_gemm",
+           "moe_route", "moe_route_backward", "moe_sort_workspace_size", "moe_sort",
+           "moe_collect", "moe_collect_backward", "moe_int8_stride", "moe_int8_quantize",
+           "moe_int8_dequantize", "moe_int8_grouped_gemm",
+           "moe_orthogonalize_workspace_size", "moe_orthogonalize")
 
 
 class MoeConfig(ctypes.Structure):
@@ -79,6 +86,14 @@ class MoeGrouped(ctypes.Structure):
                 ("N", ctypes.c_int32), ("K", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("ld_x", ctypes.c_int64),
                 ("ld_y", ctypes.c_int64)]
+
+
+class MoeRouter(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("ld", ctypes.c_int64)]
 
 
 class MoeError(RuntimeError):
@@ -146,6 +161,28 @@ def load() -> ctypes.CDLL:
     L.moe_mxfp4_quantize.argtypes = [i32, i64, i64, vp, i64, i64, vp, i32, vp, vp, vp, vp]
     L.moe_mxfp4_dequantize.argtypes = [i32, i64, i64, vp, vp, vp, i64, vp, vp]
     L.moe_mxfp4_grouped_gemm.argtypes = [gp, vp, vp, vp, vp, vp, vp, vp]
+    rp = ctypes.POINTER(MoeRouter)
+    szp = ctypes.POINTER(ctypes.c_size_t)
+    L.moe_route.argtypes = [rp, vp, vp, vp, vp, vp]
+    L.moe_route_backward.argtypes = [rp, vp, vp, vp, vp, vp]
+    L.moe_sort_workspace_size.argtypes = [i64, i32, szp]
+    L.moe_sort.argtypes = [i64, i32, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_collect.argtypes = [i32, i64, i32, i64, i64, vp, i64, vp, vp, vp, i64, vp]
+    L.moe_collect_backward.argtypes = [i32, i64, i32, i64, i64, vp, i64, vp, i64, vp, vp, vp,
+                                       i64, vp, vp]
+    L.moe_int8_stride.argtypes = [i64]
+    L.moe_int8_stride.restype = i64
+    L.moe_int8_quantize.argtypes = [i32, i64, i64, vp, i64, i64, vp, i32, vp, vp, vp, vp]
+    L.moe_int8_dequantize.argtypes = [i32, i64, i64, vp, vp, vp, i64, vp, vp]
+    L.moe_int8_grouped_gemm.argtypes = [gp, vp, vp, vp, vp, vp, vp, vp]
+    L.moe_orthogonalize_workspace_size.argtypes = [i32, i32, i32, szp]
+    L.moe_orthogonalize.argtypes = [i32, i32, i32, i32, vp, vp, i32, vp, ctypes.c_float, vp, sz,
+                                    vp]
+    for n in ("moe_route", "moe_route_backward", "moe_sort_workspace_size", "moe_sort",
+              "moe_collect", "moe_collect_backward", "moe_int8_quantize",
+              "moe_int8_dequantize", "moe_int8_grouped_gemm",
+              "moe_orthogonalize_workspace_size", "moe_orthogonalize"):
+        getattr(L, n).restype = ctypes.c_int
     for n in ("moe_grouped_gemm", "moe_grouped_gemm_dx", "moe_grouped_gemm_dw",
               "moe_grouped_dw_workspace_size", "moe_swiglu", "moe_swiglu_backward",
               "moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_grouped_gemm",
@@ -658,13 +695,7 @@ def moe_grouped_gemm_dw(g, offsets, x, dy, dw, ws=None, accumulate=False, stream
     with accumulate; ws: grouped_dw_workspace_size bytes (None if 0)."""
     el, ld_x, ld_y = _grouped_dims(g)
     rows, E, N, K, dev = g.rows, g.E, g.N, g.K, torch.cuda.current_device()
-    w_ptr, w_bytes = None, 0
-    if ws is not None:
-        _on_device(ws, "ws", dev)
-        if not ws.is_contiguous():
-            raise ValueError("ws: must be contiguous")
-        w_bytes = _nbytes(ws)
-        w_ptr = ws.data_ptr() if w_bytes else None  # an empty tensor has no address
+    w_ptr, w_bytes = _workspace(ws, dev)
     _check(load().moe_grouped_gemm_dw(
         g, _offsets(offsets, E, dev), _mat(x, "x", el, rows, K, ld_x, dev),
         _mat(dy, "dy", el, rows, N, ld_y, dev),
@@ -739,6 +770,222 @@ def moe_mxfp4_grouped_gemm(g, offsets, x_codes, x_scales, w_codes, w_scales, y,
         _matrices(w_codes, "w_codes", u8, (E, N, K // 2), dev),
         _matrices(w_scales, "w_scales", u8, (E, N, S), dev),
         _mat(y, "y", el, rows, N, ld_y, dev), _call_stream(stream, dev)))
+
+
+# ---------------------------------------------------------------------------
+# Around the experts' products (the header's section of that name): routing, the
+# sort of its assignments, the sum of the outputs back to tokens, 8-bit integers
+# and the orthogonalised update.
+
+_SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+
+
+def router(T, E, k, dtype="f32", score="softmax", groups=1, top_groups=0, group_top=0,
+           renormalize=True, scale=1.0, ld=0) -> MoeRouter:
+    """A router of T tokens to k of E experts. dtype and ld: of the logits
+    (rows ld elements apart, 0: E). A token chooses from the top_groups best
+    (0: all) of `groups` groups of neighbouring experts; a group's score is
+    the sum of its group_top (1 or 2; 0: 2) best choice scores."""
+    if isinstance(dtype, str):
+        dtype = {"f32": MOE_F32, "bf16": MOE_BF16, "f16": MOE_F16}[dtype]
+    elif isinstance(dtype, torch.dtype):
+        dtype = _DTYPES[dtype]
+    if isinstance(score, str):
+        score = _SCORES[score]
+    for v, name in ((E, "E"), (k, "k"), (groups, "groups"), (top_groups, "top_groups"),
+                    (group_top, "group_top")):
+        _int32(v, name)
+    return MoeRouter(int(T), int(E), int(k), int(dtype), int(score), int(groups),
+                     int(top_groups), int(group_top), 1 if renormalize else 0, float(scale),
+                     int(ld))
+
+
+def _router_dims(r):
+    if r.dtype not in _TORCH_DTYPES:
+        raise ValueError(f"unknown dtype {r.dtype}")
+    return _TORCH_DTYPES[r.dtype], r.T, r.E, r.k, r.ld or r.E
+
+
+def moe_route(r, logits, idx, weight, bias=None, stream=None):
+    """logits [T, E] to idx int32 [T, k] and weight float32 [T, k]; bias
+    float32 [E] steers the choice alone."""
+    el, T, E, k, ld = _router_dims(r)
+    dev = torch.cuda.current_device()
+    _check(load().moe_route(
+        r, _mat(logits, "logits", el, T, E, ld, dev),
+        None if bias is None else _dense(bias, "bias", torch.float32, E, dev),
+        _matrices(idx, "idx", torch.int32, (T, k), dev),
+        _matrices(weight, "weight", torch.float32, (T, k), dev), _call_stream(stream, dev)))
+
+
+def moe_route_backward(r, logits, idx, dweight, dlogits, stream=None):
+    """dlogits [T, E] (rows r.ld apart, as the logits) from dweight [T, k]."""
+    el, T, E, k, ld = _router_dims(r)
+    dev = torch.cuda.current_device()
+    _check(load().moe_route_backward(
+        r, _mat(logits, "logits", el, T, E, ld, dev),
+        _matrices(idx, "idx", torch.int32, (T, k), dev),
+        _matrices(dweight, "dweight", torch.float32, (T, k), dev),
+        _mat(dlogits, "dlogits", el, T, E, ld, dev), _call_stream(stream, dev)))
+
+
+def sort_workspace_size(n: int, E: int) -> int:
+    """Workspace of moe_sort for n assignments."""
+    b = ctypes.c_size_t(0)
+    _check(load().moe_sort_workspace_size(int(n), _int32(E, "E"), ctypes.byref(b)))
+    return b.value
+
+
+def _workspace(ws, dev):
+    """(address, bytes) of a workspace tensor, or of none."""
+    if ws is None:
+        return None, 0
+    _on_device(ws, "ws", dev)
+    if not ws.is_contiguous():
+        raise ValueError("ws: must be contiguous")
+    size = _nbytes(ws)
+    return (ws.data_ptr() if size else None), size  # an empty tensor has no address
+
+
+def moe_sort(idx, E, perm, pos, offsets, ws=None, stream=None):
+    """Assignments idx (int32, all its elements) by expert: perm and pos int32
+    of as many elements, offsets int32 [E + 1]; ws: sort_workspace_size bytes
+    (None if 0)."""
+    dev = torch.cuda.current_device()
+    i32 = torch.int32
+    _on_device(idx, "idx", dev)
+    n = idx.numel()
+    w_ptr, w_bytes = _workspace(ws, dev)
+    _check(load().moe_sort(n, _int32(E, "E"), _dense(idx, "idx", i32, n, dev),
+                           _dense(perm, "perm", i32, n, dev), _dense(pos, "pos", i32, n, dev),
+                           _offsets(offsets, E, dev), w_ptr, w_bytes, _call_stream(stream, dev)))
+
+
+def _positions(pos, T, dev):
+    """k and the address of pos [T, k]."""
+    _on_device(pos, "pos", dev)
+    if pos.dim() != 2 or pos.shape[0] != T:
+        raise ValueError(f"pos: shape {tuple(pos.shape)}, expected ({T}, k)")
+    k = pos.shape[1]
+    return k, _dense(pos, "pos", torch.int32, T * k, dev)
+
+
+def moe_collect(z, pos, y, weight=None, stream=None):
+    """y[t] = sum over j of weight[t, j] z[pos[t, j]]: z [rows, d], pos int32
+    [T, k], y [T, d], weight float32 [T, k] (None: all 1)."""
+    dev = torch.cuda.current_device()
+    dt, T, d, ld_y = _rows_of(y, "y", dev)
+    z_dt, rows, _, ld_z = _rows_of(z, "z", dev)
+    z_ptr, _ = _pair_of(z, "z", dt, rows, d, dev)
+    k, pos_ptr = _positions(pos, T, dev)
+    w_ptr = None if weight is None else _matrices(weight, "weight", torch.float32, (T, k), dev)
+    _check(load().moe_collect(_DTYPES[dt], T, k, rows, d, z_ptr, ld_z, pos_ptr, w_ptr,
+                              y.data_ptr(), ld_y, _call_stream(stream, dev)))
+
+
+def moe_collect_backward(dy, pos, dz=None, weight=None, z=None, dweight=None, stream=None):
+    """dz[pos[t, j]] = weight[t, j] dy[t] and, where dweight [T, k] is given,
+    dweight[t, j] = <z[pos[t, j]], dy[t]>: dy [T, d], dz and z [rows, d]. With
+    weight None, dz is a gather of dy's rows."""
+    dev = torch.cuda.current_device()
+    dt, T, d, ld_dy = _rows_of(dy, "dy", dev)
+    k, pos_ptr = _positions(pos, T, dev)
+    if dweight is not None and z is None:
+        raise ValueError("dweight needs z")
+    if dz is None and dweight is None:
+        raise ValueError("neither dz nor dweight is given")
+    rows = (dz if dz is not None else z).shape[0]
+    dz_ptr, ld_dz = (None, 0) if dz is None else _pair_of(dz, "dz", dt, rows, d, dev)
+    z_ptr, ld_z = (None, 0) if z is None else _pair_of(z, "z", dt, rows, d, dev)
+    f32 = torch.float32
+    _check(load().moe_collect_backward(
+        _DTYPES[dt], T, k, rows, d, dy.data_ptr(), ld_dy, z_ptr, ld_z, pos_ptr,
+        None if weight is None else _matrices(weight, "weight", f32, (T, k), dev), dz_ptr, ld_dz,
+        None if dweight is None else _matrices(dweight, "dweight", f32, (T, k), dev),
+        _call_stream(stream, dev)))
+
+
+def int8_stride(K: int) -> int:
+    """Codes of a row of 8-bit integers."""
+    if not 1 <= K <= 2**20:
+        raise ValueError(f"K = {K} must lie in [1, 2^20]")
+    return (K + 15) // 16 * 16
+
+
+def moe_int8_quantize(x, codes, scales, index=None, index_div=1, n_rows=None, stream=None):
+    """Rows of x [src_rows, K] to 8-bit integers: codes int8 [...,
+    int8_stride(K)] and scales float32 [...], contiguous; rows, index and
+    index_div as for moe_mxfp4_quantize."""
+    dev = torch.cuda.current_device()
+    if isinstance(x, torch.Tensor) and x.dim() > 2 and x.is_contiguous():
+        x = x.view(-1, x.shape[-1])
+    dt, src, K, ld_x = _rows_of(x, "x", dev)
+    rows, index_ptr = src, None
+    if index is not None:
+        rows = index.numel()
+        index_ptr = _dense(index, "index", torch.int32, rows, dev)
+    _check(load().moe_int8_quantize(
+        _DTYPES[dt], rows, K, x.data_ptr(), ld_x, src, index_ptr, _int32(index_div, "index_div"),
+        _n_rows(n_rows, dev), _matrices(codes, "codes", torch.int8, (rows, int8_stride(K)), dev),
+        _dense(scales, "scales", torch.float32, rows, dev), _call_stream(stream, dev)))
+
+
+def moe_int8_dequantize(codes, scales, y, n_rows=None, stream=None):
+    """The values of codes and scales, y [rows, K]."""
+    dev = torch.cuda.current_device()
+    dt, rows, K, ld_y = _rows_of(y, "y", dev)
+    _check(load().moe_int8_dequantize(
+        _DTYPES[dt], rows, K, _matrices(codes, "codes", torch.int8, (rows, int8_stride(K)), dev),
+        _dense(scales, "scales", torch.float32, rows, dev), y.data_ptr(), ld_y,
+        _n_rows(n_rows, dev), _call_stream(stream, dev)))
+
+
+def moe_int8_grouped_gemm(g, offsets, x_codes, x_scales, w_codes, w_scales, y, stream=None):
+    """moe_grouped_gemm on 8-bit rows: x_codes [rows, S], x_scales [rows],
+    w_codes [E, N, S], w_scales [E, N] with S = int8_stride(K); y has g's dtype."""
+    el, _, ld_y = _grouped_dims(g)
+    rows, E, N, K, dev = g.rows, g.E, g.N, g.K, torch.cuda.current_device()
+    S, i8, f32 = int8_stride(K), torch.int8, torch.float32
+    _check(load().moe_int8_grouped_gemm(
+        g, _offsets(offsets, E, dev), _matrices(x_codes, "x_codes", i8, (rows, S), dev),
+        _dense(x_scales, "x_scales", f32, rows, dev),
+        _matrices(w_codes, "w_codes", i8, (E, N, S), dev),
+        _matrices(w_scales, "w_scales", f32, (E, N), dev),
+        _mat(y, "y", el, rows, N, ld_y, dev), _call_stream(stream, dev)))
+
+
+def orthogonalize_workspace_size(E: int, N: int, K: int) -> int:
+    """Workspace of moe_orthogonalize for E matrices [N, K]."""
+    b = ctypes.c_size_t(0)
+    _check(load().moe_orthogonalize_workspace_size(_int32(E, "E"), _int32(N, "N"),
+                                                   _int32(K, "K"), ctypes.byref(b)))
+    return b.value
+
+
+def moe_orthogonalize(g, y, ws, steps=5, coefficients=None, scale=1.0, stream=None):
+    """The orthogonalised update of the matrices g [E, N, K] (or one [N, K]):
+    y bfloat16 of the same shape. coefficients: `steps` triples (a, b, c), or
+    None for the usual ones."""
+    dev = torch.cuda.current_device()
+    _on_device(g, "g", dev)
+    if g.dim() not in (2, 3) or g.dtype not in _DTYPES:
+        raise ValueError(f"g: shape {tuple(g.shape)}, dtype {g.dtype}: expected float matrices")
+    if not g.is_contiguous():
+        raise ValueError("g: must be contiguous")
+    E, N, K = (1, *g.shape) if g.dim() == 2 else g.shape
+    _on_device(y, "y", dev)
+    if y.shape != g.shape or y.dtype is not torch.bfloat16 or not y.is_contiguous():
+        raise ValueError(f"y: expected contiguous bfloat16 of shape {tuple(g.shape)}")
+    c = None
+    if coefficients is not None:
+        flat = [float(v) for triple in coefficients for v in triple]
+        if len(flat) != 3 * steps:
+            raise ValueError(f"coefficients: expected {steps} triples")
+        c = (ctypes.c_float * len(flat))(*flat)
+    w_ptr, w_bytes = _workspace(ws, dev)
+    _check(load().moe_orthogonalize(_DTYPES[g.dtype], E, N, K, g.data_ptr(), y.data_ptr(),
+                                    _int32(steps, "steps"), c, float(scale), w_ptr, w_bytes,
+                                    _call_stream(stream, dev)))
 
 
 def workspace_views(cfg: MoeConfig, ws: torch.Tensor) -> dict:

@@ -24,9 +24,11 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["route_plan.hip", "dispatch_combine.hip", "grouped_gemm.hip",
            "wgrad.hip", "backward.hip", "api.hip", "ragged_gemm.hip", "ragged_ring.hip",
            "ragged_skinny.hip", "ragged_wgrad.hip", "swiglu.hip", "mxfp4.hip",
-           "ragged_api.hip"]
+           "ragged_api.hip", "router.hip", "sort.hip", "collect.hip", "int8.hip",
+           "orthogonalize.hip", "router_api.hip"]
 HEADERS = ["device_common.hpp", "launch.hpp", "api_common.hpp", "ragged.hpp",
-           "ragged_device.hpp", "ragged_mma.hpp", "ragged_operand.hpp", "ragged_ring.hpp"]
+           "ragged_device.hpp", "ragged_mma.hpp", "ragged_operand.hpp", "ragged_ring.hpp",
+           "ragged_checks.hpp", "ring_body.hpp", "router.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,86 +1,14 @@
 // C ABI of the ragged expert operators: argument checks and launches. No
 // call allocates, waits or keeps state, so every one of them can be captured
 // into a graph.
-#include "api_common.hpp"
-#include "ragged.hpp"
+#include "ragged_checks.hpp"
 
 namespace {
 
-using moe::api_fail;
-using moe::ElemType;
-
-constexpr int64_t k2G = int64_t(1) << 31;
-// Output tiles of one launch (of 128 x 128): its grid's threads stay below 2^32.
-constexpr int64_t kMaxTiles = int64_t(1) << 23;
-
-int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-moe_status_t check_dtype(int32_t dtype, ElemType* out) {
-  switch (dtype) {
-    case MOE_F32: *out = ElemType::kF32; return MOE_OK;
-    case MOE_BF16: *out = ElemType::kBF16; return MOE_OK;
-    case MOE_F16: *out = ElemType::kF16; return MOE_OK;
-  }
-  return api_fail(MOE_ERR_INVALID_ARGUMENT, "unknown dtype");
-}
-
-moe_status_t check_ptr(const void* p, const char* name, size_t align) {
-  if (!p) return api_fail(MOE_ERR_INVALID_ARGUMENT, "is NULL", name);
-  if (reinterpret_cast<uintptr_t>(p) % align)
-    return api_fail(MOE_ERR_INVALID_ARGUMENT,
-                    align == 16 ? "must be 16-byte aligned" : "must be aligned to its element",
-                    name);
-  return MOE_OK;
-}
-
-// A leading dimension (0: the width) of rows of `width` elements.
-moe_status_t check_ld(int64_t ld, int64_t width, const char* name, int64_t* out) {
-  *out = ld == 0 ? width : ld;
-  if (*out < width)
-    return api_fail(MOE_ERR_INVALID_ARGUMENT, "is below the row's width (0 means the width)",
-                    name);
-  if (*out > moe::kRaggedMaxWidth)
-    return api_fail(MOE_ERR_UNSUPPORTED, "is above 2^20 elements", name);
-  return MOE_OK;
-}
-
-moe_status_t check_grouped(const moe_grouped_t* g, moe::RaggedShape* s) {
-  if (!g) return api_fail(MOE_ERR_INVALID_ARGUMENT, "config is NULL");
-  if (g->rows < 0) return api_fail(MOE_ERR_INVALID_ARGUMENT, "rows must be >= 0");
-  if (g->E < 1) return api_fail(MOE_ERR_INVALID_ARGUMENT, "E must be >= 1");
-  if (g->N < 1 || g->K < 1) return api_fail(MOE_ERR_INVALID_ARGUMENT, "N and K must be >= 1");
-  moe_status_t st = check_dtype(g->dtype, &s->type);
-  if (st != MOE_OK) return st;
-  if (g->E > moe::kRaggedMaxExperts)
-    return api_fail(MOE_ERR_UNSUPPORTED, "E > 1024 is not supported");
-  if (g->rows >= k2G) return api_fail(MOE_ERR_UNSUPPORTED, "rows must be < 2^31");
-  if ((st = check_ld(g->ld_x, g->K, "ld_x", &s->ld_x)) != MOE_OK) return st;
-  if ((st = check_ld(g->ld_y, g->N, "ld_y", &s->ld_y)) != MOE_OK) return st;
-  // fp32 for every type: the weight gradient's matrices are fp32
-  if ((int64_t)g->N * g->K * 4 >= k2G)
-    return api_fail(MOE_ERR_UNSUPPORTED, "N*K must be < 2^29");
-  const int64_t tn = div_up(g->N, 128), tk = div_up(g->K, 128);
-  s->rows = g->rows;
-  s->E = g->E;
-  s->N = g->N;
-  s->K = g->K;
-  if ((g->rows / 128 + g->E) * (tn > tk ? tn : tk) >= kMaxTiles ||
-      (moe::dw_split(*s).slots + g->E) * tn * tk >= kMaxTiles)
-    return api_fail(MOE_ERR_UNSUPPORTED, "more than 2^23 output tiles of 128 x 128");
-  return MOE_OK;
-}
+using namespace moe;
 
 size_t dw_bytes(const moe::RaggedShape& s) {
   return (size_t)moe::dw_split(s).slots * (size_t)s.N * (size_t)s.K * 4;
-}
-
-moe_status_t check_rows(int64_t rows, int64_t width) {
-  if (rows < 0) return api_fail(MOE_ERR_INVALID_ARGUMENT, "rows must be >= 0");
-  if (width < 1) return api_fail(MOE_ERR_INVALID_ARGUMENT, "the row's width must be >= 1");
-  if (rows >= k2G) return api_fail(MOE_ERR_UNSUPPORTED, "rows must be < 2^31");
-  if (width > moe::kRaggedMaxWidth)
-    return api_fail(MOE_ERR_UNSUPPORTED, "the row's width is above 2^20 elements");
-  return MOE_OK;
 }
 
 moe_status_t check_mx_width(int64_t K) {
@@ -88,18 +16,6 @@ moe_status_t check_mx_width(int64_t K) {
     return api_fail(MOE_ERR_INVALID_ARGUMENT, "K must be a multiple of 32");
   return MOE_OK;
 }
-
-#define MOE_TRY(call)                    \
-  do {                                   \
-    const moe_status_t _s = (call);      \
-    if (_s != MOE_OK) return _s;         \
-  } while (0)
-
-#define MOE_LAUNCH(call, where)                                      \
-  do {                                                               \
-    const hipError_t _e = (call);                                    \
-    return _e == hipSuccess ? MOE_OK : moe::api_hip_fail(_e, where); \
-  } while (0)
 
 }  // namespace
 

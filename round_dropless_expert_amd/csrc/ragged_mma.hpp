@@ -61,6 +61,29 @@ __device__ __forceinline__ float acc_read(float a) {
   return v;
 }
 
+__device__ __forceinline__ int acc_read(int a) {
+  int v;
+  asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
+  return v;
+}
+
+// What a sum is multiplied by before it is stored: nothing, or a scale of its
+// row and one of its column (floats, from the tile's first on; reads past the
+// last return zeros).
+struct NoScale {
+  static constexpr bool kOn = false;
+};
+struct RowColScale {
+  static constexpr bool kOn = true;
+  __amdgpu_buffer_rsrc_t rows, cols;
+  __device__ __forceinline__ float row(int r) const {
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rows, r * 4, 0, 0));
+  }
+  __device__ __forceinline__ f32x4 col4(int c) const {
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(cols, c * 4, 0, 0));
+  }
+};
+
 // A wavefront's part of a tile's output: rows of `out` (ldo bytes apart, mr of
 // them in the tile), columns n0 .. of B. Lane (l32, half) holds, for row l32
 // of a 32-row block, columns 8 q + 4 half + 0..3 of each 32-column block. The
@@ -70,10 +93,11 @@ __device__ __forceinline__ float acc_read(float a) {
 // conflicts. kAdd: added to what is there. (The accumulators are read by
 // asm: the caller gives the last MFMAs the wait states that the compiler
 // cannot see.)
-template <typename Out, int WI, int WJ, bool kVec, bool kAdd, int kPolicy>
-__device__ __forceinline__ void store_tile(const f32x16 (&acc)[WI][WJ], char* stg, char* out,
+template <typename Out, int WI, int WJ, bool kVec, bool kAdd, int kPolicy, typename Acc,
+          typename Scale = NoScale>
+__device__ __forceinline__ void store_tile(const Acc (&acc)[WI][WJ], char* stg, char* out,
                                            uint32_t ldo, int mr, int B, int n0, int wn, int wm,
-                                           int lane) {
+                                           int lane, const Scale& scale = Scale()) {
   constexpr int BN = 64 * WI, BM = 64 * WJ;
   constexpr int kOs = sizeof(Out), kPerBlk = kOs == 2 ? 2 : 1;  // 32-column blocks
   constexpr int kChunk = 16 / kOs;
@@ -83,9 +107,16 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[WI][WJ], char* st
   const __amdgpu_buffer_rsrc_t ro = __builtin_amdgcn_make_buffer_rsrc(
       (void*)out, 0, (int)((uint32_t)(mr - 1) * ldo + (uint32_t)B * kOs), kRsrcWord3);
   const int rrow = lane >> 3, rchunk = lane & 7;
+  f32x4 col_scale[Scale::kOn ? WI * 4 : 1];
+  if constexpr (Scale::kOn)
+#pragma unroll
+    for (int i = 0; i < WI * 4; ++i)
+      col_scale[i] = scale.col4(wn * (BN / 2) + i * 8 + 4 * half);
 #pragma unroll
   for (int jb = 0; jb < WJ; ++jb) {
     const int row0 = wm * (BM / 2) + jb * 32;
+    float row_scale = 1.f;
+    if constexpr (Scale::kOn) row_scale = scale.row(row0 + l32);
 #pragma unroll
     for (int ip = 0; ip < WI / kPerBlk; ++ip) {
 #pragma unroll
@@ -95,8 +126,14 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[WI][WJ], char* st
           typedef Out vec4_t __attribute__((ext_vector_type(4)));
           vec4_t o;
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            o[v] = from_f32<Out>(acc_read(acc[kPerBlk * ip + u][jb][4 * q + v]));
+          for (int v = 0; v < 4; ++v) {
+            const auto sum = acc_read(acc[kPerBlk * ip + u][jb][4 * q + v]);
+            if constexpr (Scale::kOn)
+              o[v] = from_f32<Out>((float)sum * row_scale *
+                                   col_scale[(kPerBlk * ip + u) * 4 + q][v]);
+            else
+              o[v] = from_f32<Out>(sum);
+          }
           if constexpr (kOs == 2) {
             const int chunk = (u * 4 + q) ^ (l32 & 7);
             *reinterpret_cast<u32x2*>(stg + l32 * 128 + chunk * 16 + half * 8) =

@@ -13,7 +13,10 @@ enum class RingKind {
   kInputGradF16,
   kMxBF16,  // MXFP4 operands, by the output's type
   kMxF16,
-  kMxF32
+  kMxF32,
+  kI8BF16,  // 8-bit integers, by the output's type
+  kI8F16,
+  kI8F32
 };
 
 // Rows of every operand start at 16-byte boundaries and hold whole 16-byte
@@ -23,8 +26,8 @@ struct RingParams {
   const char* w;    // [E] matrices of wbytes: [B] rows of cbytes (forward), or
                     // [C] rows of B 16-bit features (input gradient), ldw apart
   char* out;        // [rows][B], ldo apart
-  const char* act_scales;  // MXFP4: [rows], lds apart
-  const char* w_scales;    // [E][B], lds apart
+  const char* act_scales;  // MXFP4: [rows], lds apart; 8 bits: float [rows]
+  const char* w_scales;    // [E][B], lds apart; float [E][B]
   const int32_t* offsets;
   int64_t lda, ldw, ldo, lds, wbytes;
   int rows, E, B;

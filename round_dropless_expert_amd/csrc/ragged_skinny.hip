@@ -5,7 +5,7 @@
 //
 // A workgroup takes 16 FB features and 16 MT rows of one expert. Its four
 // wavefronts take the batches of K steps in turn (16 rows x 64 bytes a step
-// and operand: 16x16x32 for 16-bit types, 16x16x128 for MXFP4) and their sums
+// and operand: 16x16x32 for 16-bit types, 16x16x64 for 8-bit ones, 16x16x128 for MXFP4) and their sums
 // are joined in LDS, in wavefront order: the order of the sum is fixed. A
 // batch's loads are issued while the one before is multiplied.
 //
@@ -21,6 +21,7 @@
 namespace moe {
 namespace {
 
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kRsrcWord3 = 0x00020000;          // raw buffer
@@ -29,14 +30,16 @@ constexpr int kNonTemporal = 2;
 constexpr int kBatch = 4;  // K steps: the 16 scale bytes a lane loads at once
 
 struct SkinnyBf16 {
-  static constexpr bool kScaled = false;
+  typedef f32x4 acc_t;
+  static constexpr bool kScaled = false, kInt = false;
   __device__ static __forceinline__ f32x4 mma(u32x4 a, u32x4 b, int, int, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
   }
 };
 struct SkinnyF16 {
-  static constexpr bool kScaled = false;
+  typedef f32x4 acc_t;
+  static constexpr bool kScaled = false, kInt = false;
   __device__ static __forceinline__ f32x4 mma(u32x4 a, u32x4 b, int, int, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
@@ -45,11 +48,22 @@ struct SkinnyF16 {
 // 4-bit values: lane l supplies row l % 16, block l / 16 of the step's four,
 // and the block's scale byte.
 struct SkinnyMx {
-  static constexpr bool kScaled = true;
+  typedef f32x4 acc_t;
+  static constexpr bool kScaled = true, kInt = false;
   __device__ static __forceinline__ f32x4 mma(u32x4 a, u32x4 b, int sa, int sb, f32x4 c) {
     const i32x8 av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
     const i32x8 bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, sa, 0, sb);
+  }
+};
+
+// 8-bit integers, summed exactly.
+struct SkinnyI8 {
+  typedef i32x4 acc_t;
+  static constexpr bool kScaled = false, kInt = true;
+  __device__ static __forceinline__ i32x4 mma(u32x4 a, u32x4 b, int, int, i32x4 c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a),
+                                                 __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
   }
 };
 
@@ -61,9 +75,13 @@ struct Batch {
   u32x4 sw[Op::kScaled ? FB : 1], st[Op::kScaled ? MT : 1];
 };
 
+// What a wavefront's share of a sum is.
+template <typename Op>
+using sum_t = __remove_reference_t(decltype(typename Op::acc_t{}[0]));
+
 template <typename Op, typename Out, int FB, int MT>
 __device__ __forceinline__ void skinny_rows(const RingParams& p, const ExpertUnit& u, int n0,
-                                            int m0, float* joined) {
+                                            int m0, sum_t<Op>* joined) {
   constexpr bool kScaled = Op::kScaled;
   constexpr int kFeatures = 16 * FB, kPitch = kFeatures + 4;  // floats
   const int tid = threadIdx.x, lane = tid & 63;
@@ -134,11 +152,11 @@ __device__ __forceinline__ void skinny_rows(const RingParams& p, const ExpertUni
                        0, 0));
     }
   };
-  f32x4 acc[FB][MT];
+  typename Op::acc_t acc[FB][MT];
 #pragma unroll
   for (int i = 0; i < FB; ++i)
 #pragma unroll
-    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < MT; ++j) acc[i][j] = typename Op::acc_t{0, 0, 0, 0};
   auto multiply = [&](const Batch<Op, FB, MT>& b, int s0) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
@@ -177,7 +195,7 @@ __device__ __forceinline__ void skinny_rows(const RingParams& p, const ExpertUni
   for (int j = 0; j < MT; ++j)
 #pragma unroll
     for (int i = 0; i < FB; ++i)
-      *reinterpret_cast<f32x4*>(joined + ((wave * MT + j) * 16 + l16) * kPitch +
+      *reinterpret_cast<typename Op::acc_t*>(joined + ((wave * MT + j) * 16 + l16) * kPitch +
                                 16 * i + 4 * blk) =
           acc[i][j];
   __syncthreads();
@@ -187,17 +205,22 @@ __device__ __forceinline__ void skinny_rows(const RingParams& p, const ExpertUni
   for (int k = 0; k < FB * MT; ++k) {
     const int token = tid / kFeatures + 256 / kFeatures * k, f = tid % kFeatures;
     if (token < mr && f < fw) {
-      float r = 0.f;
+      sum_t<Op> r = 0;
 #pragma unroll
       for (int w = 0; w < 4; ++w) r += joined[(w * MT * 16 + token) * kPitch + f];
-      y[token * ldo + f] = from_f32<Out>(r);
+      if constexpr (Op::kInt)
+        y[token * ldo + f] =
+            from_f32<Out>((float)r * reinterpret_cast<const float*>(p.act_scales)[t_row + token] *
+                          reinterpret_cast<const float*>(p.w_scales)[w_row + f]);
+      else
+        y[token * ldo + f] = from_f32<Out>(r);
     }
   }
 }
 
 template <typename Op, typename Out, int FB, int MT>
 __global__ __launch_bounds__(256) void skinny_kernel(RingParams p) {
-  __shared__ __attribute__((aligned(16))) float joined[4 * MT * 16 * (16 * FB + 4)];
+  __shared__ __attribute__((aligned(16))) sum_t<Op> joined[4 * MT * 16 * (16 * FB + 4)];
   const int nb = (p.B + 16 * FB - 1) / (16 * FB);
   ExpertUnit u;
   const int t = blockIdx.x;
@@ -243,6 +266,9 @@ hipError_t launch_skinny(RingKind kind, const RingParams& p, int num_cus, hipStr
     case RingKind::kMxBF16: return launch<SkinnyMx, bf16>(p, num_cus, st);
     case RingKind::kMxF16: return launch<SkinnyMx, f16>(p, num_cus, st);
     case RingKind::kMxF32: return launch<SkinnyMx, float>(p, num_cus, st);
+    case RingKind::kI8BF16: return launch<SkinnyI8, bf16>(p, num_cus, st);
+    case RingKind::kI8F16: return launch<SkinnyI8, f16>(p, num_cus, st);
+    case RingKind::kI8F32: return launch<SkinnyI8, float>(p, num_cus, st);
     default: return hipErrorInvalidValue;
   }
 }

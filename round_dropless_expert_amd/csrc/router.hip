@@ -19,25 +19,56 @@
 namespace moe {
 namespace {
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
 __device__ __forceinline__ bool no_number(float l) { return !(l > -INFINITY); }  // -inf, NaN
 
 template <typename T>
 __device__ __forceinline__ float load_f32(const T* p) {
   return to_f32(*p);
 }
+// Element i of an array of type t.
+__device__ __forceinline__ float load_as(const void* p, ElemType t, int64_t i) {
+  if (t == ElemType::kF32) return static_cast<const float*>(p)[i];
+  if (t == ElemType::kBF16) return to_f32(static_cast<const bf16*>(p)[i]);
+  return to_f32(static_cast<const f16*>(p)[i]);
+}
 
-// Maximum and sum over the kLanes neighbouring lanes of a segment.
-template <int kLanes>
-__device__ __forceinline__ float seg_max(float v) {
-#pragma unroll
-  for (int x = 1; x < kLanes; x <<= 1) v = fmaxf(v, __shfl_xor(v, x));
-  return v;
+// The value of another lane of the segment: step x pairs lanes at xor distance 1
+// and 2, then mirrored in eights and sixteens (whose fours, and eights, hold the
+// same value by then), then at xor distance 16 and 32.
+template <int x>
+__device__ __forceinline__ int other_lane(int v) {
+  if constexpr (x == 1) return __builtin_amdgcn_mov_dpp(v, 0xb1, 0xf, 0xf, true);
+  else if constexpr (x == 2) return __builtin_amdgcn_mov_dpp(v, 0x4e, 0xf, 0xf, true);
+  else if constexpr (x == 4) return __builtin_amdgcn_mov_dpp(v, 0x141, 0xf, 0xf, true);
+  else if constexpr (x == 8) return __builtin_amdgcn_mov_dpp(v, 0x140, 0xf, 0xf, true);
+  else return __shfl_xor(v, x);
+}
+template <int x>
+__device__ __forceinline__ float other_lane(float v) {
+  return __builtin_bit_cast(float, other_lane<x>(__builtin_bit_cast(int, v)));
+}
+template <int x>
+__device__ __forceinline__ double other_lane(double v) {
+  const u32x2 b = __builtin_bit_cast(u32x2, v);
+  const u32x2 o = {(uint32_t)other_lane<x>((int)b[0]), (uint32_t)other_lane<x>((int)b[1])};
+  return __builtin_bit_cast(double, o);
+}
+// f(value, other lane's value) over the kLanes neighbouring lanes of a segment;
+// every lane ends with the same bits (f is commutative).
+template <int kLanes, int x = 1, typename V, typename F>
+__device__ __forceinline__ V over_segment(V v, F f) {
+  if constexpr (x < kLanes) return over_segment<kLanes, 2 * x>(f(v, other_lane<x>(v)), f);
+  else return v;
 }
 template <int kLanes>
-__device__ __forceinline__ float seg_sum(float v) {
-#pragma unroll
-  for (int x = 1; x < kLanes; x <<= 1) v += __shfl_xor(v, x);
-  return v;
+__device__ __forceinline__ float seg_max(float v) {
+  return over_segment<kLanes>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int kLanes, typename V>
+__device__ __forceinline__ V seg_sum(V v) {
+  return over_segment<kLanes>(v, [](V a, V b) { return a + b; });
 }
 
 // e^(l - top), 1 where both are infinite.
@@ -69,18 +100,30 @@ __device__ __forceinline__ float weight_of(float l, bool use, float top, float s
   return all > 0.f ? scale * (e / all) : 0.f;
 }
 
+// The larger value of the wavefront, and of equal ones that of the lower index.
+template <int x = 1>
+__device__ __forceinline__ void first_of_wave(double& v, int& at) {
+  if constexpr (x < kWave) {
+    const double ov = other_lane<x>(v);
+    const int oa = other_lane<x>(at);
+    const bool take = (ov > v) | ((ov == v) & (oa < at));
+    v = take ? ov : v;
+    at = take ? oa : at;
+    first_of_wave<2 * x>(v, at);
+  }
+}
+
 // A token's choice in fp64, by one wavefront. Lane l holds experts l + 64 m.
 // `c` is the wavefront's share of LDS, E doubles (used with groups).
-template <typename T, int M>
+template <int M>
 __device__ __forceinline__ void route_exact(const RouterParams& p, int64_t t, double* c) {
   const int lane = threadIdx.x & (kWave - 1);
-  const T* row = static_cast<const T*>(p.logits) + t * p.ld;
   float l[M];
   float top = -INFINITY;
 #pragma unroll
   for (int m = 0; m < M; ++m) {
     const int e = lane + kWave * m;
-    l[m] = e < p.E ? load_f32(row + e) : -INFINITY;
+    l[m] = e < p.E ? load_as(p.logits, p.type, t * p.ld + e) : -INFINITY;
     if (!no_number(l[m])) top = fmaxf(top, l[m]);
   }
   top = seg_max<kWave>(top);
@@ -93,8 +136,7 @@ __device__ __forceinline__ void route_exact(const RouterParams& p, int64_t t, do
       s[m] = no_number(l[m]) ? 0.0 : l[m] == top ? 1.0 : exp((double)l[m] - (double)top);
       sum += s[m];
     }
-#pragma unroll
-    for (int x = 1; x < kWave; x <<= 1) sum += __shfl_xor(sum, x);
+    sum = seg_sum<kWave>(sum);
     sum32 = (float)sum;
 #pragma unroll
     for (int m = 0; m < M; ++m) s[m] = s[m] / sum;
@@ -157,15 +199,7 @@ __device__ __forceinline__ void route_exact(const RouterParams& p, int64_t t, do
         v = s[m];
         at = lane + kWave * m;
       }
-#pragma unroll
-    for (int x = 1; x < kWave; x <<= 1) {
-      const double ov = __shfl_xor(v, x);
-      const int oa = __shfl_xor(at, x);
-      if (ov > v || (ov == v && oa < at)) {
-        v = ov;
-        at = oa;
-      }
-    }
+    first_of_wave(v, at);
     // its logit, from the lane that holds it
     float lv = 0.f;
 #pragma unroll
@@ -189,20 +223,397 @@ __device__ __forceinline__ void route_exact(const RouterParams& p, int64_t t, do
   }
 }
 
-template <typename T, int M>
+template <int M>
 __global__ __launch_bounds__(256) void router_exact_kernel(RouterParams p) {
   __shared__ double c[4][kWave * M];
   const int wave = threadIdx.x / kWave;
   for (int64_t t = (int64_t)blockIdx.x * 4 + wave; t < p.T; t += (int64_t)gridDim.x * 4)
-    route_exact<T, M>(p, t, c[wave]);
+    route_exact<M>(p, t, c[wave]);
 }
 
-template <typename T>
+// M logits of a token from expert e0 on; those from E on are any of the row's.
+template <typename T, int M>
+__device__ __forceinline__ void load_logits(const RouterParams& p, int64_t t, int e0,
+                                            float (&l)[M]) {
+  constexpr int V = 16 / sizeof(T);
+  const T* row = static_cast<const T*>(p.logits) + t * p.ld;
+  if constexpr (M % V == 0) {
+    if (p.vec) {  // whole vectors: E is a multiple of V
+      union {
+        T e[V];
+        u32x4 v;
+      } r[M / V];
+#pragma unroll
+      for (int c = 0; c < M / V; ++c) {
+        const int e = e0 + c * V;
+        r[c].v = *reinterpret_cast<const u32x4*>(row + (e < p.E ? e : p.E - V));
+      }
+#pragma unroll
+      for (int m = 0; m < M; ++m) l[m] = to_f32(r[m / V].e[m % V]);
+      return;
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    const int e = e0 + m;
+    l[m] = to_f32(row[e < p.E ? e : p.E - 1]);
+  }
+}
+
+// Where expert e's choice lies in LDS: one word in 32 is skipped, against bank
+// conflicts of the lanes that walk neighbouring groups.
+__host__ __device__ constexpr int choice_at(int e) { return e + e / 32; }
+
+// Larger and smaller of two keys (never NaN).
+__device__ __forceinline__ void order_keys(double& a, double& b) {
+  const double hi = __builtin_fmax(a, b), lo = __builtin_fmin(a, b);
+  a = hi;
+  b = lo;
+}
+// A bitonic list of K keys, into descending order.
+template <int K>
+__device__ __forceinline__ void sort_bitonic(double* v) {
+#pragma unroll
+  for (int s = K / 2; s > 0; s >>= 1)
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+      if ((i & s) == 0) order_keys(v[i], v[i + s]);
+}
+// K keys in any order.
+template <int K>
+__device__ __forceinline__ void sort_keys(double* v) {
+  if constexpr (K > 1) {
+    sort_keys<K / 2>(v);
+    sort_keys<K / 2>(v + K / 2);
+    // first half descending, second read backwards: compare across, then both
+    // halves are bitonic
+#pragma unroll
+    for (int i = 0; i < K / 2; ++i) order_keys(v[i], v[K - 1 - i]);
+    sort_bitonic<K / 2>(v);
+    sort_bitonic<K / 2>(v + K / 2);
+  }
+}
+// The K best of two descending lists, into a.
+template <int K>
+__device__ __forceinline__ void merge_keys(double (&a)[K], const double (&b)[K]) {
+#pragma unroll
+  for (int i = 0; i < K; ++i) a[i] = __builtin_fmax(a[i], b[K - 1 - i]);
+  sort_bitonic<K>(a);
+}
+template <int kLanes, int K, int x = 1>
+__device__ __forceinline__ void merge_segment(double (&a)[K]) {
+  if constexpr (x < kLanes) {
+    double b[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) b[i] = other_lane<x>(a[i]);
+    merge_keys<K>(a, b);
+    merge_segment<kLanes, K, 2 * x>(a);
+  }
+}
+
+// An expert's key: its value, with the low bits of the fp64 mantissa (which fp32
+// values leave empty) telling equal ones apart, the lower index first. One
+// v_max_f64 then compares value and index. Values end at fp32's largest: a token
+// that chooses one there is chosen again.
+constexpr float kMost = 0x1.fffffep127f;
+__device__ __forceinline__ double key_of(float v, int e) {
+  u32x2 b = __builtin_bit_cast(u32x2, (double)__builtin_amdgcn_fmed3f(v + 0.f, -kMost, kMost));
+  b[0] |= (uint32_t)e ^ (~(uint32_t)((int32_t)b[1] >> 31) & 1023u);  // e, or 1023 - e
+  return __builtin_bit_cast(double, b);
+}
+__device__ __forceinline__ int expert_of(double key) {
+  const u32x2 b = __builtin_bit_cast(u32x2, key);
+  return (int)((b[0] ^ ~(uint32_t)((int32_t)b[1] >> 31)) & 1023u);
+}
+
+// The best two of the lanes of a group (1, 2, 4, 8 or 16 neighbours).
+template <int x>
+__device__ __forceinline__ void merge_two(float& first, float& second, int lanes) {
+  if constexpr (x < 16) {
+    if (x < lanes) {
+      const float f = other_lane<x>(first), s = other_lane<x>(second);
+      second = fmaxf(fminf(first, f), fmaxf(second, s));
+      first = fmaxf(first, f);
+    }
+    merge_two<2 * x>(first, second, lanes);
+  }
+}
+
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr int kGroupStep = 4;  // choices that a group's lane reads at once
+
+// kLanes lanes a token, lane q holding experts q M .. q M + M - 1, k <= K. Each
+// lane sorts its K best keys, and exchanges with the lanes of its segment merge
+// them. Groups (16 lanes): where a group's experts are whole lanes their best two
+// are merged like that, otherwise a lane a group reads them from LDS; rotations of
+// the lanes count the groups before each.
+//
+// Scores are fp32, by the hardware's base-2 exponential and reciprocal (an ulp
+// each). They are off by at most tol = 2^-24 (A pmax + |c|): a sigmoid by A = 8 (4
+// by its steps: l log2 e is off by |l| 2^-23 and s (1 - s) |l| < 0.23), a softmax
+// of M values a lane by A = 2 (M + 16) of its largest score; the sum with the bias
+// by one of c. Where two chosen values, the last chosen and another, or two groups
+// lie within the sum of their errors, the token goes to route_exact. Without a
+// bias keys are the logits themselves.
+//
+// The code has no branch an expert: conditions are selects, and what can be
+// chosen is a bit mask a lane.
+template <int kLanes, int M, int K>
+__global__ __launch_bounds__(256) void router_kernel(RouterParams p) {
+  static_assert(K <= kLanes && kLanes <= 16, "a chosen expert a lane; DPP rows");
+  constexpr int EP = kLanes * M, kTokens = 256 / kLanes;
+  constexpr int kRow = choice_at(EP);
+  extern __shared__ float choices[];  // with groups: [kTokens][kRow]
+  const int q = threadIdx.x % kLanes, seg = threadIdx.x / kLanes, e0 = q * M;
+  const bool biased = p.bias != nullptr;
+  const int64_t steps = (p.T + kTokens - 1) / kTokens;
+  for (int64_t step = blockIdx.x; step < steps; step += gridDim.x) {
+    const int64_t t = step * kTokens + seg;
+    const bool live = t < p.T;
+    float l[M];
+    if (p.type == ElemType::kF32) load_logits<float, M>(p, live ? t : 0, e0, l);
+    else if (p.type == ElemType::kBF16) load_logits<bf16, M>(p, live ? t : 0, e0, l);
+    else load_logits<f16, M>(p, live ? t : 0, e0, l);
+
+    // bit m of `open`: expert e0 + m can be chosen
+    const int own = p.E - e0 < 0 ? 0 : (p.E - e0 < M ? p.E - e0 : M);
+    uint32_t open = own < 32 ? (1u << own) - 1 : ~0u;
+    float top = -INFINITY;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      l[m] = ((open >> m) & 1) != 0 ? fmaxf(l[m], -INFINITY) : -INFINITY;  // NaN: -inf
+      top = fmaxf(top, l[m]);
+    }
+    float sum = 0.f, c[M];
+    float worst = 8.f;  // A pmax
+    if (!p.sigmoid) {
+      top = seg_max<kLanes>(top);
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        const float d = l[m] == top ? 0.f : l[m] - top;
+        c[m] = __builtin_amdgcn_exp2f((l[m] > -INFINITY ? d : -INFINITY) * kLog2e);
+        sum += c[m];
+      }
+      sum = seg_sum<kLanes>(sum);
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+      for (int m = 0; m < M; ++m) c[m] *= inv;
+      worst = (float)(2 * (M + 16)) * inv;
+    }
+    // what the choice goes by
+    bool unsure = false;
+    if (biased || p.groups > 1) {
+      if (p.sigmoid)
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+          c[m] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * l[m]));
+      if (biased) {
+        float b[M];
+        if (M % 4 == 0 && p.bias_vec) {
+#pragma unroll
+          for (int m = 0; m < M; m += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(
+                p.bias + (uint32_t)(e0 + m < p.E ? e0 + m : p.E - 4));
+            b[m] = f.x;
+            b[m + 1] = f.y;
+            b[m + 2] = f.z;
+            b[m + 3] = f.w;
+          }
+        } else {
+#pragma unroll
+          for (int m = 0; m < M; ++m) b[m] = p.bias[(uint32_t)(e0 + m < p.E ? e0 + m : p.E - 1)];
+        }
+#pragma unroll
+        for (int m = 0; m < M; ++m) c[m] += b[m];
+      }
+#pragma unroll
+      for (int m = 0; m < M; ++m) c[m] = l[m] > -INFINITY ? fmaxf(c[m], -INFINITY) : -INFINITY;
+    }
+    if constexpr (kLanes == 16) {
+      if (p.groups > 1) {
+        float first = -INFINITY, second = -INFINITY;
+        bool is_group;
+        int id, share = 1;  // this lane's group, and the lanes that hold it
+        if (p.lanes_per_group) {
+#pragma unroll
+          for (int m = 0; m < M; ++m) {
+            second = __builtin_amdgcn_fmed3f(first, second, c[m]);
+            first = fmaxf(first, c[m]);
+          }
+          merge_two<1>(first, second, p.lanes_per_group);
+          share = p.lanes_per_group;
+          id = q / share;
+          is_group = e0 < p.E;
+        } else {
+          float* mine = choices + seg * kRow;
+#pragma unroll
+          for (int m = 0; m < M; ++m) mine[choice_at(e0 + m)] = c[m];
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          __builtin_amdgcn_wave_barrier();
+          id = q;
+          is_group = q < p.groups;
+          for (int i = 0; i < p.per_group; i += kGroupStep) {
+            float v[kGroupStep];
+#pragma unroll
+            for (int u = 0; u < kGroupStep; ++u) {
+              const int e = q * p.per_group + i + u;
+              v[u] = mine[choice_at(e < EP ? e : EP - 1)];
+            }
+#pragma unroll
+            for (int u = 0; u < kGroupStep; ++u) {
+              const float x = i + u < p.per_group ? v[u] : -INFINITY;
+              second = __builtin_amdgcn_fmed3f(first, second, x);
+              first = fmaxf(first, x);
+            }
+          }
+        }
+        const float g = p.group_top == 2 && p.per_group > 1 ? first + second : first;
+        unsure = is_group & !(g == g);
+        // two groups' sums of two choices each
+        const float big = seg_max<kLanes>(
+            is_group & (fabsf(g) < INFINITY) ? fmaxf(fabsf(first), fabsf(second)) : 0.f);
+        const float near = 0x1p-24f * (4.f * worst + 16.f * big);
+        // lanes of groups before this one, by rotations of the 16 lanes; a lane of
+        // no group holds -inf and an id behind all
+        const float mark = is_group ? g : -INFINITY;
+        const int name = is_group ? id : 64;
+        int ahead = 0;
+#define MOE_TURN(n)                                                                           \
+  {                                                                                           \
+    const float v = __builtin_bit_cast(                                                       \
+        float,                                                                                \
+        __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, mark), 0x120 + n, 0xf, 0xf, true));  \
+    const int o = __builtin_amdgcn_mov_dpp(name, 0x120 + n, 0xf, 0xf, true);                  \
+    ahead += (v > mark) | ((v == mark) & (o < name));                                         \
+    unsure |= (o != name) & (fabsf(v - mark) <= near);                                        \
+  }
+        MOE_TURN(1) MOE_TURN(2) MOE_TURN(3) MOE_TURN(4) MOE_TURN(5) MOE_TURN(6) MOE_TURN(7)
+        MOE_TURN(8) MOE_TURN(9) MOE_TURN(10) MOE_TURN(11) MOE_TURN(12) MOE_TURN(13)
+        MOE_TURN(14) MOE_TURN(15)
+#undef MOE_TURN
+        const bool chosen = is_group & (ahead < p.top_groups * share);
+        if (p.lanes_per_group) {
+          open = chosen ? open : 0;
+        } else {
+          const uint64_t in = __builtin_amdgcn_ballot_w64(chosen);
+          const uint32_t keep = (uint32_t)(in >> (threadIdx.x & 48)) & 0xffffu;
+          int group = e0 / p.per_group, left = (group + 1) * p.per_group - e0;
+          uint32_t kept = 0;
+#pragma unroll
+          for (int m = 0; m < M; ++m) {
+            kept |= ((keep >> (group & 31)) & 1) << m;
+            --left;
+            group += left == 0;
+            left = left == 0 ? p.per_group : left;
+          }
+          open &= kept;
+        }
+      }
+    }
+    double best[K];
+    {
+      // each lane's K best: blocks of K sorted and merged
+      constexpr int kBlocks = (M + K - 1) / K;
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        double v[K];
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+          const int m = b * K + i;
+          v[i] = -INFINITY;
+          if (m < M) {
+            const bool can = ((open >> m) & 1) != 0;
+            const double key = key_of(biased ? c[m] : l[m], e0 + m);
+            v[i] = can ? key : -INFINITY;
+            c[m] = can ? c[m] : -INFINITY;
+          }
+        }
+        sort_keys<K>(v);
+        if (b == 0)
+#pragma unroll
+          for (int i = 0; i < K; ++i) best[i] = v[i];
+        else
+          merge_keys<K>(best, v);
+      }
+    }
+    merge_segment<kLanes, K>(best);
+    double mine = best[0], last = best[0];
+#pragma unroll
+    for (int j = 1; j < K; ++j) last = j == p.k - 1 ? best[j] : last;
+    // (an end's own value, index bits and all, is at least that far out)
+    unsure |= !(last > -(double)kMost) | !(best[0] < (double)kMost);
+    if (biased) {
+      const float ck = (float)last, c1 = (float)best[0];
+      const float near = 0x1p-24f * (2.f * worst + 4.f * fmaxf(fabsf(ck), fabsf(c1)));
+#pragma unroll
+      for (int j = 0; j + 1 < K; ++j)
+        if (j + 1 < p.k) unsure |= !(best[j] - best[j + 1] > (double)near);
+      int over = 0;
+#pragma unroll
+      for (int m = 0; m < M; ++m) over += c[m] >= ck - near;
+      unsure |= seg_sum<kLanes>(over) != p.k;
+    }
+#pragma unroll
+    for (int j = 1; j < K; ++j) mine = q == j ? best[j] : mine;
+    const bool use = q < p.k;
+    const int e = use ? expert_of(mine) : 0;
+    const float le = live && use ? load_as(p.logits, p.type, t * p.ld + e) : -INFINITY;
+    const float w = weight_of<kLanes>(le, use, top, sum, p.sigmoid, p.renormalize, p.scale);
+    if (live && use) {
+      p.idx[t * p.k + q] = e;
+      p.weight[t * p.k + q] = w;
+    }
+    // tokens to choose again: one wavefront each
+    uint64_t again = __builtin_amdgcn_ballot_w64(live && unsure);
+    double* share = reinterpret_cast<double*>(
+        choices + (threadIdx.x / kWave) * (kWave / kLanes) * kRow);
+    while (again) {
+      const int at = __builtin_ctzll(again) / kLanes;  // a segment of the wavefront
+      again &= ~(((1ull << (kLanes - 1) << 1) - 1) << (at * kLanes));
+      __builtin_amdgcn_wave_barrier();
+      route_exact<(EP + kWave - 1) / kWave>(
+          p, step * kTokens + (threadIdx.x / kWave) * (kWave / kLanes) + at, share);
+    }
+    if (kLanes == 16 && p.groups > 1) {
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+}
+
+template <int kLanes, int M>
+hipError_t route_lanes(RouterParams p, int num_cus, hipStream_t st) {
+  constexpr int kTokens = 256 / kLanes;
+  const int64_t steps = (p.T + kTokens - 1) / kTokens, most = (int64_t)num_cus * 16;
+  const dim3 grid((unsigned)(steps < most ? steps : most));
+  // the lanes of a group, where they hold nothing else
+  p.lanes_per_group = 0;
+  if (p.groups > 1 && p.per_group % M == 0) {
+    const int lanes = p.per_group / M;
+    if ((lanes & (lanes - 1)) == 0 && lanes <= 16) p.lanes_per_group = lanes;
+  }
+  const size_t lds = p.groups > 1 ? sizeof(float) * kTokens * choice_at(kLanes * M) : 0;
+  if (p.k <= 4)
+    hipLaunchKernelGGL((router_kernel<kLanes, M, 4>), grid, dim3(256), lds, st, p);
+  else
+    hipLaunchKernelGGL((router_kernel<kLanes, M, 8>), grid, dim3(256), lds, st, p);
+  return hipGetLastError();
+}
+
+// The fast kernel takes up to 8 of up to 512 experts, with up to 16 groups; the
+// exact one, a wavefront a token, takes the rest.
 hipError_t route(const RouterParams& p, int num_cus, hipStream_t st) {
+  if (p.k <= 8 && p.E <= 512 && p.groups <= 16) {
+    if (p.groups == 1 && p.E <= 16) return route_lanes<8, 2>(p, num_cus, st);
+    if (p.groups == 1 && p.E <= 32) return route_lanes<8, 4>(p, num_cus, st);
+    if (p.E <= 64) return route_lanes<16, 4>(p, num_cus, st);
+    if (p.E <= 128) return route_lanes<16, 8>(p, num_cus, st);
+    if (p.E <= 256) return route_lanes<16, 16>(p, num_cus, st);
+    return route_lanes<16, 32>(p, num_cus, st);
+  }
   const int64_t blocks = (p.T + 3) / 4, most = (int64_t)num_cus * 32;
   const dim3 grid((unsigned)(blocks < most ? blocks : most));
-#define MOE_EXACT(M) \
-  hipLaunchKernelGGL((router_exact_kernel<T, M>), grid, dim3(256), 0, st, p)
+#define MOE_EXACT(M) hipLaunchKernelGGL((router_exact_kernel<M>), grid, dim3(256), 0, st, p)
   if (p.E <= 64) MOE_EXACT(1);
   else if (p.E <= 128) MOE_EXACT(2);
   else if (p.E <= 256) MOE_EXACT(4);
@@ -355,13 +766,9 @@ hipError_t grad(const RouterGradParams& p, int num_cus, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_router(ElemType t, const RouterParams& p, int num_cus, hipStream_t st) {
+hipError_t launch_router(const RouterParams& p, int num_cus, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
-  switch (t) {
-    case ElemType::kF32: return route<float>(p, num_cus, st);
-    case ElemType::kBF16: return route<bf16>(p, num_cus, st);
-    default: return route<f16>(p, num_cus, st);
-  }
+  return route(p, num_cus, st);
 }
 
 hipError_t launch_router_backward(ElemType t, const RouterGradParams& p, int num_cus,

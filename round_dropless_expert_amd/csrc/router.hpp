@@ -19,13 +19,16 @@ struct RouterParams {
   int32_t* idx;        // [T][k]
   float* weight;       // [T][k]
   int64_t T, ld;
+  ElemType type;       // of logits
   int E, k;
   int groups, per_group, top_groups, group_top;
   float scale;
   bool sigmoid, renormalize;
-  bool vec;            // rows are 16-byte aligned
+  bool vec;            // rows are 16-byte aligned and hold whole vectors
+  bool bias_vec;       // and so is bias
+  int lanes_per_group; // set by the launch
 };
-hipError_t launch_router(ElemType t, const RouterParams& p, int num_cus, hipStream_t st);
+hipError_t launch_router(const RouterParams& p, int num_cus, hipStream_t st);
 
 struct RouterGradParams {
   const void* logits;

@@ -109,6 +109,7 @@ moe_status_t moe_route(const moe_router_t* r, const void* logits, const float* b
   p.weight = weight;
   p.T = r->T;
   p.ld = c.ld;
+  p.type = c.type;
   p.E = r->E;
   p.k = r->k;
   p.groups = c.groups;
@@ -118,8 +119,9 @@ moe_status_t moe_route(const moe_router_t* r, const void* logits, const float* b
   p.scale = r->scale;
   p.sigmoid = r->score == MOE_SCORE_SIGMOID;
   p.renormalize = r->renormalize != 0;
-  p.vec = rows_aligned(logits, c.ld, c.type);
-  MOE_LAUNCH(launch_router(c.type, p, cus, static_cast<hipStream_t>(stream)), "routing launch");
+  p.vec = rows_aligned(logits, c.ld, c.type) && r->E * elem_bytes(c.type) % 16 == 0;
+  p.bias_vec = rows_aligned(bias, r->E, ElemType::kF32);
+  MOE_LAUNCH(launch_router(p, cus, static_cast<hipStream_t>(stream)), "routing launch");
 }
 
 moe_status_t moe_route_backward(const moe_router_t* r, const void* logits, const int32_t* idx,

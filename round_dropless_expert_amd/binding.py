@@ -570,6 +570,8 @@ def _call_stream(stream, dev):
 
 
 def _on_device(t, name, dev):
+    if isinstance(t, torch.Tensor) and t.get_device() == dev:  # -1: the host's
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor or an int address")
     if not t.is_cuda:
@@ -581,11 +583,12 @@ def _on_device(t, name, dev):
 def _dense(t, name, dtype, numel, dev):
     """Address of a contiguous tensor of at least numel elements on the
     current device."""
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype
+            and t.is_contiguous() and t.numel() >= numel):
+        return t.data_ptr()
     if t is None or isinstance(t, int):
         return t
     _on_device(t, name, dev)
-    if t.dtype is dtype and t.is_contiguous() and t.numel() >= numel:
-        return t.data_ptr()
     return _arg(t, name, dtype, numel)  # raises
 
 
@@ -608,11 +611,12 @@ def _matrices(t, name, dtype, shape, dev):
 
 def _mat(t, name, dtype, rows, cols, ld, dev):
     """Address of a [rows, cols] matrix whose rows are ld elements apart."""
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype
+            and t.shape == (rows, cols) and t.stride() == (ld, 1)):
+        return t.data_ptr()
     if t is None or isinstance(t, int):
         return t
     _on_device(t, name, dev)
-    if t.dtype is dtype and t.shape == (rows, cols) and t.stride() == (ld, 1):
-        return t.data_ptr()
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
@@ -644,6 +648,11 @@ def _rows_of(t, name, dev):
 
 def _pair_of(t, name, dtype, rows, cols, dev):
     """Address and row stride of a [rows, cols] matrix of any row stride."""
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype
+            and t.shape == (rows, cols) and rows > 1):
+        ld, one = t.stride()
+        if one == 1 and ld >= cols:
+            return t.data_ptr(), ld
     dt, r, c, ld = _rows_of(t, name, dev)
     if dt is not dtype:
         raise ValueError(f"{name}: dtype {dt}, expected {dtype}")
@@ -864,10 +873,10 @@ def moe_sort(idx, E, perm, pos, offsets, ws=None, stream=None):
 def _positions(pos, T, dev):
     """k and the address of pos [T, k]."""
     _on_device(pos, "pos", dev)
-    if pos.dim() != 2 or pos.shape[0] != T:
-        raise ValueError(f"pos: shape {tuple(pos.shape)}, expected ({T}, k)")
-    k = pos.shape[1]
-    return k, _dense(pos, "pos", torch.int32, T * k, dev)
+    shape = pos.shape
+    if len(shape) != 2 or shape[0] != T:
+        raise ValueError(f"pos: shape {tuple(shape)}, expected ({T}, k)")
+    return shape[1], _dense(pos, "pos", torch.int32, T * shape[1], dev)
 
 
 def moe_collect(z, pos, y, weight=None, stream=None):
@@ -875,8 +884,9 @@ def moe_collect(z, pos, y, weight=None, stream=None):
     [T, k], y [T, d], weight float32 [T, k] (None: all 1)."""
     dev = torch.cuda.current_device()
     dt, T, d, ld_y = _rows_of(y, "y", dev)
-    z_dt, rows, _, ld_z = _rows_of(z, "z", dev)
-    z_ptr, _ = _pair_of(z, "z", dt, rows, d, dev)
+    _on_device(z, "z", dev)
+    rows = z.shape[0] if z.dim() else 0
+    z_ptr, ld_z = _pair_of(z, "z", dt, rows, d, dev)
     k, pos_ptr = _positions(pos, T, dev)
     w_ptr = None if weight is None else _matrices(weight, "weight", torch.float32, (T, k), dev)
     _check(load().moe_collect(_DTYPES[dt], T, k, rows, d, z_ptr, ld_z, pos_ptr, w_ptr,
@@ -894,7 +904,9 @@ def moe_collect_backward(dy, pos, dz=None, weight=None, z=None, dweight=None, st
         raise ValueError("dweight needs z")
     if dz is None and dweight is None:
         raise ValueError("neither dz nor dweight is given")
-    rows = (dz if dz is not None else z).shape[0]
+    some = dz if dz is not None else z
+    _on_device(some, "dz" if dz is not None else "z", dev)
+    rows = some.shape[0] if some.dim() else 0
     dz_ptr, ld_dz = (None, 0) if dz is None else _pair_of(dz, "dz", dt, rows, d, dev)
     z_ptr, ld_z = (None, 0) if z is None else _pair_of(z, "z", dt, rows, d, dev)
     f32 = torch.float32

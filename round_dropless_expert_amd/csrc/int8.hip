@@ -3,10 +3,12 @@
 //
 //   scale = max|x| / 127     q = 127 x / max|x| to nearest, ties to even
 //
-// The code is that of the exact quotient: 127 x / max|x| in fp32 is off by less
-// than 127 2^-22, and a value nearer than that to the middle of two codes is
-// divided in fp64 (127 x is exact there, and a quotient that is no tie lies at
-// least 2^-33 from one).
+// The code is that of the exact quotient. With v = 127 / max|x| in fp32, x v lies
+// within 127 2^-24 of it, and one fma with 1.5 2^23 rounds x v to an integer; an
+// x v nearer than 2^-16 to the middle of two is divided in fp64 (127 x is exact
+// there, and a quotient that is no tie lies at least 2^-33 from one). Seven
+// instructions an element, which is what keeps the quantisation at the memory's
+// rate.
 #include "ragged_device.hpp"
 #include "ragged_ring.hpp"
 #include "router.hpp"
@@ -16,8 +18,8 @@ namespace {
 
 typedef signed char i8;
 
-// 16-byte vectors of a row that a lane holds.
-constexpr int kHeld = 8;
+constexpr int kRsrcWord3 = 0x00020000;  // raw buffer
+constexpr int kNonTemporal = 2;
 
 struct QuantParams {
   const void* x;
@@ -58,60 +60,164 @@ __device__ __forceinline__ Vec<T> load_row(const T* row, int64_t c, int64_t K, b
   return r;
 }
 
-// Largest magnitude, as fp32 bits (NaN above infinity above numbers).
+// Largest magnitude of a vector, as bits in the order of the values (NaN above
+// infinity above numbers), and its fp32 bits.
 template <typename T>
 __device__ __forceinline__ uint32_t top_of(const Vec<T>& x, uint32_t top) {
+  if constexpr (sizeof(T) == 2) {
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 m = __builtin_bit_cast(u16x2, top);
 #pragma unroll
-  for (int i = 0; i < Vec<T>::V; ++i) {
-    const uint32_t b = __builtin_bit_cast(uint32_t, to_f32(x.e[i])) & 0x7fffffffu;
-    top = top > b ? top : b;
+    for (int i = 0; i < 4; ++i)
+      m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, x.v[i] & 0x7fff7fffu));
+    return __builtin_bit_cast(uint32_t, m);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t b = x.v[i] & 0x7fffffffu;
+      top = top > b ? top : b;
+    }
+    return top;
   }
-  return top;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t top_bits(uint32_t top) {
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t lo = top & 0xffffu, hi = top >> 16, m = lo > hi ? lo : hi;
+    return __builtin_bit_cast(uint32_t, to_f32(__builtin_bit_cast(T, (uint16_t)m)));
+  } else {
+    return top;
+  }
 }
 
-struct Quant {
-  float top, inv;  // max|x|, 127 / max|x|
-  bool exact;      // too small for inv
-};
-__device__ __forceinline__ int code_of(float x, const Quant& q) {
-  const float r = x * q.inv;
-  const float n = __builtin_rintf(r);
-  // |r - n| <= 1/2; near 1/2 the quotient decides
-  if (q.exact || __builtin_fabsf(__builtin_fabsf(r - n) - 0.5f) < 0x1p-14f)
-    return (int)__builtin_rint(127.0 * (double)x / (double)q.top);
-  return (int)n;
-}
-
-// kLanes lanes a row, kHeld vectors of it in each lane's registers; what a
-// longer row has beyond them is read a second time.
-template <typename T, int kLanes, bool kVec>
-__global__ __launch_bounds__(256) void int8_quantize_kernel(QuantParams p) {
+// Codes of a vector, four a word; true if one of them needs the quotient.
+template <typename T>
+__device__ __forceinline__ bool codes_of(const Vec<T>& x, float inv,
+                                         uint32_t (&out)[Vec<T>::V / 4]) {
   constexpr int V = Vec<T>::V;
-  __shared__ uint32_t tops[2][4];
-  const int lane = threadIdx.x % kLanes;
-  const int per = (int)(p.stride / V);  // vectors of a row, its padding included
-  const int64_t rows = live_rows(p.rows, p.n_rows);
-  int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes; row < rows;
-       row += (int64_t)gridDim.x * (256 / kLanes)) {
-    int64_t src = row;
-    bool real = true;
+  constexpr float kMagic = 0x1.8p23f;  // its neighbours are integers apart
+  float worst = 0.f;
+  uint32_t code[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float f = to_f32(x.e[i]);
+    const float t = __builtin_fmaf(f, inv, kMagic);
+    code[i] = __builtin_bit_cast(uint32_t, t);
+    worst = fmaxf(worst, __builtin_fabsf(__builtin_fmaf(f, inv, -(t - kMagic))));
+  }
+#pragma unroll
+  for (int i = 0; i < V / 4; ++i) {
+    const uint32_t lo = __builtin_amdgcn_perm(code[4 * i + 1], code[4 * i], 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(code[4 * i + 3], code[4 * i + 2], 0x04000c0cu);
+    out[i] = lo | hi;
+  }
+  return worst > 0.5f - 0x1p-16f;
+}
+// The codes by fp64 quotients, an element at a time: rare, and no reason to hold
+// registers.
+template <typename T>
+__device__ __forceinline__ void exact_codes_of(const Vec<T>& x, float top,
+                                               uint32_t (&out)[Vec<T>::V / 4]) {
+  constexpr int V = Vec<T>::V;
+  uint64_t all = 0;
+#pragma unroll 1
+  for (int i = V - 1; i >= 0; --i) {
+    const int w = sizeof(T) == 2 ? i / 2 : i;
+    const uint32_t word = w == 0 ? x.v[0] : w == 1 ? x.v[1] : w == 2 ? x.v[2] : x.v[3];
+    float f;
+    if constexpr (sizeof(T) == 2)
+      f = to_f32(__builtin_bit_cast(T, (uint16_t)(i & 1 ? word >> 16 : word)));
+    else
+      f = __builtin_bit_cast(float, word);
+    const int c = (int)__builtin_rint(127.0 * (double)f / (double)top);
+    all = all << 8 | (uint32_t)(c & 255);
+  }
+  out[0] = (uint32_t)all;
+  if constexpr (V == 8) out[1] = (uint32_t)(all >> 32);
+}
+
+// A row that is read and written. kVec: its wavefronts share it and its addresses
+// are 16-byte aligned and hold whole 4-byte words; loads and stores then go through
+// buffer ranges, with no branch at its end. (With branches each load waited for the
+// one before: 98304 rows of 7168 bf16 took 560 us.)
+template <typename T, bool kVec>
+struct Row {
+  const T* in;
+  i8* out;
+  int64_t K;
+  int per;  // vectors, the padding included
+  bool real;
+  __amdgpu_buffer_rsrc_t src, dst;
+
+  __device__ __forceinline__ void set(const QuantParams& p, int64_t row) {
+    int64_t from = row;
+    real = true;
     if (p.index) {
       const int32_t a = p.index[row];
-      src = a < 0 ? -1 : a / p.index_div;
-      real = src >= 0 && src < p.src_rows;
+      from = a < 0 ? -1 : a / p.index_div;
+      real = from >= 0 && from < p.src_rows;
     }
-    const T* in = static_cast<const T*>(p.x) + (real ? src : 0) * p.ld_x;
+    in = static_cast<const T*>(p.x) + (real ? from : 0) * p.ld_x;
+    out = p.codes + row * p.stride;
+    K = p.K;
+    per = (int)(p.stride / Vec<T>::V);
+    if constexpr (kVec) {
+      src = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)in, 0, real ? (int)(K * sizeof(T)) : 0, kRsrcWord3);
+      dst = __builtin_amdgcn_make_buffer_rsrc((void*)out, 0, (int)p.stride, kRsrcWord3);
+    }
+  }
+  __device__ __forceinline__ Vec<T> load(int v) const {
+    if constexpr (kVec) {
+      Vec<T> r;
+      r.v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(src, v * 16, 0, 0));
+      return r;
+    } else {
+      return load_row<T, false>(in, (int64_t)v * Vec<T>::V, K, real && v < per);
+    }
+  }
+  __device__ __forceinline__ void store(const uint32_t (&w)[Vec<T>::V / 4], int v) const {
+    typedef uint32_t words_t __attribute__((ext_vector_type(Vec<T>::V / 4)));
+    words_t o;
+#pragma unroll
+    for (int i = 0; i < Vec<T>::V / 4; ++i) o[i] = w[i];
+    if constexpr (kVec) {
+      if constexpr (sizeof(T) == 2)
+        __builtin_amdgcn_raw_buffer_store_b64(o, dst, v * 8, 0, kNonTemporal);
+      else
+        __builtin_amdgcn_raw_buffer_store_b32(w[0], dst, v * 4, 0, kNonTemporal);
+    } else if (v < per) {
+      __builtin_nontemporal_store(o, reinterpret_cast<words_t*>(out + (int64_t)v * Vec<T>::V));
+    }
+  }
+};
+
+// kLanes lanes a row, kHeld 16-byte vectors of it in each lane's registers; what a
+// longer row has beyond them is read a second time, and so are the vectors that
+// need quotients.
+template <typename T, int kLanes, int kHeld, bool kVec>
+__global__ __launch_bounds__(256) void int8_quantize_kernel(QuantParams p) {
+  constexpr int V = Vec<T>::V;
+  static_assert(kLanes >= kWave || !kVec, "a wavefront's row is one");
+  __shared__ uint32_t tops[2][4];
+  const int lane = threadIdx.x % kLanes;
+  const int64_t rows = live_rows(p.rows, p.n_rows);
+  int turn = 0;
+  int64_t row = (int64_t)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
+  if constexpr (kLanes >= kWave)  // uniform
+    row = (int64_t)blockIdx.x * (256 / kLanes) +
+          __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
+  for (; row < rows; row += (int64_t)gridDim.x * (256 / kLanes)) {
+    Row<T, kVec> r;
+    r.set(p, row);
     Vec<T> x[kHeld];
     uint32_t top = 0;
 #pragma unroll
-    for (int u = 0; u < kHeld; ++u)
-      x[u] = load_row<T, kVec>(in, (int64_t)(lane + u * kLanes) * V, p.K,
-                               real && lane + u * kLanes < per);
+    for (int u = 0; u < kHeld; ++u) x[u] = r.load(lane + u * kLanes);
 #pragma unroll
     for (int u = 0; u < kHeld; ++u) top = top_of<T>(x[u], top);
-    for (int v = lane + kHeld * kLanes; v < per; v += kLanes)
-      top = top_of<T>(load_row<T, kVec>(in, (int64_t)v * V, p.K, real), top);
+    for (int v = lane + kHeld * kLanes; v < r.per; v += kLanes) top = top_of<T>(r.load(v), top);
+    top = top_bits<T>(top);
 #pragma unroll
     for (int s = 1; s < (kLanes < kWave ? kLanes : kWave); s <<= 1) {
       const uint32_t o = __shfl_xor(top, s);
@@ -127,28 +233,35 @@ __global__ __launch_bounds__(256) void int8_quantize_kernel(QuantParams p) {
       turn ^= 1;
     }
     const bool bad = top >= 0x7f800000u;
-    Quant q;
-    q.top = __builtin_bit_cast(float, top);
-    q.exact = top < 0x0d800000u && top != 0;  // 2^-100
-    q.inv = top == 0 || bad || q.exact ? 0.f : 127.f / q.top;
-    i8* out = p.codes + row * p.stride;
-    auto put = [&](const Vec<T>& xv, int v) {
-      union {
-        i8 b[V];
-        uint32_t w[V / 4];
-      } o;
+    const float most = bad ? 0.f : __builtin_bit_cast(float, top);
+    const bool exact = most < 0x1p-100f && most > 0.f;  // too small for 127 / most
+    const float inv = most == 0.f || exact ? 0.f : 127.f / most;
+    uint32_t redo = 0;  // bit u: of the vectors held
 #pragma unroll
-      for (int i = 0; i < V; ++i) o.b[i] = bad ? (i8)0 : (i8)code_of(to_f32(xv.e[i]), q);
+    for (int u = 0; u < kHeld; ++u) {
+      uint32_t w[V / 4];
+      redo |= (uint32_t)codes_of<T>(x[u], inv, w) << u;
 #pragma unroll
-      for (int i = 0; i < V / 4; ++i)
-        __builtin_nontemporal_store(o.w[i], reinterpret_cast<uint32_t*>(out + (int64_t)v * V) + i);
-    };
+      for (int i = 0; i < V / 4; ++i) w[i] = bad ? 0 : w[i];
+      r.store(w, lane + u * kLanes);
+    }
+    redo = bad ? 0 : exact ? (1u << kHeld) - 1 : redo;
+    while (redo) {
+      const int v = lane + __builtin_ctz(redo) * kLanes;
+      redo &= redo - 1;
+      uint32_t w[V / 4];
+      exact_codes_of<T>(r.load(v), most, w);
+      r.store(w, v);
+    }
+    for (int v = lane + kHeld * kLanes; v < r.per; v += kLanes) {
+      const Vec<T> again = r.load(v);
+      uint32_t w[V / 4];
+      if ((codes_of<T>(again, inv, w) || exact) && !bad) exact_codes_of<T>(again, most, w);
 #pragma unroll
-    for (int u = 0; u < kHeld; ++u)
-      if (lane + u * kLanes < per) put(x[u], lane + u * kLanes);
-    for (int v = lane + kHeld * kLanes; v < per; v += kLanes)
-      put(load_row<T, kVec>(in, (int64_t)v * V, p.K, real), v);
-    if (lane == 0) p.scales[row] = bad ? __builtin_nanf("") : q.top / 127.f;
+      for (int i = 0; i < V / 4; ++i) w[i] = bad ? 0 : w[i];
+      r.store(w, v);
+    }
+    if (lane == 0) p.scales[row] = bad ? __builtin_nanf("") : most / 127.f;
   }
 }
 
@@ -199,24 +312,33 @@ __global__ __launch_bounds__(256) void int8_dequantize_kernel(DequantParams p) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-template <typename T, int kLanes>
+template <typename T, int kLanes, int kHeld>
 hipError_t quantize_lanes(const QuantParams& p, int num_cus, hipStream_t st) {
   const int64_t blocks = (p.rows + 256 / kLanes - 1) / (256 / kLanes);
-  const int64_t most = (int64_t)num_cus * 256;
+  const int64_t most = (int64_t)num_cus * 64;
   const dim3 grid((unsigned)(blocks < most ? blocks : most));
-  if (p.ld_x % Vec<T>::V == 0 && aligned16(p.x))
-    hipLaunchKernelGGL((int8_quantize_kernel<T, kLanes, true>), grid, dim3(256), 0, st, p);
-  else
-    hipLaunchKernelGGL((int8_quantize_kernel<T, kLanes, false>), grid, dim3(256), 0, st, p);
+  if constexpr (kLanes >= kWave) {
+    if (p.ld_x % Vec<T>::V == 0 && aligned16(p.x) && p.K * sizeof(T) % 4 == 0) {
+      hipLaunchKernelGGL((int8_quantize_kernel<T, kLanes, kHeld, true>), grid, dim3(256), 0, st,
+                         p);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((int8_quantize_kernel<T, kLanes, kHeld, false>), grid, dim3(256), 0, st, p);
   return hipGetLastError();
 }
 
+// A wavefront a row while its registers hold one: no barrier, and the row's loads
+// are all in flight. A few lanes where a row has few vectors, a workgroup where
+// it has many.
 template <typename T>
 hipError_t quantize(const QuantParams& p, int num_cus, hipStream_t st) {
   const int64_t per = p.stride / Vec<T>::V;
-  if (per <= 16 * kHeld) return quantize_lanes<T, 16>(p, num_cus, st);
-  if (per <= kWave * kHeld) return quantize_lanes<T, kWave>(p, num_cus, st);
-  return quantize_lanes<T, 256>(p, num_cus, st);
+  if (per <= 16 * 4) return quantize_lanes<T, 16, 4>(p, num_cus, st);
+  if (per <= kWave * 4) return quantize_lanes<T, kWave, 4>(p, num_cus, st);
+  if (per <= kWave * 8) return quantize_lanes<T, kWave, 8>(p, num_cus, st);
+  if (per <= kWave * 16) return quantize_lanes<T, kWave, 16>(p, num_cus, st);
+  return quantize_lanes<T, 256, 8>(p, num_cus, st);
 }
 
 template <typename T>

@@ -207,6 +207,7 @@ def test_host_tensors_and_wrong_shapes_are_refused(B, monkeypatch):
         with pytest.raises(ValueError):
             call()
     monkeypatch.setattr(B, "_on_device", lambda t, name, dev: None)
+    monkeypatch.setattr(B, "_arg", lambda t, *a: t.data_ptr())
     with pytest.raises(ValueError, match="y"):
         B.moe_orthogonalize(f, f, None)  # an update is bfloat16
     with pytest.raises(ValueError, match="triples"):

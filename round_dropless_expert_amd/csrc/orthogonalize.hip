@@ -28,6 +28,8 @@
 namespace moe {
 namespace {
 
+typedef f16 f16x4 __attribute__((ext_vector_type(4)));
+
 constexpr int kNormParts = 128;  // workgroups that sum a matrix's squares
 constexpr double kNormFloor = 1e-20;
 
@@ -36,16 +38,36 @@ template <typename T>
 __global__ __launch_bounds__(256) void ortho_norm_kernel(const T* g, int64_t size,
                                                          double* parts) {
   __shared__ double sums[4];
+  constexpr int V = 16 / sizeof(T), U = 4;  // vectors in flight
   const T* x = g + blockIdx.y * size;
-  constexpr int U = 8;
+  const int64_t vectors = size / V;
   double sum = 0.0;
-  for (int64_t i = (int64_t)blockIdx.x * 256 * U + threadIdx.x; i < size;
+  for (int64_t i = (int64_t)blockIdx.x * 256 * U + threadIdx.x; i < vectors;
        i += (int64_t)gridDim.x * 256 * U) {
-    float v[U];
+    union {
+      T e[V];
+      u32x4 v;
+    } r[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = i + u * 256 < size ? to_f32(x[i + u * 256]) : 0.f;
+    for (int u = 0; u < U; ++u) {
+      // (the address need only be an element's)
+      const int64_t at = i + u * 256 < vectors ? i + u * 256 : vectors - 1;
+      __builtin_memcpy(&r[u].v, x + at * V, 16);
+    }
 #pragma unroll
-    for (int u = 0; u < U; ++u) sum += (double)v[u] * (double)v[u];
+    for (int u = 0; u < U; ++u) {
+      double part = 0.0;
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const double d = (double)to_f32(r[u].e[k]);
+        part = fma(d, d, part);
+      }
+      sum += i + u * 256 < vectors ? part : 0.0;
+    }
+  }
+  if (blockIdx.x == 0 && (int64_t)threadIdx.x < size - vectors * V) {
+    const double d = (double)to_f32(x[vectors * V + threadIdx.x]);
+    sum += d * d;
   }
 #pragma unroll
   for (int s = 1; s < kWave; s <<= 1) sum += __shfl_xor(sum, s);
@@ -53,6 +75,13 @@ __global__ __launch_bounds__(256) void ortho_norm_kernel(const T* g, int64_t siz
   __syncthreads();
   if (threadIdx.x == 0)
     parts[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = sums[0] + sums[1] + sums[2] + sums[3];
+}
+
+// What a matrix is multiplied by, from the sum of its squares: an infinite norm
+// divides by nothing, and the matrix becomes NaN.
+__device__ __forceinline__ double factor_of(double squares, double scale) {
+  const double norm = sqrt(squares);
+  return norm < __builtin_inf() ? scale / (norm + kNormFloor) : __builtin_nan("");
 }
 
 struct SplitParams {
@@ -79,10 +108,7 @@ __global__ __launch_bounds__(256) void ortho_split_kernel(SplitParams p) {
     for (int i = lane; i < p.n_parts; i += kWave) sum += p.parts[(int64_t)e * p.n_parts + i];
 #pragma unroll
     for (int s = 1; s < kWave; s <<= 1) sum += __shfl_xor(sum, s);
-    const double norm = sqrt(sum);
-    // an infinite norm divides by nothing: the matrix becomes NaN
-    if (lane == 0)
-      factor = norm < __builtin_inf() ? p.scale / (norm + kNormFloor) : __builtin_nan("");
+    if (lane == 0) factor = factor_of(sum, p.scale);
   }
   __syncthreads();
   const double f = factor;
@@ -91,20 +117,46 @@ __global__ __launch_bounds__(256) void ortho_split_kernel(SplitParams p) {
   const T* g = static_cast<const T*>(p.g) + (int64_t)e * p.N * p.K;
   f16* same = reinterpret_cast<f16*>(p.same) + e * p.same_batch;
   f16* turned = reinterpret_cast<f16*>(p.turned) + e * p.turned_batch;
-#pragma unroll 4
-  for (int i = 0; i < 16; ++i) {
-    const int r = wave * 16 + i, row = r0 + r, col = c0 + lane;
-    float v = 0.f;
-    if (row < p.N && col < p.K) v = (float)((double)to_f32(g[(int64_t)row * p.K + col]) * f);
-    const f16 h = from_f32<f16>(v);
-    tile[r][lane] = h;
-    if (row < p.N && col < Kp) same[row * p.ld_same + col] = h;
+  const int part = tid >> 4, four = (tid & 15) * 4;
+  float v[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = r0 + part + 16 * i, col = c0 + four;
+    const T* at = g + (int64_t)row * p.K + col;
+    T x[4] = {};
+    if (row < p.N && col + 4 <= p.K) {
+      __builtin_memcpy(x, at, sizeof x);
+    } else if (row < p.N) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (col + k < p.K) x[k] = at[k];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[i][k] = to_f32(x[k]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = part + 16 * i, row = r0 + r, col = c0 + four;
+    f16x4 h;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      // elements past the last are 0, not a NaN factor's product with it
+      const bool in = (row < p.N) & (col + k < p.K);
+      h[k] = in ? from_f32<f16>((float)((double)v[i][k] * f)) : (f16)0.f;
+      tile[r][four + k] = h[k];
+    }
+    if (row < p.N && col < Kp)  // whole fours
+      *reinterpret_cast<f16x4*>(same + row * p.ld_same + col) = h;
   }
   __syncthreads();
-#pragma unroll 4
-  for (int i = 0; i < 16; ++i) {
-    const int c = wave * 16 + i;
-    if (c0 + c < p.K && r0 + lane < Np) turned[(c0 + c) * p.ld_turned + r0 + lane] = tile[lane][c];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = part + 16 * i;
+    f16x4 h;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) h[k] = tile[four + k][c];
+    if (c0 + c < p.K && r0 + four < Np)
+      *reinterpret_cast<f16x4*>(turned + (c0 + c) * p.ld_turned + r0 + four) = h;
   }
 }
 
@@ -139,6 +191,7 @@ struct OrthoJob {
   };
   static constexpr bool kSymmetric = kMode == kGram || kMode == kPoly;
   static constexpr bool kLast = kMode == kLastTall || kMode == kLastWide;
+  static constexpr int kStaging = 8192;  // bytes of LDS a wavefront
   const OrthoParams& p;
 
   __device__ __forceinline__ int tiles_of_matrix() const {
@@ -181,106 +234,152 @@ struct OrthoJob {
         exists ? (int)((uint32_t)(mr - 1) * (uint32_t)p.lda + (uint32_t)p.cbytes) : 0, kRsrcWord3);
   }
 
-  // 32 rows x 64 columns of 16 bits from LDS (chunk q of row r at q ^ r % 8) to
-  // row r0 of a buffer and column c0.
-  __device__ __forceinline__ void put(const char* stg, char* to, int64_t ld, int r0, int rows,
-                                      int c0, int cols, int lane) const {
+  // Rows m0 .. of a matrix that is stored to: those past `rows` and columns past
+  // `cols` are dropped.
+  struct Target {
+    __amdgpu_buffer_rsrc_t buffer;
+    uint16_t* at;
+    uint32_t ld;  // bytes
+    int rows, cols;
+  };
+  __device__ __forceinline__ Target target(char* base, int64_t batch, int64_t ld, int m0, int most,
+                                           int rows, int cols) const {
+    Target t;
+    t.at = reinterpret_cast<uint16_t*>(base) + batch + m0 * ld;
+    t.ld = (uint32_t)ld * 2;
+    t.rows = rows - m0 < most ? rows - m0 : most;
+    t.cols = cols;
+    t.buffer = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)t.at, 0, (int)((uint32_t)(t.rows - 1) * t.ld + (uint32_t)cols * 2), kRsrcWord3);
+    return t;
+  }
+  // 64 rows x 64 columns of 16 bits from LDS (chunk q of row r at q ^ r % 8) to
+  // row r0 of the target and column c0: all are read before the first is stored.
+  __device__ __forceinline__ void put(const char* stg, const Target& t, int r0, int c0,
+                                      int lane) const {
     const int rrow = lane >> 3, rchunk = lane & 7, col = c0 + rchunk * 8;
+    u32x4 v[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       const int r = i * 8 + rrow;
-      const u32x4 v =
-          *reinterpret_cast<const u32x4*>(stg + r * 128 + ((rchunk ^ (r & 7)) * 16));
-      uint16_t* at = reinterpret_cast<uint16_t*>(to) + (int64_t)(r0 + r) * ld + col;
-      if (r0 + r < rows && col < cols) {
-        if (!kLast || (p.vec && col + 8 <= cols)) {
-          *reinterpret_cast<u32x4*>(at) = v;
-        } else if (col + 8 <= cols) {
-          __builtin_memcpy(at, &v, 16);
+      v[i] = *reinterpret_cast<const u32x4*>(stg + r * 128 + ((rchunk ^ (r & 7)) * 16));
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = i * 8 + rrow;
+      if (!kLast || p.vec) {
+        const uint32_t off = (uint32_t)(r0 + r) * t.ld + (uint32_t)col * 2;
+        __builtin_amdgcn_raw_buffer_store_b128(v[i], t.buffer,
+                                               (int)(col < t.cols ? off : kOutOfRange), 0,
+                                               kNonTemporal);
+      } else if (r0 + r < t.rows) {
+        uint16_t* at = t.at + (int64_t)(r0 + r) * (t.ld / 2) + col;
+        if (col + 8 <= t.cols) {
+          __builtin_memcpy(at, &v[i], 16);
         } else {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            if (col + k < cols) at[k] = (uint16_t)(v[k / 2] >> (16 * (k & 1)));
+            if (col + k < t.cols) at[k] = (uint16_t)(v[i][k / 2] >> (16 * (k & 1)));
         }
       }
     }
   }
 
   // Sums in 64 x 64 blocks: every lane (row l32 of a block of 32, columns 8 q + 4
-  // half + 0..3) rounds its 64 values, which go out by rows and by columns.
+  // half + 0..3) rounds its 64 values in pairs of columns, which go out by rows and
+  // by columns, 8 KiB of LDS at a time. For the columns, neighbouring lanes exchange
+  // one value of each pair, so that a lane holds two rows of one column.
   template <int WI, int WJ>
   __device__ __forceinline__ void store(const Tile& T, const f32x16 (&acc)[WI][WJ], char* stg,
                                         int wn, int wm, int lane) const {
     static_assert(WI % 2 == 0 && WJ % 2 == 0, "blocks of 64 x 64");
     const int half = lane >> 5, l32 = lane & 31;
-    char* out = p.out + T.e * p.out_batch * 2;
-    char* turned = p.turned + T.e * p.turned_batch * 2;
+    const Target out = target(p.out, T.e * p.out_batch, p.ldo, T.m0, BM, p.rows, p.out_cols);
+    const Target turned = target(p.turned, T.e * p.turned_batch, p.ldt, T.n0, BN, p.B,
+                                 p.turned_cols);
     const bool mirror = !kSymmetric || T.m0 != T.n0;
+    // halves of (own pair, neighbour's): an even lane takes the first column of
+    // both, an odd one the second of both, the neighbour's row before its own
+    const uint32_t pick = lane & 1 ? 0x07060302u : 0x01000504u;
 #pragma unroll
     for (int jp = 0; jp < WJ / 2; ++jp)
 #pragma unroll
       for (int ip = 0; ip < WI / 2; ++ip) {
-        const int row0 = T.m0 + wm * (BM / 2) + jp * 64, col0 = T.n0 + wn * (BN / 2) + ip * 64;
-        uint16_t v[2][2][16];  // of block (jp, ip): rows, columns, values
+        const int row0 = wm * (BM / 2) + jp * 64, col0 = wn * (BN / 2) + ip * 64;
+        uint32_t v[2][2][8];  // of block (j, i): pairs of columns
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const int row = row0 + j * 32 + l32, col = col0 + i * 32 + 8 * q + 4 * half;
+              const int row = T.m0 + row0 + j * 32 + l32;
+              const int col = T.n0 + col0 + i * 32 + 8 * q + 4 * half;
               f16 add[4] = {};
-              if constexpr (kMode == kPoly)
-                if (row < p.rows && col < p.out_cols)  // whole fours of padded columns
-                  __builtin_memcpy(add,
-                                   p.act + T.e * p.act_batch + (int64_t)row * p.lda + col * 2, 8);
+              if constexpr (kMode == kPoly) {
+                // whole fours of padded columns; rows and columns past the last
+                // read the first
+                const bool in = row < p.rows && col < p.out_cols;
+                __builtin_memcpy(add, p.act + T.e * p.act_batch +
+                                          (in ? (int64_t)row * p.lda + col * 2 : 0), 8);
+              }
+              float s[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                float s = p.alpha * acc_read(acc[2 * ip + i][2 * jp + j][4 * q + k]);
+                s[k] = acc_read(acc[2 * ip + i][2 * jp + j][4 * q + k]);
+                if constexpr (kMode != kApply) s[k] *= p.alpha;
                 if constexpr (kMode == kPoly) {
-                  s = fmaf(p.beta, to_f32(add[k]), s);
-                  if (row == col + k) s += p.diag;
+                  s[k] = fmaf(p.beta, to_f32(add[k]), s[k]);
+                  s[k] += row == col + k ? p.diag : 0.f;
                 }
-                if constexpr (kLast)
-                  v[j][i][4 * q + k] = __builtin_bit_cast(uint16_t, from_f32<bf16>(s));
-                else
-                  v[j][i][4 * q + k] = __builtin_bit_cast(uint16_t, from_f32<f16>(s));
               }
-            }
-        if constexpr (kMode != kLastWide)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
+              for (int k = 0; k < 2; ++k) v[j][i][2 * q + k] = pack(s[2 * k], s[2 * k + 1]);
+            }
+        if constexpr (kMode != kLastWide) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const u32x2 four = {v[j][i][4 * q] | (uint32_t)v[j][i][4 * q + 1] << 16,
-                                    v[j][i][4 * q + 2] | (uint32_t)v[j][i][4 * q + 3] << 16};
-                *reinterpret_cast<u32x2*>(stg + l32 * 128 + (((i * 4 + q) ^ (l32 & 7)) * 16) +
-                                          half * 8) = four;
-              }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            put(stg, out, p.ldo, row0 + j * 32, p.rows, col0, p.out_cols, lane);
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-          }
+              for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<u32x2*>(stg + (j * 32 + l32) * 128 +
+                                          (((i * 4 + q) ^ (l32 & 7)) * 16) + half * 8) =
+                    u32x2{v[j][i][2 * q], v[j][i][2 * q + 1]};
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          put(stg, out, row0, T.n0 + col0, lane);
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
         if constexpr (kMode != kLastTall)
-          if (mirror)
+          if (mirror) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
               for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                  const int r = 8 * (x >> 2) + 4 * half + (x & 3);
-                  *reinterpret_cast<uint16_t*>(
-                      stg + r * 128 + (((j * 4 + (l32 >> 3)) ^ (r & 7)) * 16) + (l32 & 7) * 2) =
-                      v[j][i][x];
+                for (int x = 0; x < 8; ++x) {
+                  const uint32_t own = v[j][i][x];
+                  const uint32_t next =
+                      (uint32_t)__builtin_amdgcn_mov_dpp((int)own, 0xb1, 0xf, 0xf, true);
+                  const int r = i * 32 + 8 * (x >> 1) + 4 * half + 2 * (x & 1) + (lane & 1);
+                  *reinterpret_cast<uint32_t*>(
+                      stg + r * 128 + (((j * 4 + (l32 >> 3)) ^ (r & 7)) * 16) + (l32 & 6) * 2) =
+                      __builtin_amdgcn_perm(own, next, pick);
                 }
-              __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-              put(stg, turned, p.ldt, col0 + i * 32, p.B, row0, p.turned_cols, lane);
-              __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            put(stg, turned, col0, T.m0 + row0, lane);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          }
       }
+  }
+  __device__ __forceinline__ static uint32_t pack(float a, float b) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef f16 f16x2 __attribute__((ext_vector_type(2)));
+    typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const f32x2 s = {a, b};
+    if constexpr (kLast) return __builtin_bit_cast(uint32_t, __builtin_convertvector(s, bf16x2));
+    else return __builtin_bit_cast(uint32_t, __builtin_convertvector(s, f16x2));
   }
 };
 
@@ -311,6 +410,349 @@ hipError_t product(const OrthoParams& p, int num_cus, hipStream_t st) {
     hipLaunchKernelGGL((ortho_wide_kernel<kMode>), grid, dim3(256), 0, st, p);
   else
     hipLaunchKernelGGL((ortho_ring_kernel<kMode>), grid, dim3(256), 0, st, p);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- small matrices
+// A matrix whose X and A fit in LDS together is one workgroup's: one launch
+// instead of three a step. NB blocks of 32 rows hold m; rows are 16 bytes longer
+// than their values, so that 32 of them, read 16 bytes each, cover all banks.
+//
+// A wavefront's results wait in registers while A is read, then Q replaces A. X is
+// replaced in strips of 32 columns: X'[:, strip] = Q X[:, strip], so a wavefront
+// that holds its strip's fragments may overwrite it. The MFMA's row operand is the
+// index that lies along a stored row (a lane ends with fours of it).
+constexpr int kSmallBlocks = 6;
+constexpr int kSmallWaves = 8;
+// LDS of X and A: so that two matrices share a CU where they can, or all of it.
+constexpr int kSmallBytes = 65536 - 256, kLargeBytes = 163840 - 256;
+// Bytes of a row of n values.
+__host__ __device__ constexpr int small_row(int n) { return 2 * n + 16; }
+
+struct SmallParams {
+  const void* g;
+  bf16* y;
+  ElemType type;
+  int N, K, steps;
+  float up, scale;
+  float c[3 * kOrthoMaxSteps];
+};
+
+constexpr int kSmallThreads = kSmallWaves * kWave;
+
+// Where an element of G [N][K] or y lies in X [m][n]: a walk along G's rows.
+struct Place {
+  int c, at;           // column of G, byte of X
+  int K, next, turn;   // steps to the next column, and to the next row's first
+  __device__ __forceinline__ Place(int e, int N, int K_, int ldx) : K(K_) {
+    const bool wide = N <= K;
+    // e below 2^24: the quotient is off by one at most
+    int r = (int)((float)e * (1.f / (float)K));
+    r -= r * K > e;
+    r += (r + 1) * K <= e;
+    c = e - r * K;
+    at = wide ? r * ldx + c * 2 : c * ldx + r * 2;
+    next = wide ? 2 : ldx;
+    turn = wide ? ldx - K * 2 : 2 - K * ldx;
+  }
+  __device__ __forceinline__ void step() {
+    ++c;
+    at += next;
+    const bool over = c == K;
+    at += over ? turn : 0;
+    c = over ? 0 : c;
+  }
+};
+
+// f(vector of 16 bytes, its first element) for the vectors of g, kHeld of them in
+// flight a lane; the elements behind the last are given one by one.
+template <typename T, typename F>
+__device__ __forceinline__ void small_vectors(const T* g, int size, F f) {
+  constexpr int V = 16 / sizeof(T), kHeld = 4;
+  const int vectors = size / V;
+  for (int i0 = threadIdx.x; i0 < vectors; i0 += kHeld * kSmallThreads) {
+    T e[kHeld][V];
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      const int i = i0 + u * kSmallThreads;
+      __builtin_memcpy(e[u], g + (i < vectors ? i : i0) * V, 16);  // from any address
+    }
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u)
+      if (i0 + u * kSmallThreads < vectors) f(e[u], (i0 + u * kSmallThreads) * V, V);
+  }
+  if ((int)threadIdx.x < size - vectors * V) {
+    const T e[V] = {g[vectors * V + threadIdx.x]};
+    f(e, vectors * V + (int)threadIdx.x, 1);
+  }
+}
+
+// X = f G in LDS, [m][n] (its other values are zero already), f from the norm.
+template <typename T>
+__device__ __forceinline__ void small_load(const T* g, int N, int K, int ldx, double up, char* x,
+                                           double* sums) {
+  constexpr int V = 16 / sizeof(T);
+  const int size = N * K;
+  double sum = 0.0;
+  small_vectors(g, size, [&](const T (&e)[V], int, int) {  // (a lone element: zeros behind)
+#pragma unroll
+    for (int k = 0; k < V; ++k) sum = fma((double)to_f32(e[k]), (double)to_f32(e[k]), sum);
+  });
+#pragma unroll
+  for (int s = 1; s < kWave; s <<= 1) sum += __shfl_xor(sum, s);
+  if (threadIdx.x % kWave == 0) sums[threadIdx.x / kWave] = sum;
+  __syncthreads();
+  sum = 0.0;
+#pragma unroll
+  for (int w = 0; w < kSmallWaves; ++w) sum += sums[w];
+  // in fp32 as two factors, the first a power of two, where f itself could leave
+  // its normal numbers
+  const double f = factor_of(sum, up);
+  const float f0 = f < 0x1p-64 ? 0x1p-64f : 1.f, f1 = (float)(f / (double)f0);
+  small_vectors(g, size, [&](const T (&e)[V], int first, int count) {
+    Place at(first, N, K, ldx);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      if (k < count)
+        *reinterpret_cast<f16*>(x + at.at) = from_f32<f16>(to_f32(e[k]) * f0 * f1);
+      at.step();
+    }
+  });
+}
+
+template <int NB, int kBytes>
+__global__ __launch_bounds__(kSmallThreads, 1) void ortho_small_kernel(SmallParams p) {
+  constexpr int mp = 32 * NB, lda = small_row(mp);
+  constexpr int kBlocks = NB * (NB + 1) / 2, kOwn = (kBlocks + kSmallWaves - 1) / kSmallWaves;
+  __shared__ __attribute__((aligned(16))) char lds[kBytes];
+  __shared__ double sums[kSmallWaves];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int half = lane >> 5, l32 = lane & 31;
+  const bool wide = p.N <= p.K;
+  const int n = wide ? p.K : p.N;
+  const int np = (n + 31) & ~31, ldx = small_row(np), strips = np / 32;
+  char* a = lds;
+  char* x = lds + mp * lda;
+  const int64_t origin = (int64_t)blockIdx.x * p.N * p.K;
+  for (int i = tid * 16; i < mp * ldx; i += kSmallThreads * 16)
+    *reinterpret_cast<u32x4*>(x + i) = u32x4{0, 0, 0, 0};
+  if (p.type == ElemType::kF32)
+    small_load(static_cast<const float*>(p.g) + origin, p.N, p.K, ldx, (double)p.up, x, sums);
+  else if (p.type == ElemType::kBF16)
+    small_load(static_cast<const bf16*>(p.g) + origin, p.N, p.K, ldx, (double)p.up, x, sums);
+  else
+    small_load(static_cast<const f16*>(p.g) + origin, p.N, p.K, ldx, (double)p.up, x, sums);
+  __syncthreads();
+
+  // rows 32 b .. of a matrix in LDS, 16 of their values from k on: an operand
+  auto rows_of = [&](const char* t, int ld, int b, int k) -> f16x8 {
+    return *reinterpret_cast<const f16x8*>(t + (32 * b + l32) * ld + (k + 8 * half) * 2);
+  };
+  // columns 32 s .. of X, its rows 16 k ..: gfx950's transposing LDS read gives lane
+  // i of 16 element i % 4 of the 8 bytes that lanes 4 j + i / 4 address, j = 0..3
+  const int grp = lane >> 4, tr_row = 8 * (grp >> 1) + ((lane >> 2) & 3);
+  const int tr_col = 16 * (grp & 1) + 4 * (lane & 3);
+  auto columns_of = [&](int s, int k) -> f16x8 {
+    const char* at = x + (16 * k + tr_row) * ldx + (32 * s + tr_col) * 2;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_char*)at);
+    const s16x4 hi =
+        __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_char*)(at + 4 * ldx));
+    return __builtin_bit_cast(f16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  auto store4 = [&](char* at, float v0, float v1, float v2, float v3) {
+    const f16x4 h = {from_f32<f16>(v0), from_f32<f16>(v1), from_f32<f16>(v2), from_f32<f16>(v3)};
+    *reinterpret_cast<f16x4*>(at) = h;
+  };
+  const float down = 1.f / (p.up * p.up);
+
+  // this wavefront's blocks of a symmetric matrix, on and below the diagonal; one
+  // past the last repeats it and is not stored
+  int bi[kOwn], bj[kOwn];
+#pragma unroll
+  for (int o = 0; o < kOwn; ++o) {
+    const int t = wave + o * kSmallWaves < kBlocks ? wave + o * kSmallWaves : kBlocks - 1;
+    int i = 0;
+    while ((i + 1) * (i + 2) / 2 <= t) ++i;
+    bi[o] = i;
+    bj[o] = t - i * (i + 1) / 2;
+  }
+  // sum over k of rows bi and bj of t, both fragments of the next 32 values in flight
+  f32x16 acc[kOwn];
+  auto multiply = [&](const char* t, int ld, int count) {
+    f16x8 u[kOwn][2], w[kOwn][2];
+    auto load = [&](int k) {
+#pragma unroll
+      for (int o = 0; o < kOwn; ++o)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          u[o][h] = rows_of(t, ld, bi[o], k + 16 * h);
+          w[o][h] = rows_of(t, ld, bj[o], k + 16 * h);
+        }
+    };
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o) acc[o] = f32x16{};
+    load(0);
+    for (int k = 0; k < count; k += 32) {
+      f16x8 u0[kOwn][2], w0[kOwn][2];
+#pragma unroll
+      for (int o = 0; o < kOwn; ++o)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          u0[o][h] = u[o][h];
+          w0[o][h] = w[o][h];
+        }
+      load(k + 32 < count ? k + 32 : 0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int o = 0; o < kOwn; ++o)
+          acc[o] = __builtin_amdgcn_mfma_f32_32x32x16_f16(u0[o][h], w0[o][h], acc[o], 0, 0, 0);
+    }
+  };
+  // a block to its place and, turned around, to the one across the diagonal
+  auto store_blocks = [&]() {
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o)
+      if (wave + o * kSmallWaves < kBlocks) {
+        char* at = a + (32 * bj[o] + l32) * lda + 64 * bi[o] + 8 * half;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          store4(at + 16 * q, acc[o][4 * q], acc[o][4 * q + 1], acc[o][4 * q + 2],
+                 acc[o][4 * q + 3]);
+        if (bi[o] != bj[o]) {
+          char* across = a + (32 * bi[o] + 4 * half) * lda + (32 * bj[o] + l32) * 2;
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            *reinterpret_cast<f16*>(across + (8 * (v >> 2) + (v & 3)) * lda) =
+                from_f32<f16>(acc[o][v]);
+        }
+      }
+  };
+
+  for (int step = 0; step < p.steps; ++step) {
+    const float ca = p.c[3 * step], cb = p.c[3 * step + 1], cc = p.c[3 * step + 2];
+    // A = X X^T
+    multiply(x, ldx, np);
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[o][v] *= down;
+    store_blocks();
+    __syncthreads();
+    // Q = a I + b A + c A A
+    multiply(a, lda, mp);
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o) {
+      const char* at = a + (32 * bj[o] + l32) * lda + 64 * bi[o] + 8 * half;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f16x4 h = *reinterpret_cast<const f16x4*>(at + 16 * q);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float r = fmaf(cb, to_f32(h[v]), cc * acc[o][4 * q + v]);
+          acc[o][4 * q + v] = bi[o] == bj[o] && l32 == 8 * q + 4 * half + v ? r + ca : r;
+        }
+      }
+    }
+    __syncthreads();
+    store_blocks();
+    __syncthreads();
+    // X' = Q X
+    const bool last = step + 1 == p.steps;
+    const float out = p.scale / p.up;
+    for (int s = wave; s < strips; s += kSmallWaves) {
+      f16x8 col[2 * NB];
+#pragma unroll
+      for (int k = 0; k < 2 * NB; ++k) col[k] = columns_of(s, k);
+      f32x16 r[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) r[b] = f32x16{};
+#pragma unroll
+      for (int k = 0; k < 2 * NB; ++k)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          r[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(col[k], rows_of(a, lda, b, 16 * k), r[b],
+                                                        0, 0, 0);
+      // lane: row 32 b + l32 of X', columns 32 s + 8 q + 4 half + 0..3
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        char* at = x + (32 * b + l32) * ldx + 64 * s + 8 * half;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (!last) {
+            store4(at + 16 * q, r[b][4 * q], r[b][4 * q + 1], r[b][4 * q + 2], r[b][4 * q + 3]);
+          } else {  // y, in X's place
+            const bf16x4 h = {from_f32<bf16>(r[b][4 * q] * out),
+                              from_f32<bf16>(r[b][4 * q + 1] * out),
+                              from_f32<bf16>(r[b][4 * q + 2] * out),
+                              from_f32<bf16>(r[b][4 * q + 3] * out)};
+            *reinterpret_cast<bf16x4*>(at + 16 * q) = h;
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+  // y, 16 bytes a lane
+  constexpr int V = 8;
+  bf16* y = p.y + origin;
+  const int size = p.N * p.K;
+  for (int i = tid * V; i < size; i += kSmallThreads * V) {
+    bf16 h[V];
+    Place at(i, p.N, p.K, ldx);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      h[k] = *reinterpret_cast<const bf16*>(x + (i + k < size ? at.at : 0));
+      at.step();
+    }
+    if (i + V <= size) {
+      __builtin_memcpy(y + i, h, 16);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (i + k < size) y[i + k] = h[k];
+    }
+  }
+}
+
+int small_bytes(int m, int n) {
+  const int mp = (m + 31) / 32 * 32, np = (n + 31) / 32 * 32;
+  return mp * (small_row(mp) + small_row(np));
+}
+bool small_takes(int m, int n) {
+  return m <= 32 * kSmallBlocks && n <= 16384 && small_bytes(m, n) <= kLargeBytes;
+}
+
+hipError_t launch_small(ElemType t, int E, int N, int K, const void* g, void* y, int steps,
+                        const float* coefficients, float scale, float up, hipStream_t st) {
+  SmallParams p{};
+  p.g = g;
+  p.y = static_cast<bf16*>(y);
+  p.type = t;
+  p.N = N;
+  p.K = K;
+  p.steps = steps;
+  p.up = up;
+  p.scale = scale;
+  for (int i = 0; i < 3 * steps; ++i) p.c[i] = coefficients[i];
+  const dim3 grid(E), block(kSmallThreads);
+#define MOE_SMALL(NB)                                                                          \
+  if (small_bytes(m, n) <= kSmallBytes)                                                        \
+    hipLaunchKernelGGL((ortho_small_kernel<NB, kSmallBytes>), grid, block, 0, st, p);          \
+  else                                                                                         \
+    hipLaunchKernelGGL((ortho_small_kernel<NB, kLargeBytes>), grid, block, 0, st, p);          \
+  break
+  const int m = N < K ? N : K, n = N < K ? K : N;
+  switch ((m + 31) / 32) {
+    case 1: MOE_SMALL(1);
+    case 2: MOE_SMALL(2);
+    case 3: MOE_SMALL(3);
+    case 4: MOE_SMALL(4);
+    case 5: MOE_SMALL(5);
+    default: MOE_SMALL(6);
+  }
+#undef MOE_SMALL
   return hipGetLastError();
 }
 
@@ -349,7 +791,7 @@ template <typename T>
 hipError_t split(int E, int N, int K, const void* g, double scale, const Layout& L, char* ws,
                  hipStream_t st) {
   const int64_t size = (int64_t)N * K;
-  int parts = (int)((size + 256 * 8 * 4 - 1) / (256 * 8 * 4));
+  int parts = (int)((size + 256 * 32 - 1) / (256 * 32));
   parts = parts < kNormParts ? parts : kNormParts;
   double* sums = reinterpret_cast<double*>(ws + L.parts);
   hipLaunchKernelGGL(ortho_norm_kernel<T>, dim3(parts, E), dim3(256), 0, st,
@@ -388,6 +830,8 @@ hipError_t launch_orthogonalize(ElemType t, int E, int N, int K, const void* g, 
   while ((int64_t)4 << (2 * s) <= L.m * L.n) ++s;  // 2^s <= sqrt(m n) < 2^(s + 1)
   s = s > 4 ? s - 4 : 0;
   const float up = (float)(1 << s);
+  if (small_takes((int)L.m, (int)L.n))
+    return launch_small(t, E, N, K, g, y, steps, coefficients, scale, up, st);
   hipError_t e = t == ElemType::kF32    ? split<float>(E, N, K, g, up, L, ws, st)
                  : t == ElemType::kBF16 ? split<bf16>(E, N, K, g, up, L, ws, st)
                                         : split<f16>(E, N, K, g, up, L, ws, st);

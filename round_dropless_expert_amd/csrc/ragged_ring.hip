@@ -52,6 +52,7 @@ struct RaggedJob {
     int32_t first_row[kRows ? kRaggedMaxExperts : 1];
     int32_t n_rows[kRows ? kRaggedMaxExperts : 1];
   };
+  static constexpr int kStaging = 4096;
   const RingParams& p;
   Table& table;
 

@@ -6,7 +6,7 @@
 //   locate(t)               tile t, uniform over the workgroup
 //   operands(T, exists, ..) the buffers of a tile's operands; empty ones where
 //                           the tile does not exist
-//   store(T, acc, ..)       the tile's sums, with 4 KiB of LDS a wavefront
+//   store(T, acc, ..)       the tile's sums, with kStaging bytes of LDS a wavefront
 //   p                       row strides lda, ldw, bytes of c in a row cbytes
 #pragma once
 
@@ -147,7 +147,7 @@ __device__ __forceinline__ void ring(Job& job) {
                                  : 0;
   constexpr int kWait = kLoads + (kLoads - kLoadsLast);
   static_assert(kWait <= 63, "vmcnt range");
-  static_assert(kSlotBytes >= 4 * 4096, "the epilogue stages 4 KiB a wavefront in slot 3");
+  static_assert(kSlotBytes >= 4 * Job::kStaging, "the epilogue stages in slot 3");
 
   __shared__ __attribute__((aligned(1024))) char slot0[kSlotBytes];
   __shared__ __attribute__((aligned(1024))) char slot1[kSlotBytes];
@@ -413,7 +413,7 @@ __device__ __forceinline__ void ring(Job& job) {
     // accumulators are read by asm: the nops are the wait states the compiler
     // cannot see.)
     asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
-    job.store(T, acc, slot3 + wave * 4096, wn, wm, lane);
+    job.store(T, acc, slot3 + wave * Job::kStaging, wn, wm, lane);
     // every wavefront's staging reads are done before the next tile's ring
     // writes slot 3
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -450,7 +450,7 @@ __device__ __forceinline__ void wide_ring(Job& job) {
   constexpr int kReads = WI + WJ;
 
   __shared__ __attribute__((aligned(1024))) char slots[2][kSlotBytes];
-  __shared__ __attribute__((aligned(1024))) char staging[4][4096];
+  __shared__ __attribute__((aligned(1024))) char staging[4][Job::kStaging];
   // scales of two slots: 16 bytes a row
   __shared__ __attribute__((aligned(1024))) char scales[kScaled ? 512 * 16 : 16];
 

@@ -19,13 +19,18 @@ namespace moe {
 namespace {
 
 // V elements of a row from column c on, of which n exist.
-template <typename T, bool kVec>
-__device__ __forceinline__ void load_vec(const T* p, int n, float* out) {
-  constexpr int V = 16 / sizeof(T);
+template <typename T>
+struct Vec {
+  static constexpr int V = 16 / sizeof(T);
   union {
     T e[V];
     u32x4 v;
-  } r;
+  };
+};
+template <typename T, bool kVec>
+__device__ __forceinline__ Vec<T> load_vec(const T* p, int n) {
+  constexpr int V = Vec<T>::V;
+  Vec<T> r;
   if (n >= V) {
     if constexpr (kVec)
       r.v = *reinterpret_cast<const u32x4*>(p);
@@ -37,8 +42,7 @@ __device__ __forceinline__ void load_vec(const T* p, int n, float* out) {
     for (int i = 0; i < V; ++i)
       if (i < n) r.e[i] = p[i];
   }
-#pragma unroll
-  for (int i = 0; i < V; ++i) out[i] = to_f32(r.e[i]);
+  return r;
 }
 
 // Stored past the caches, which leaves those to the rows that are read.
@@ -63,38 +67,39 @@ __device__ __forceinline__ void store_vec(T* p, int n, const float* v) {
   }
 }
 
-constexpr int kAtOnce = 4;  // rows of a token in flight
-
-template <typename T, bool kVec>
+// kAtOnce rows of a token in flight. kWhole: every strip is whole (d is a multiple
+// of 64 vectors), so that no load depends on a branch.
+template <typename T, bool kVec, bool kWhole, int kAtOnce>
 __global__ __launch_bounds__(256) void collect_kernel(CollectParams p, int strips) {
-  constexpr int V = 16 / sizeof(T);
+  constexpr int V = Vec<T>::V;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int64_t units = p.T * strips;
   for (int64_t u = (int64_t)blockIdx.x * 4 + wave; u < units; u += (int64_t)gridDim.x * 4) {
     const int64_t t = u / strips;
     const int64_t c = ((u - t * strips) * kWave + lane) * V;
-    const int n = (int)(p.d - c < V ? p.d - c : V);
+    const int n = kWhole ? V : (int)(p.d - c < V ? p.d - c : V);
     const T* z = static_cast<const T*>(p.z) + c;
     float acc[V] = {};
     for (int j0 = 0; j0 < p.k; j0 += kAtOnce) {
-      float v[kAtOnce][V], w[kAtOnce];
+      Vec<T> v[kAtOnce];
+      float w[kAtOnce];
+      bool real[kAtOnce];  // uniform
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j) {
         const bool in = j0 + j < p.k;
         const int64_t a = t * p.k + (in ? j0 + j : 0);
         const int64_t row = in ? p.pos[a] : -1;
-        const bool real = row >= 0 && row < p.rows;
+        real[j] = row >= 0 && row < p.rows;
         w[j] = p.weight ? p.weight[a] : 1.f;
-        if (real) load_vec<T, kVec>(z + row * p.ld_z, n, v[j]);
-        else w[j] = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[j][i] = real ? v[j][i] : 0.f;
+        if (real[j])
+          v[j] = load_vec<T, kVec>(z + row * p.ld_z, n);
       }
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j)
+        if (real[j])
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = fmaf(w[j], v[j][i], acc[i]);
+          for (int i = 0; i < V; ++i) acc[i] = fmaf(w[j], to_f32(v[j].e[i]), acc[i]);
     }
     if (n > 0) store_vec<T, kVec>(static_cast<T*>(p.y) + t * p.ld_y + c, n, acc);
   }
@@ -112,8 +117,7 @@ __global__ __launch_bounds__(256) void spread_kernel(CollectParams p, int strips
     const int64_t c = ((u - t * strips) * kWave + lane) * V;
     const int n = (int)(p.d - c < V ? p.d - c : V);
     if (n <= 0) continue;
-    float g[V];
-    load_vec<T, kVec>(static_cast<const T*>(p.dy) + t * p.ld_y + c, n, g);
+    const Vec<T> g = load_vec<T, kVec>(static_cast<const T*>(p.dy) + t * p.ld_y + c, n);
     for (int j = 0; j < p.k; ++j) {
       const int64_t a = t * p.k + j;
       const int64_t row = p.pos[a];
@@ -121,16 +125,16 @@ __global__ __launch_bounds__(256) void spread_kernel(CollectParams p, int strips
       const float w = p.weight ? p.weight[a] : 1.f;
       float v[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = w * g[i];
+      for (int i = 0; i < V; ++i) v[i] = w * to_f32(g.e[i]);
       store_vec<T, kVec>(static_cast<T*>(p.dz) + row * p.ld_dz + c, n, v);
     }
   }
 }
 
-template <typename T, bool kVec>
+// U vectors of both rows in flight.
+template <typename T, bool kVec, int U>
 __global__ __launch_bounds__(256) void collect_grad_kernel(CollectParams p) {
-  constexpr int V = 16 / sizeof(T);
-  constexpr int U = 2;  // vectors of a row in flight
+  constexpr int V = Vec<T>::V;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int64_t units = p.T * p.k;
@@ -146,30 +150,30 @@ __global__ __launch_bounds__(256) void collect_grad_kernel(CollectParams p) {
     const T* z = static_cast<const T*>(p.z) + row * p.ld_z;
     T* dz = static_cast<T*>(p.dz) + row * p.ld_dz;
     float dot = 0.f;
-    for (int64_t c0 = (int64_t)lane * V; c0 < p.d; c0 += U * kWave * V) {
-      float g[U][V], v[U][V];
+    // whole turns of U vectors a lane without a check, then vector by vector
+    int64_t c0 = (int64_t)lane * V;
+    auto use = [&](const Vec<T>& g, const Vec<T>& v, int64_t c, int n) {
+      float o[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        dot = fmaf(to_f32(v.e[i]), to_f32(g.e[i]), dot);
+        o[i] = w * to_f32(g.e[i]);
+      }
+      if (p.dz) store_vec<T, kVec>(dz + c, n, o);
+    };
+    for (; c0 - (int64_t)lane * V + U * kWave * V <= p.d; c0 += U * kWave * V) {
+      Vec<T> g[U], v[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t c = c0 + u * kWave * V;
-        const int n = (int)(p.d - c < V ? p.d - c : V);
-        if (n > 0) {
-          load_vec<T, kVec>(dy + c, n, g[u]);
-          load_vec<T, kVec>(z + c, n, v[u]);
-        }
+        g[u] = load_vec<T, kVec>(dy + c0 + u * kWave * V, V);
+        v[u] = load_vec<T, kVec>(z + c0 + u * kWave * V, V);
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t c = c0 + u * kWave * V;
-        const int n = (int)(p.d - c < V ? p.d - c : V);
-        if (n > 0) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            dot = fmaf(v[u][i], g[u][i], dot);
-            v[u][i] = w * g[u][i];
-          }
-          if (p.dz) store_vec<T, kVec>(dz + c, n, v[u]);
-        }
-      }
+      for (int u = 0; u < U; ++u) use(g[u], v[u], c0 + u * kWave * V, V);
+    }
+    for (; c0 < p.d; c0 += kWave * V) {
+      const int n = (int)(p.d - c0 < V ? p.d - c0 : V);
+      use(load_vec<T, kVec>(dy + c0, n), load_vec<T, kVec>(z + c0, n), c0, n);
     }
 #pragma unroll
     for (int x = 1; x < kWave; x <<= 1) dot += __shfl_xor(dot, x);
@@ -190,10 +194,20 @@ hipError_t collect(const CollectParams& p, int num_cus, hipStream_t st) {
   const int strips = (int)((p.d + kWave * V - 1) / (kWave * V));
   const bool vec = p.ld_z % V == 0 && p.ld_y % V == 0 && aligned16(p.z) && aligned16(p.y);
   const dim3 grid(grid_of(p.T * strips, num_cus));
-  if (vec)
-    hipLaunchKernelGGL((collect_kernel<T, true>), grid, dim3(256), 0, st, p, strips);
-  else
-    hipLaunchKernelGGL((collect_kernel<T, false>), grid, dim3(256), 0, st, p, strips);
+  const bool whole = p.d % (kWave * V) == 0;
+#define MOE_COLLECT(n)                                                                           \
+  if (vec && whole)                                                                              \
+    hipLaunchKernelGGL((collect_kernel<T, true, true, n>), grid, dim3(256), 0, st, p, strips);   \
+  else if (vec)                                                                                  \
+    hipLaunchKernelGGL((collect_kernel<T, true, false, n>), grid, dim3(256), 0, st, p, strips);  \
+  else                                                                                           \
+    hipLaunchKernelGGL((collect_kernel<T, false, false, n>), grid, dim3(256), 0, st, p, strips)
+  if (p.k <= 4) {
+    MOE_COLLECT(4);
+  } else {
+    MOE_COLLECT(8);
+  }
+#undef MOE_COLLECT
   return hipGetLastError();
 }
 
@@ -214,9 +228,9 @@ hipError_t collect_backward(const CollectParams& p, int num_cus, hipStream_t st)
   vec = vec && p.ld_z % V == 0 && aligned16(p.z);
   const dim3 grid(grid_of(p.T * p.k, num_cus));
   if (vec)
-    hipLaunchKernelGGL((collect_grad_kernel<T, true>), grid, dim3(256), 0, st, p);
+    hipLaunchKernelGGL((collect_grad_kernel<T, true, 4>), grid, dim3(256), 0, st, p);
   else
-    hipLaunchKernelGGL((collect_grad_kernel<T, false>), grid, dim3(256), 0, st, p);
+    hipLaunchKernelGGL((collect_grad_kernel<T, false, 4>), grid, dim3(256), 0, st, p);
   return hipGetLastError();
 }
 

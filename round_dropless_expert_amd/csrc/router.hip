@@ -100,16 +100,37 @@ __device__ __forceinline__ float weight_of(float l, bool use, float top, float s
   return all > 0.f ? scale * (e / all) : 0.f;
 }
 
-// The larger value of the wavefront, and of equal ones that of the lower index.
+__device__ __forceinline__ double read_lane(double v, int lane) {
+  const u32x2 b = __builtin_bit_cast(u32x2, v);
+  const u32x2 o = {(uint32_t)__builtin_amdgcn_readlane((int)b[0], lane),
+                   (uint32_t)__builtin_amdgcn_readlane((int)b[1], lane)};
+  return __builtin_bit_cast(double, o);
+}
+__device__ __forceinline__ void take_first(double& v, int& at, double ov, int oa) {
+  const bool take = (ov > v) | ((ov == v) & (oa < at));
+  v = take ? ov : v;
+  at = take ? oa : at;
+}
+// The larger value of the wavefront, and of equal ones that of the lower index:
+// over rows of 16 lanes by DPP, over the four rows by lane reads.
 template <int x = 1>
 __device__ __forceinline__ void first_of_wave(double& v, int& at) {
-  if constexpr (x < kWave) {
-    const double ov = other_lane<x>(v);
-    const int oa = other_lane<x>(at);
-    const bool take = (ov > v) | ((ov == v) & (oa < at));
-    v = take ? ov : v;
-    at = take ? oa : at;
+  if constexpr (x < 16) {
+    take_first(v, at, other_lane<x>(v), other_lane<x>(at));
     first_of_wave<2 * x>(v, at);
+  } else {
+    double w[4];
+    int a[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      w[r] = read_lane(v, 16 * r);
+      a[r] = __builtin_amdgcn_readlane(at, 16 * r);
+    }
+    take_first(w[0], a[0], w[1], a[1]);
+    take_first(w[2], a[2], w[3], a[3]);
+    take_first(w[0], a[0], w[2], a[2]);
+    v = w[0];
+    at = a[0];
   }
 }
 
@@ -162,17 +183,25 @@ __device__ __forceinline__ void route_exact(const RouterParams& p, int64_t t, do
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     double first = -INFINITY, second = -INFINITY;
-    if (lane < p.groups)
-      for (int i = 0; i < p.per_group; ++i) {
-        const double v = c[lane * p.per_group + i];
-        second = v > first ? first : (v > second ? v : second);
-        first = v > first ? v : first;
+    if (lane < p.groups) {
+      const double* mine = c + lane * p.per_group;
+      for (int i = 0; i < p.per_group; i += 4) {
+        double v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[u] = mine[i + u < p.per_group ? i + u : i];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const double x = i + u < p.per_group ? v[u] : -INFINITY;
+          second = x > first ? first : (x > second ? x : second);
+          first = x > first ? x : first;
+        }
       }
+    }
     double g = p.group_top == 2 && p.per_group > 1 ? first + second : first;
     if (!(g == g)) g = -INFINITY;
     int ahead = 0;  // groups that come before this lane's
     for (int q = 0; q < p.groups; ++q) {
-      const double o = __shfl(g, q);
+      const double o = read_lane(g, q);
       ahead += (o > g) | ((o == g) & (q < lane));
     }
     const uint64_t keep = __builtin_amdgcn_ballot_w64(lane < p.groups && ahead < p.top_groups);
@@ -208,7 +237,8 @@ __device__ __forceinline__ void route_exact(const RouterParams& p, int64_t t, do
         lv = l[m];
         open &= ~(1u << m);
       }
-    lv = __shfl(lv, at & (kWave - 1));
+    lv = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, lv),
+                                                             at & (kWave - 1)));
     if (lane == j) {
       mine = lv;
       chosen = at;

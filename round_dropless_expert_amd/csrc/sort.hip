@@ -42,8 +42,14 @@ __global__ __launch_bounds__(256) void sort_count_kernel(const int32_t* __restri
   for (int b = threadIdx.x; b <= E; b += 256) h[b] = 0;
   __syncthreads();
   const int64_t first = blockIdx.x * chunk, last = first + chunk < n ? first + chunk : n;
-  for (int64_t a = first + threadIdx.x; a < last; a += 256)
-    atomicAdd(&h[bucket_of(idx, a, E)], 1);
+  for (int64_t a = first + threadIdx.x; a < last; a += 256 * 8) {
+    int b[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) b[u] = bucket_of(idx, a + u * 256 < last ? a + u * 256 : a, E);
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (a + u * 256 < last) atomicAdd(&h[b[u]], 1);
+  }
   __syncthreads();
   for (int b = threadIdx.x; b <= E; b += 256)
     counts[(int64_t)blockIdx.x * (E + 1) + b] = h[b];
@@ -58,6 +64,7 @@ __global__ __launch_bounds__(1024) void sort_place_kernel(
   __shared__ int place[kSortWaves][kMaxBuckets];  // counts, then next places
   __shared__ int start[kMaxBuckets];              // totals, then first places
   __shared__ int parts[kSortWaves];
+  __shared__ int shared_sum[kOne ? 1 : 1024], shared_pre[kOne ? 1 : 1024];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int B = E + 1;
   const int64_t first = blockIdx.x * chunk, last = first + chunk < n ? first + chunk : n;
@@ -82,24 +89,36 @@ __global__ __launch_bounds__(1024) void sort_place_kernel(
     if (kOne) total = sum;
   }
   if constexpr (!kOne) {
-    if (on) {
-      int c = 0;
-      for (; c + 8 <= chunks; c += 8) {
-        int v[8];
+    // groups of `width` threads share the chunks; 16 counts of each in flight
+    const int width = B <= 128 ? 128 : B <= 256 ? 256 : B <= 512 ? 512 : 1024;
+    const int b = tid & (width - 1), group = tid / width, groups = 1024 / width;
+    int sum = 0, pre = 0;
+    if (b < B) {
+      int c = group;
+      for (; c + 15 * groups < chunks; c += 16 * groups) {
+        int v[16];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = counts[(int64_t)(c + u) * B + tid];
+        for (int u = 0; u < 16; ++u) v[u] = counts[(int64_t)(c + u * groups) * B + b];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          total += v[u];
-          before += c + u < (int)blockIdx.x ? v[u] : 0;
+        for (int u = 0; u < 16; ++u) {
+          sum += v[u];
+          pre += c + u * groups < (int)blockIdx.x ? v[u] : 0;
         }
       }
-      for (; c < chunks; ++c) {
-        const int v = counts[(int64_t)c * B + tid];
-        total += v;
-        before += c < (int)blockIdx.x ? v : 0;
+      for (; c < chunks; c += groups) {
+        const int v = counts[(int64_t)c * B + b];
+        sum += v;
+        pre += c < (int)blockIdx.x ? v : 0;
       }
     }
+    shared_sum[tid] = sum;
+    shared_pre[tid] = pre;
+    __syncthreads();
+    if (on)
+      for (int g = 0; g < groups; ++g) {
+        total += shared_sum[g * width + tid];
+        before += shared_pre[g * width + tid];
+      }
   }
   // exclusive prefix over the buckets (1024 of them here, the last one by
   // itself where there are 1025)

@@ -600,6 +600,7 @@ __global__ __launch_bounds__(256) void router_kernel(RouterParams p) {
     while (again) {
       const int at = __builtin_ctzll(again) / kLanes;  // a segment of the wavefront
       again &= ~(((1ull << (kLanes - 1) << 1) - 1) << (at * kLanes));
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
       route_exact<(EP + kWave - 1) / kWave>(
           p, step * kTokens + (threadIdx.x / kWave) * (kWave / kLanes) + at, share);

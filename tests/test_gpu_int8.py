@@ -197,3 +197,35 @@ def test_product_extremes(B):
         off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
         B.moe_int8_grouped_gemm(g, off, xq, one, wq, torch.ones(1, N, device="cuda"), y)
         assert (y.double() == float(np.float32(a * b * K))).all()
+
+
+def test_quantize_from_nothing(B):
+    """An index into no rows: zeros and scales of 0."""
+    q, s = quantize(B, torch.empty(0, 40, device="cuda"),
+                    index=torch.zeros(5, dtype=torch.int32, device="cuda"))
+    assert (q == 0).all() and (s == 0).all()
+
+
+@pytest.mark.parametrize("dt", list(DT))
+def test_quantize_the_widest_rows(B, dt):
+    x = randn((2, 2 ** 20), DT[dt], 9)
+    q, s = quantize(B, x)
+    check_codes(q, s, x)
+
+
+def test_product_of_many_experts(B):
+    """1024 experts, most of them without rows."""
+    E, N, K = 1024, 40, 80
+    counts = [(7 * e) % 5 if e % 9 == 0 else 0 for e in range(E)]
+    off = R.offsets_of(counts, 3)
+    rows = int(off[-1]) + 4
+    xq = torch.randint(-127, 128, (rows, K), generator=gen(1), device="cuda", dtype=torch.int8)
+    wq = torch.randint(-127, 128, (E, N, K), generator=gen(2), device="cuda", dtype=torch.int8)
+    one, ws = torch.ones(rows, device="cuda"), torch.ones(E, N, device="cuda")
+    y = torch.full((rows, N), 77.0, device="cuda")
+    B.moe_int8_grouped_gemm(B.grouped(rows, E, N, K, "f32"), torch.from_numpy(off).cuda(), xq, one,
+                            wq, ws, y)
+    ref = torch.full((rows, N), 77.0, dtype=torch.float64)
+    for e, a, b in R.segments(off):
+        ref[a:b] = xq[a:b].double().cpu() @ wq[e].double().cpu().t()
+    assert torch.equal(y.double().cpu(), ref)  # whole numbers below 2^24

@@ -50,7 +50,7 @@ def test_update(B, dt, E, N, K):
     check(update(B, g), g, [U.USUAL] * 5)
 
 
-@pytest.mark.parametrize("N,K", [(96, 160), (160, 96), (256, 256)])
+@pytest.mark.parametrize("N,K", [(96, 160), (160, 96), (256, 256), (300, 260)])
 def test_spectra(B, N, K):
     """A few strong directions; a matrix of low rank; rows and columns of zeros;
     gradients of any size."""
@@ -81,13 +81,15 @@ def test_steps_and_coefficients(B):
     assert float(torch.linalg.matrix_norm(q - eye, 2).max()) <= 2 * 100 ** 0.5 * (2.0 ** -8 + 2.0 ** -10)
 
 
-def test_zeros_and_non_numbers(B):
-    g = torch.randn(5, 70, 50, generator=gen(7), device="cuda")
+# a matrix a workgroup, and tiles of both kinds
+@pytest.mark.parametrize("N,K", [(70, 50), (50, 70), (261, 300), (300, 261), (1300, 1400)])
+def test_zeros_and_non_numbers(B, N, K):
+    g = torch.randn(5, N, K, generator=gen(7), device="cuda")
     good = update(B, g)
     g2 = g.clone()
     g2[0] = 0
     g2[2, 3, 4] = float("inf")
-    g2[4, 60, 49] = float("nan")
+    g2[4, N - 1, K - 1] = float("nan")
     y = update(B, g2)
     assert (y[0] == 0).all()
     assert torch.isnan(y[2]).all() and torch.isnan(y[4]).all()
@@ -113,3 +115,18 @@ def test_large_tiles(B, E, N, K):
     y = update(B, g)
     for e in (0, E - 1):
         check(y[e:e + 1], g[e:e + 1], [U.USUAL] * 5)
+
+
+@pytest.mark.parametrize("N,K", [(16384, 200), (30, 16384), (64, 1100), (1100, 64), (193, 193)])
+def test_long_sides(B, N, K):
+    g = torch.randn(1, N, K, generator=gen(10), device="cuda") * 1e-3
+    check(update(B, g), g, [U.USUAL] * 5)
+
+
+def test_updates_repeat(B):
+    """The same bits again, with other matrices around them."""
+    for N, K in ((100, 120), (260, 400), (1024, 512)):
+        g = torch.randn(6, N, K, generator=gen(11), device="cuda")
+        y = update(B, g)
+        assert torch.equal(y, update(B, g))
+        assert torch.equal(y[2:3], update(B, g[2:3].contiguous()))

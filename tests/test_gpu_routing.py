@@ -66,7 +66,8 @@ SHAPES = [(1, 1, 1, 1), (4, 2, 1, 1), (8, 3, 4, 2), (16, 8, 2, 1), (17, 5, 1, 1)
           (64, 8, 8, 4), (60, 4, 5, 3), (96, 6, 12, 5), (100, 8, 1, 1), (128, 4, 16, 3),
           (160, 6, 8, 3), (192, 8, 6, 2), (256, 8, 8, 4), (256, 1, 1, 1), (256, 8, 256 // 4, 9),
           (384, 8, 1, 1), (512, 8, 16, 4), (513, 10, 27, 20), (1024, 64, 32, 8), (1024, 7, 1, 1),
-          (40, 40, 1, 1), (64, 64, 1, 1), (48, 16, 48, 30)]
+          (40, 40, 1, 1), (64, 64, 1, 1), (48, 16, 48, 30), (12, 4, 12, 5), (16, 2, 16, 2),
+          (96, 8, 3, 1), (512, 8, 2, 1), (192, 1, 12, 1)]
 
 
 @pytest.mark.parametrize("E,k,groups,top", SHAPES)
@@ -137,6 +138,17 @@ def test_route_masked(B, E, k, groups, top):
     live[5] = False  # sigmoids of 1 that fp64 cannot tell apart
     for score in ("softmax", "sigmoid"):
         check_route(B, l[live], k, score, bias, groups, top)
+
+
+def test_route_infinite_bias(B):
+    """An expert that every token takes, one that none does."""
+    l = randn((70, 64), torch.float32, 15)
+    bias = randn((64,), torch.float32, 16, scale=0.05)
+    bias[9] = float("inf")
+    bias[11] = U.NINF
+    for groups, top in ((1, 1), (8, 2)):
+        for score in ("softmax", "sigmoid"):
+            check_route(B, l, 4, score, bias, groups, top)
 
 
 def backward(B, r, logits, idx, dw):

@@ -130,3 +130,37 @@ def test_updates_repeat(B):
         y = update(B, g)
         assert torch.equal(y, update(B, g))
         assert torch.equal(y[2:3], update(B, g[2:3].contiguous()))
+
+
+@pytest.mark.parametrize("E,N,K", [
+    (3, 16, 16), (2, 40, 100), (2, 100, 40), (3, 77, 201), (3, 201, 77), (2, 192, 190),
+    (1, 193, 60), (2, 257, 300), (2, 300, 257), (1, 129, 1000), (1, 1000, 130), (3, 640, 520),
+    (2, 1024, 1536), (2, 1536, 1024), (2, 1411, 1297), (2, 2048, 2048)])
+def test_whole_numbers(B, E, N, K):
+    """Every value exact, so every element of y is known: 4^p elements of +-1 and
+    zeros have the norm 2^p, A and A A are whole numbers over powers of two, and
+    with coefficients that are powers of two Q = (8 I + 2 n1 + n2) / 256 and X' need
+    at most 11 and 24 bits. A first step with Q = I passes X on."""
+    m = min(N, K)
+    p = 1
+    while 4 ** (p + 1) <= min(16 * m, N * K // 2):
+        p += 1
+    g = torch.zeros(E, N * K)
+    r = torch.Generator().manual_seed(N + K)
+    for e in range(E):
+        at = torch.randperm(N * K, generator=r)[: 4 ** p]
+        g[e, at] = torch.randint(0, 2, (4 ** p,), generator=r).float() * 2 - 1
+    g = g.view(E, N, K)
+    x = (g if N <= K else g.transpose(1, 2)).double()
+    n1 = x @ x.transpose(1, 2)
+    q = 8 * torch.eye(m, dtype=torch.float64) + 2 * n1 + n1 @ n1
+    assert q.abs().max() < 2048 and n1.abs().max() < 2048
+    y = q @ x  # 256 2^p times the result
+    assert y.abs().max() < 2 ** 24
+    want = (y if N <= K else y.transpose(1, 2)).float().bfloat16()
+    c = [(8 / 256, 2 * 4.0 ** p / 256, 16.0 ** p / 256)]
+    for dt in (torch.float32, torch.bfloat16):
+        for steps in ([(1.0, 0.0, 0.0)] + c, c):
+            got = update(B, g.to(dt).cuda(), steps=len(steps), coefficients=steps,
+                         scale=256.0 * 2 ** p)
+            assert torch.equal(got.cpu(), want), (dt, len(steps))

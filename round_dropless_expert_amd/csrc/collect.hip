@@ -12,6 +12,11 @@
 // wavefront takes a whole row instead, one (t, j) each: its dot product then
 // stays in the wavefront, and the k reads of dy[t] by neighbouring wavefronts
 // come from the caches.
+//
+// 16384 tokens, 6 experts each, d = 7168, bf16: the sum 282-294 us (1.64 GB, 5.7
+// TB/s; 354 with a branch at each load), both gradients
+// 585-590 us (3.05 GB, 5.2 TB/s); a device copy moves 5.1 TB/s. 5 tokens of 1001
+// values: 3.3 us each.
 #include "ragged_device.hpp"
 #include "router.hpp"
 
@@ -67,9 +72,11 @@ __device__ __forceinline__ void store_vec(T* p, int n, const float* v) {
   }
 }
 
-// kAtOnce rows of a token in flight. kWhole: every strip is whole (d is a multiple
-// of 64 vectors), so that no load depends on a branch.
-template <typename T, bool kVec, bool kWhole, int kAtOnce>
+constexpr int kAtOnce = 4;  // rows of a token in flight (eight are no faster)
+
+// kWhole: every strip is whole (d is a multiple of 64 vectors), so that no load
+// depends on a branch.
+template <typename T, bool kVec, bool kWhole>
 __global__ __launch_bounds__(256) void collect_kernel(CollectParams p, int strips) {
   constexpr int V = Vec<T>::V;
   const int lane = threadIdx.x & (kWave - 1);
@@ -195,19 +202,12 @@ hipError_t collect(const CollectParams& p, int num_cus, hipStream_t st) {
   const bool vec = p.ld_z % V == 0 && p.ld_y % V == 0 && aligned16(p.z) && aligned16(p.y);
   const dim3 grid(grid_of(p.T * strips, num_cus));
   const bool whole = p.d % (kWave * V) == 0;
-#define MOE_COLLECT(n)                                                                           \
-  if (vec && whole)                                                                              \
-    hipLaunchKernelGGL((collect_kernel<T, true, true, n>), grid, dim3(256), 0, st, p, strips);   \
-  else if (vec)                                                                                  \
-    hipLaunchKernelGGL((collect_kernel<T, true, false, n>), grid, dim3(256), 0, st, p, strips);  \
-  else                                                                                           \
-    hipLaunchKernelGGL((collect_kernel<T, false, false, n>), grid, dim3(256), 0, st, p, strips)
-  if (p.k <= 4) {
-    MOE_COLLECT(4);
-  } else {
-    MOE_COLLECT(8);
-  }
-#undef MOE_COLLECT
+  if (vec && whole)
+    hipLaunchKernelGGL((collect_kernel<T, true, true>), grid, dim3(256), 0, st, p, strips);
+  else if (vec)
+    hipLaunchKernelGGL((collect_kernel<T, true, false>), grid, dim3(256), 0, st, p, strips);
+  else
+    hipLaunchKernelGGL((collect_kernel<T, false, false>), grid, dim3(256), 0, st, p, strips);
   return hipGetLastError();
 }
 

@@ -21,6 +21,15 @@
 // as |X| = 1 at the start no element passes 2^10. A and Q need no scale: Q's
 // elements are near a on the diagonal, and an error of 2^-25 in A moves Q by b
 // 2^-25 there.
+//
+// 32 matrices of 2048 x 2048 from fp32, five steps: 5.9-6.0 ms, 5.50 TFLOP with half
+// of the symmetric products, 0.92 PFLOP/s (a library product in fp16 reaches 1.19):
+// 86 + 225 us to divide by the norm, then per step A 300, Q 330 and X' 520 us (the
+// last one 480). MFMA pipes are busy 57-66% of the cycles at 1.7-1.8 GHz, the chip's
+// power limit; the ring's loop alone keeps them busy 76%. The rest is a tile's
+// stores (256 KiB a workgroup and round, all at once: 10 us for one orientation, 17
+// for both) and, for A and Q, the 4.5 rounds of 36 x 32 tiles over 256 CUs. Starting
+// the workgroups a quarter of a tile apart did not help (520 against 530 us).
 #include "ragged_device.hpp"
 #include "ring_body.hpp"
 #include "router.hpp"
@@ -396,7 +405,10 @@ __global__ __launch_bounds__(256, 1) void ortho_ring_kernel(OrthoParams p) {
 }
 
 // 256 x 256 tiles, or 128 x 128 where those keep more CUs at work: turns of the
-// CUs times a tile's area over its relative speed.
+// CUs times a tile's area over its relative speed. All products of an update, with
+// 256 and with 128: 32 of 2048 x 2048 6.1 and 8.3 ms, 4 of them 1.05 and 1.27, one 0.84
+// and 0.40; 32 of 512 x 512 410 and 322 us, 16 of 1024 x 1024 661 and 747; 8 of 1024 x
+// 2048 740 and 702, by product (as here) 617.
 template <int kMode>
 hipError_t product(const OrthoParams& p, int num_cus, hipStream_t st) {
   auto cost = [&](int b, float speed) {
@@ -422,6 +434,10 @@ hipError_t product(const OrthoParams& p, int num_cus, hipStream_t st) {
 // replaced in strips of 32 columns: X'[:, strip] = Q X[:, strip], so a wavefront
 // that holds its strip's fragments may overwrite it. The MFMA's row operand is the
 // index that lies along a stored row (a lane ends with fours of it).
+//
+// Latency: a step of 3 matrices of 201 x 77 takes 2.9 us of its own, reading, the norm
+// and writing 9 (23 us in all; 93 with three launches a step); 32 of 128 x 256 38 (126),
+// 256 of 128 x 128 40 (136), 512 of 192 x 192 176 (520).
 constexpr int kSmallBlocks = 6;
 constexpr int kSmallWaves = 8;
 // LDS of X and A: so that two matrices share a CU where they can, or all of it.

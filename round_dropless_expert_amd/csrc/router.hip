@@ -13,6 +13,13 @@
 // The weights are fp32 functions of the chosen logits, computed so that they
 // neither overflow nor vanish together: a softmax over the chosen logits, or
 // sigmoids with a common factor where all of them are small.
+//
+// Bound by instructions, not by the 19 MB that 16384 tokens of 256 experts have
+// to move (4 us): 1400 vector instructions a wavefront of four tokens for the
+// choice of 8 alone, 1900 with sigmoids, a bias and eight groups. 16384 x 256 in
+// eight groups with a bias: 22-25 us (50 when every token is chosen in fp64), 7 of
+// them the tail of the few tokens that are chosen again; without groups and bias
+// 12 us; one token 6.3 and 4.6 us, of which 2.5 are the launch.
 #include "ragged_device.hpp"
 #include "router.hpp"
 
@@ -632,7 +639,9 @@ hipError_t route_lanes(RouterParams p, int num_cus, hipStream_t st) {
 }
 
 // The fast kernel takes up to 8 of up to 512 experts, with up to 16 groups; the
-// exact one, a wavefront a token, takes the rest.
+// exact one, a wavefront a token, takes the rest (16384 tokens of 256 experts with
+// a bias: 8 of them 20 us, 9 41). Eight lanes a token where few experts leave sixteen
+// idle: 65536 tokens of 32 experts 8.0 and 17.6 us.
 hipError_t route(const RouterParams& p, int num_cus, hipStream_t st) {
   if (p.k <= 8 && p.E <= 512 && p.groups <= 16) {
     if (p.groups == 1 && p.E <= 16) return route_lanes<8, 2>(p, num_cus, st);
@@ -661,7 +670,9 @@ hipError_t route(const RouterParams& p, int num_cus, hipStream_t st) {
 //   sigmoid                 dl_j = s_j (1 - s_j) g_j
 //   softmax                 dl_e = s_e (g_e - sum s g)      for every expert
 // kLanes lanes a token. What the chosen experts get is left in LDS, one value
-// each; then every lane writes its experts' gradients, whole rows at once.
+// each; then every lane writes its experts' gradients, whole rows at once. 16384
+// tokens of 64 experts, 6 chosen, full softmax, fp32: 6.7 us for 9.2 MB (1.8 us at
+// a copy's rate, 2.5 the launch).
 constexpr int kGradTokens = 32;  // of a workgroup at most
 
 template <typename T, int kLanes, bool kVec>

@@ -12,6 +12,10 @@
 // Few assignments are one launch of one workgroup; more are a launch that
 // counts the chunks and one that places them, in which each workgroup sums
 // the counts of the chunks before its own.
+//
+// Latency: 8 assignments of 256 experts 4.4 us, 32768 (64 experts) 8.3, 131072 (256)
+// 10.5 (4 and 9 us the launches, 1.6 MB moved), 524288 17. In one launch and in two:
+// 2048 assignments of 64 experts 5.4 and 7.6 us, 4096 7.1 and 8.0, 8192 10.7 and 8.1.
 #include "ragged_device.hpp"
 #include "router.hpp"
 

@@ -514,7 +514,7 @@ def capacity_for_rounds(cfg: MoeConfig, counts, target_rounds=1,
 
 
 # ---------------------------------------------------------------------------
-# Ragged expert operators (the last section of the header): rows sorted by
+# Ragged expert operators (the header's section of that name): rows sorted by
 # expert, expert e owning the rows offsets[e] .. offsets[e + 1] - 1.
 
 _DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}

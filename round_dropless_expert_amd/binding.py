@@ -596,8 +596,8 @@ def _matrices(t, name, dtype, shape, dev):
     """Address of a contiguous tensor of at least the elements of shape (...,
     height, width) whose trailing dimensions make rows of that width or whole
     matrices (a plain buffer has none): a transposed layout is refused."""
-    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype
-            and t.shape == shape and t.is_contiguous()):
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous() and t.get_device() == dev):
         return t.data_ptr()
     if t is None or isinstance(t, int):
         return t
@@ -630,6 +630,11 @@ def _mat(t, name, dtype, rows, cols, ld, dev):
 
 def _rows_of(t, name, dev):
     """(dtype, rows, width, row stride) of a matrix argument."""
+    if isinstance(t, torch.Tensor) and t.get_device() == dev:
+        shape, stride, dt = t.shape, t.stride(), t.dtype
+        if (len(shape) == 2 and dt in _DTYPES and stride[1] == 1 and shape[0] > 1
+                and stride[0] >= shape[1]):
+            return dt, shape[0], shape[1], stride[0]
     _on_device(t, name, dev)
     if t.dim() != 2:
         raise ValueError(f"{name}: expected a matrix, got {t.dim()} dimensions")
@@ -648,17 +653,29 @@ def _rows_of(t, name, dev):
 
 def _pair_of(t, name, dtype, rows, cols, dev):
     """Address and row stride of a [rows, cols] matrix of any row stride."""
-    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype
-            and t.shape == (rows, cols) and rows > 1):
-        ld, one = t.stride()
-        if one == 1 and ld >= cols:
-            return t.data_ptr(), ld
+    if isinstance(t, torch.Tensor) and t.get_device() == dev:
+        shape, stride = t.shape, t.stride()
+        if (shape == (rows, cols) and t.dtype is dtype and rows > 1 and stride[1] == 1
+                and stride[0] >= cols):
+            return t.data_ptr(), stride[0]
     dt, r, c, ld = _rows_of(t, name, dev)
     if dt is not dtype:
         raise ValueError(f"{name}: dtype {dt}, expected {dtype}")
     if r != rows or c != cols:
         raise ValueError(f"{name}: shape ({r}, {c}), expected ({rows}, {cols})")
     return t.data_ptr(), ld
+
+
+def _rows_like(t, name, dtype, cols, dev):
+    """Address, row stride and rows of a matrix of any number of rows."""
+    if isinstance(t, torch.Tensor) and t.get_device() == dev:
+        shape, stride = t.shape, t.stride()
+        if (len(shape) == 2 and shape[1] == cols and t.dtype is dtype and shape[0] > 1
+                and stride[1] == 1 and stride[0] >= cols):
+            return t.data_ptr(), stride[0], shape[0]
+    _on_device(t, name, dev)
+    rows = t.shape[0] if t.dim() else 0
+    return (*_pair_of(t, name, dtype, rows, cols, dev), rows)
 
 
 def _offsets(offsets, E, dev):
@@ -872,11 +889,15 @@ def moe_sort(idx, E, perm, pos, offsets, ws=None, stream=None):
 
 def _positions(pos, T, dev):
     """k and the address of pos [T, k]."""
+    if isinstance(pos, torch.Tensor) and pos.get_device() == dev:
+        shape = pos.shape
+        if (len(shape) == 2 and shape[0] == T and pos.dtype is torch.int32
+                and pos.is_contiguous()):
+            return shape[1], pos.data_ptr()
     _on_device(pos, "pos", dev)
-    shape = pos.shape
-    if len(shape) != 2 or shape[0] != T:
-        raise ValueError(f"pos: shape {tuple(shape)}, expected ({T}, k)")
-    return shape[1], _dense(pos, "pos", torch.int32, T * shape[1], dev)
+    if pos.dim() != 2 or pos.shape[0] != T:
+        raise ValueError(f"pos: shape {tuple(pos.shape)}, expected ({T}, k)")
+    return pos.shape[1], _dense(pos, "pos", torch.int32, pos.numel(), dev)
 
 
 def moe_collect(z, pos, y, weight=None, stream=None):
@@ -884,9 +905,7 @@ def moe_collect(z, pos, y, weight=None, stream=None):
     [T, k], y [T, d], weight float32 [T, k] (None: all 1)."""
     dev = torch.cuda.current_device()
     dt, T, d, ld_y = _rows_of(y, "y", dev)
-    _on_device(z, "z", dev)
-    rows = z.shape[0] if z.dim() else 0
-    z_ptr, ld_z = _pair_of(z, "z", dt, rows, d, dev)
+    z_ptr, ld_z, rows = _rows_like(z, "z", dt, d, dev)
     k, pos_ptr = _positions(pos, T, dev)
     w_ptr = None if weight is None else _matrices(weight, "weight", torch.float32, (T, k), dev)
     _check(load().moe_collect(_DTYPES[dt], T, k, rows, d, z_ptr, ld_z, pos_ptr, w_ptr,
@@ -900,21 +919,26 @@ def moe_collect_backward(dy, pos, dz=None, weight=None, z=None, dweight=None, st
     dev = torch.cuda.current_device()
     dt, T, d, ld_dy = _rows_of(dy, "dy", dev)
     k, pos_ptr = _positions(pos, T, dev)
-    if dweight is not None and z is None:
-        raise ValueError("dweight needs z")
-    if dz is None and dweight is None:
+    w_ptr = dw_ptr = z_ptr = dz_ptr = None
+    ld_z = ld_dz = rows = 0
+    if dz is not None:
+        dz_ptr, ld_dz, rows = _rows_like(dz, "dz", dt, d, dev)
+    elif dweight is None:
         raise ValueError("neither dz nor dweight is given")
-    some = dz if dz is not None else z
-    _on_device(some, "dz" if dz is not None else "z", dev)
-    rows = some.shape[0] if some.dim() else 0
-    dz_ptr, ld_dz = (None, 0) if dz is None else _pair_of(dz, "dz", dt, rows, d, dev)
-    z_ptr, ld_z = (None, 0) if z is None else _pair_of(z, "z", dt, rows, d, dev)
-    f32 = torch.float32
+    if dweight is not None:
+        if z is None:
+            raise ValueError("dweight needs z")
+        dw_ptr = _matrices(dweight, "dweight", torch.float32, (T, k), dev)
+    if z is not None:
+        if dz is None:
+            z_ptr, ld_z, rows = _rows_like(z, "z", dt, d, dev)
+        else:
+            z_ptr, ld_z = _pair_of(z, "z", dt, rows, d, dev)
+    if weight is not None:
+        w_ptr = _matrices(weight, "weight", torch.float32, (T, k), dev)
     _check(load().moe_collect_backward(
-        _DTYPES[dt], T, k, rows, d, dy.data_ptr(), ld_dy, z_ptr, ld_z, pos_ptr,
-        None if weight is None else _matrices(weight, "weight", f32, (T, k), dev), dz_ptr, ld_dz,
-        None if dweight is None else _matrices(dweight, "dweight", f32, (T, k), dev),
-        _call_stream(stream, dev)))
+        _DTYPES[dt], T, k, rows, d, dy.data_ptr(), ld_dy, z_ptr, ld_z, pos_ptr, w_ptr, dz_ptr,
+        ld_dz, dw_ptr, _call_stream(stream, dev)))
 
 
 def int8_stride(K: int) -> int:
@@ -936,8 +960,9 @@ def moe_int8_quantize(x, codes, scales, index=None, index_div=1, n_rows=None, st
     if index is not None:
         rows = index.numel()
         index_ptr = _dense(index, "index", torch.int32, rows, dev)
+    index_div = index_div if index_div == 1 else _int32(index_div, "index_div")
     _check(load().moe_int8_quantize(
-        _DTYPES[dt], rows, K, x.data_ptr(), ld_x, src, index_ptr, _int32(index_div, "index_div"),
+        _DTYPES[dt], rows, K, x.data_ptr(), ld_x, src, index_ptr, index_div,
         _n_rows(n_rows, dev), _matrices(codes, "codes", torch.int8, (rows, int8_stride(K)), dev),
         _dense(scales, "scales", torch.float32, rows, dev), _call_stream(stream, dev)))
 

@@ -26,9 +26,9 @@ struct RouterParams {
   bool sigmoid, renormalize;
   bool vec;            // rows are 16-byte aligned and hold whole vectors
   bool bias_vec;       // and so is bias
-  int lanes_per_group; // set by the launch
+  int lanes_per_group, group_factor; // set by the launch
 };
-hipError_t launch_router(const RouterParams& p, int num_cus, hipStream_t st);
+hipError_t launch_router(RouterParams p, int num_cus, hipStream_t st);
 
 struct RouterGradParams {
   const void* logits;

@@ -140,6 +140,59 @@ def test_route_masked(B, E, k, groups, top):
         check_route(B, l[live], k, score, bias, groups, top)
 
 
+# E, k, groups, top_groups: both numbers of lanes a token, up to 16 choices, the
+# widest rows without a bias
+WIDE = [(33, 8, 1, 1), (50, 7, 1, 1), (65, 8, 1, 1), (127, 3, 1, 1), (128, 8, 1, 1),
+        (16, 16, 1, 1), (33, 9, 1, 1), (64, 16, 8, 3), (100, 12, 1, 1), (128, 16, 4, 1),
+        (256, 9, 8, 4), (255, 16, 5, 3), (300, 11, 1, 1), (512, 16, 16, 5), (600, 3, 1, 1),
+        (1000, 16, 1, 1), (1023, 8, 1, 1)]
+
+
+@pytest.mark.parametrize("E,k,groups,top", WIDE)
+def test_route_wide(B, E, k, groups, top):
+    T = 333
+    l = randn((T, E), torch.float32, E, 3, 1.5)
+    l[5] = U.NINF
+    l[6, : E - k // 2] = U.NINF
+    l[7] = float("nan")
+    bias = randn((E,), torch.float32, 17, scale=0.05)
+    for i, score in enumerate(("softmax", "sigmoid")):
+        check_route(B, l, k, score, None, groups, top, 1 + i, renormalize=i == 0)
+        check_route(B, l, k, score, bias, groups, top, 2 - i)
+        check_route(B, l.bfloat16(), k, score, None, groups, top, renormalize=i == 1)
+
+
+@pytest.mark.parametrize("E,k,groups,top", [(64, 8, 1, 1), (128, 8, 1, 1), (128, 16, 1, 1),
+                                            (256, 16, 8, 4), (256, 8, 8, 4)])
+def test_route_close_values_wide(B, E, k, groups, top):
+    """Near and true ties where each token is chosen again, alone or with three more
+    of its wavefront."""
+    T = 400
+    l = randn((T, E), torch.float32, 18)
+    l[::3] = l[::3, :1] + 1e-7 * torch.randint(0, 6, (134, E), generator=gen(19),
+                                               device="cuda").float()
+    bias = 1e-7 * torch.randint(0, 3, (E,), generator=gen(20), device="cuda").float()
+    for score in ("softmax", "sigmoid"):
+        check_route(B, l, k, score, bias, groups, top)
+        check_route(B, l, k, score, None, groups, top)
+    l = torch.randint(0, 4, (T, E), generator=gen(21), device="cuda").float()
+    for score in ("softmax", "sigmoid"):
+        check_route(B, l, k, score, torch.zeros(E, device="cuda"), groups, top)
+
+
+def test_route_more_tokens_than_a_grid(B):
+    """Past 2^32 threads: two launches."""
+    T = (32 << 23) + 1001
+    l = torch.empty(T, 2, dtype=torch.bfloat16, device="cuda")
+    l.normal_(generator=gen(22))
+    r = B.router(T, 2, 1, l.dtype, "softmax")
+    idx = torch.full((T, 1), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T, 1), 77.0, device="cuda")
+    B.moe_route(r, l, idx, w)
+    assert torch.equal(idx[:, 0], (l[:, 1] > l[:, 0]).int())
+    assert (w == 1.0).all()
+
+
 def test_route_infinite_bias(B):
     """An expert that every token takes, one that none does."""
     l = randn((70, 64), torch.float32, 15)

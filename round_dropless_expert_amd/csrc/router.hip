@@ -336,8 +336,8 @@ template <int M>
 __global__ __launch_bounds__(256) void router_exact_kernel(RouterParams p) {
   __shared__ double c[4][kWave * M];
   const int wave = threadIdx.x / kWave;
-  for (int64_t t = (int64_t)blockIdx.x * 4 + wave; t < p.T; t += (int64_t)gridDim.x * 4)
-    route_exact<M>(p, t, c[wave], -INFINITY);
+  const int64_t t = (int64_t)blockIdx.x * 4 + wave;
+  if (t < p.T) route_exact<M>(p, t, c[wave], -INFINITY);
 }
 
 // M logits of a token from expert e0 on; those from E on are any of the row's.
@@ -694,6 +694,22 @@ __global__ __launch_bounds__(256) void router_kernel(RouterParams p) {
   }
 }
 
+// launch(p, grid) over ranges of the tokens: a grid has at most 2^32 threads.
+template <typename F>
+hipError_t in_grids(RouterParams p, int tokens, F launch) {
+  const int64_t T = p.T, most = (int64_t)tokens << 23;
+  for (int64_t t0 = 0; t0 < T; t0 += most) {
+    p.T = T - t0 < most ? T - t0 : most;
+    launch(p, dim3((unsigned)((p.T + tokens - 1) / tokens)));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    p.logits = static_cast<const char*>(p.logits) + p.T * p.ld * elem_bytes(p.type);
+    p.idx += p.T * p.k;
+    p.weight += p.T * p.k;
+  }
+  return hipSuccess;
+}
+
 // kScored: with a bias or groups too.
 template <int kLanes, int M, bool kScored = true>
 hipError_t route_lanes(RouterParams p, hipStream_t st) {
@@ -706,16 +722,11 @@ hipError_t route_lanes(RouterParams p, hipStream_t st) {
   }
   const size_t lds = p.groups > 1 ? sizeof(float) * kTokens * choice_at(kLanes * M) : 0;
   const bool scored = kScored && (p.bias || p.groups > 1);
-  // (a grid has at most 2^32 threads)
-  constexpr int64_t kOnce = (int64_t)kTokens << 23;
-  const int64_t T = p.T;
-  for (int64_t t0 = 0; t0 < T; t0 += kOnce) {
-    p.T = T - t0 < kOnce ? T - t0 : kOnce;
-    const dim3 grid((unsigned)((p.T + kTokens - 1) / kTokens));
-#define MOE_ROUTE(K)                                                                        \
-  if (scored)                                                                               \
+  return in_grids(p, kTokens, [&](const RouterParams& p, dim3 grid) {
+#define MOE_ROUTE(K)                                                                         \
+  if (scored)                                                                                \
     hipLaunchKernelGGL((router_kernel<kLanes, M, K, kScored>), grid, dim3(256), lds, st, p); \
-  else                                                                                      \
+  else                                                                                       \
     hipLaunchKernelGGL((router_kernel<kLanes, M, K, false>), grid, dim3(256), lds, st, p)
     if (p.k <= 4) {
       MOE_ROUTE(4);
@@ -725,13 +736,7 @@ hipError_t route_lanes(RouterParams p, hipStream_t st) {
       MOE_ROUTE(kLanes);
     }
 #undef MOE_ROUTE
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    p.logits = static_cast<const char*>(p.logits) + p.T * p.ld * elem_bytes(p.type);
-    p.idx += p.T * p.k;
-    p.weight += p.T * p.k;
-  }
-  return hipSuccess;
+  });
 }
 
 // The fast kernel takes up to 16 of up to 512 experts with up to 16 groups (with
@@ -741,7 +746,7 @@ hipError_t route_lanes(RouterParams p, hipStream_t st) {
 // and 104 (with a bias 67 and 105, but one token 14.5 and 10.4). Eight lanes a token
 // or sixteen, without groups: 65536 tokens, 6 of 64 experts 7.3 and 12, 8 of 128 9.6
 // and 13.6, 4 of 256 15.3 and 14.5.
-hipError_t route(const RouterParams& p, int num_cus, hipStream_t st) {
+hipError_t route(const RouterParams& p, hipStream_t st) {
   if (p.groups == 1 && p.k <= 8) {
     if (p.E <= 16) return route_lanes<8, 2>(p, st);
     if (p.E <= 32) return route_lanes<8, 4>(p, st);
@@ -755,16 +760,15 @@ hipError_t route(const RouterParams& p, int num_cus, hipStream_t st) {
     if (p.E <= 512) return route_lanes<16, 32>(p, st);
     if (p.groups == 1 && !p.bias) return route_lanes<16, 64, false>(p, st);
   }
-  const int64_t blocks = (p.T + 3) / 4, most = (int64_t)num_cus * 32;
-  const dim3 grid((unsigned)(blocks < most ? blocks : most));
+  return in_grids(p, 4, [&](const RouterParams& p, dim3 grid) {
 #define MOE_EXACT(M) hipLaunchKernelGGL((router_exact_kernel<M>), grid, dim3(256), 0, st, p)
-  if (p.E <= 64) MOE_EXACT(1);
-  else if (p.E <= 128) MOE_EXACT(2);
-  else if (p.E <= 256) MOE_EXACT(4);
-  else if (p.E <= 512) MOE_EXACT(8);
-  else MOE_EXACT(16);
+    if (p.E <= 64) MOE_EXACT(1);
+    else if (p.E <= 128) MOE_EXACT(2);
+    else if (p.E <= 256) MOE_EXACT(4);
+    else if (p.E <= 512) MOE_EXACT(8);
+    else MOE_EXACT(16);
 #undef MOE_EXACT
-  return hipGetLastError();
+  });
 }
 
 // ---------------------------------------------------------------- gradient
@@ -912,10 +916,10 @@ hipError_t grad(const RouterGradParams& p, int num_cus, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_router(RouterParams p, int num_cus, hipStream_t st) {
+hipError_t launch_router(RouterParams p, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
   p.group_factor = ((1 << 20) + p.per_group - 1) / p.per_group;
-  return route(p, num_cus, st);
+  return route(p, st);
 }
 
 hipError_t launch_router_backward(ElemType t, const RouterGradParams& p, int num_cus,

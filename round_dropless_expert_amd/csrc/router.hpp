@@ -28,7 +28,7 @@ struct RouterParams {
   bool bias_vec;       // and so is bias
   int lanes_per_group, group_factor; // set by the launch
 };
-hipError_t launch_router(RouterParams p, int num_cus, hipStream_t st);
+hipError_t launch_router(RouterParams p, hipStream_t st);
 
 struct RouterGradParams {
   const void* logits;

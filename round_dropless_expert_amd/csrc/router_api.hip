@@ -100,8 +100,6 @@ moe_status_t moe_route(const moe_router_t* r, const void* logits, const float* b
   if (bias) MOE_TRY(check_ptr(bias, "bias", 4));
   MOE_TRY(check_ptr(idx, "idx", 4));
   MOE_TRY(check_ptr(weight, "weight", 4));
-  int cus = 0;
-  MOE_TRY(api_num_cus(&cus));
   RouterParams p{};
   p.logits = logits;
   p.bias = bias;
@@ -121,7 +119,7 @@ moe_status_t moe_route(const moe_router_t* r, const void* logits, const float* b
   p.renormalize = r->renormalize != 0;
   p.vec = rows_aligned(logits, c.ld, c.type) && r->E * elem_bytes(c.type) % 16 == 0;
   p.bias_vec = rows_aligned(bias, r->E, ElemType::kF32);
-  MOE_LAUNCH(launch_router(p, cus, static_cast<hipStream_t>(stream)), "routing launch");
+  MOE_LAUNCH(launch_router(p, static_cast<hipStream_t>(stream)), "routing launch");
 }
 
 moe_status_t moe_route_backward(const moe_router_t* r, const void* logits, const int32_t* idx,

@@ -13,9 +13,10 @@
 // counts the chunks and one that places them, in which each workgroup sums
 // the counts of the chunks before its own.
 //
-// Latency: 8 assignments of 256 experts 4.4 us, 32768 (64 experts) 8.3, 131072 (256)
-// 10.5 (4 and 9 us the launches, 1.6 MB moved), 524288 17. In one launch and in two:
-// 2048 assignments of 64 experts 5.4 and 7.6 us, 4096 7.1 and 8.0, 8192 10.7 and 8.1.
+// Latency: 8 assignments of 256 experts 4.0 us, 32768 (64 experts) 7.8, 131072 (256)
+// 10.0 (two launches and 1.6 MB moved; every workgroup sums the counts of 64 chunks),
+// 524288 15. In one launch and in two: 2048 assignments of 64 experts 4.5 and 6.4 us,
+// 4096 5.7 and 6.5.
 #include "ragged_device.hpp"
 #include "router.hpp"
 
@@ -24,13 +25,19 @@ namespace {
 
 constexpr int kSortWaves = 16;
 constexpr int kMaxBuckets = kRaggedMaxExperts + 1;
+constexpr int kHeld = 4;               // rounds of 64 assignments a wavefront keeps
 constexpr int64_t kOneChunk = 4096;   // sorted by one workgroup
-constexpr int64_t kChunkLeast = 2048;
-constexpr int64_t kMaxChunks = 256;
 
+// 64 chunks while a chunk's assignments are held, then more of those, and at most 256
+// (every workgroup reads the counts of all). 256 experts, us, by 64, 128 and 256
+// chunks: 131072 assignments 10.0, 11.6, 11.7; 524288 17.5, 15.1, 17.8; 2000000 52, 37,
+// 30.
 int64_t chunk_of(int64_t n) {
-  const int64_t c = (n + kMaxChunks - 1) / kMaxChunks;
-  return c < kChunkLeast ? kChunkLeast : (c + 1023) / 1024 * 1024;
+  const int64_t held = (int64_t)kSortWaves * kWave * kHeld;
+  int64_t c = (n + 63) / 64;
+  if (c > held) c = held;
+  if (c < (n + 255) / 256) c = (n + 255) / 256;
+  return (c + 1023) / 1024 * 1024;
 }
 
 __device__ __forceinline__ int bucket_of(const int32_t* idx, int64_t a, int E) {
@@ -59,7 +66,8 @@ __global__ __launch_bounds__(256) void sort_count_kernel(const int32_t* __restri
     counts[(int64_t)blockIdx.x * (E + 1) + b] = h[b];
 }
 
-// kOne: the only workgroup, which counts for itself.
+// kOne: the only workgroup, which counts for itself. What a wavefront does not hold of
+// its run it reads twice.
 template <bool kOne>
 __global__ __launch_bounds__(1024) void sort_place_kernel(
     const int32_t* __restrict__ idx, int64_t n, int E, int bits, int64_t chunk, int chunks,
@@ -69,34 +77,25 @@ __global__ __launch_bounds__(1024) void sort_place_kernel(
   __shared__ int start[kMaxBuckets];              // totals, then first places
   __shared__ int parts[kSortWaves];
   __shared__ int shared_sum[kOne ? 1 : 1024], shared_pre[kOne ? 1 : 1024];
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int B = E + 1;
   const int64_t first = blockIdx.x * chunk, last = first + chunk < n ? first + chunk : n;
   const int64_t run = (chunk + kSortWaves * kWave - 1) / (kSortWaves * kWave) * kWave;
   const int64_t r0 = first + wave * run, r1 = r0 + run < last ? r0 + run : last;
-  for (int b = tid; b < kSortWaves * B; b += 1024) place[b / B][b % B] = 0;
-  __syncthreads();
-  for (int64_t a = r0 + lane; a < r1; a += kWave) atomicAdd(&place[wave][bucket_of(idx, a, E)], 1);
-  __syncthreads();
-  // per bucket: the wavefronts' counts become prefixes; the total of all
-  // chunks, and of the chunks before this one
-  const bool on = tid < B;
-  int total = 0, before = 0;
-  if (on) {
-    int sum = 0;
+  int held[kHeld];
 #pragma unroll
-    for (int w = 0; w < kSortWaves; ++w) {
-      const int c = place[w][tid];
-      place[w][tid] = sum;
-      sum += c;
-    }
-    if (kOne) total = sum;
+  for (int u = 0; u < kHeld; ++u) {
+    const int64_t a = r0 + u * kWave + lane;
+    held[u] = r0 + u * kWave < r1 ? idx[a < r1 ? a : r0] : 0;
   }
+  // counts of all chunks, and of those before this one
+  int sum = 0, pre = 0, more = 0;
+  // groups of `width` threads share the chunks; 16 counts of each in flight
+  const int width = B <= 128 ? 128 : B <= 256 ? 256 : B <= 512 ? 512 : 1024;
+  const int groups = 1024 / width;
   if constexpr (!kOne) {
-    // groups of `width` threads share the chunks; 16 counts of each in flight
-    const int width = B <= 128 ? 128 : B <= 256 ? 256 : B <= 512 ? 512 : 1024;
-    const int b = tid & (width - 1), group = tid / width, groups = 1024 / width;
-    int sum = 0, pre = 0;
+    const int b = tid & (width - 1), group = tid / width;
     if (b < B) {
       int c = group;
       for (; c + 15 * groups < chunks; c += 16 * groups) {
@@ -117,13 +116,42 @@ __global__ __launch_bounds__(1024) void sort_place_kernel(
     }
     shared_sum[tid] = sum;
     shared_pre[tid] = pre;
-    __syncthreads();
+    if (B > 1024 && wave == 0) {  // bucket 1024
+      for (int c = lane; c < (int)blockIdx.x; c += kWave) more += counts[(int64_t)c * B + 1024];
+      more = wave_inclusive_scan(more);
+      more = __builtin_amdgcn_readlane(more, kWave - 1);
+    }
+  }
+  for (int b = lane; b < B; b += kWave) place[wave][b] = 0;
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u) held[u] = held[u] >= 0 && held[u] < E ? held[u] : E;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u)
+    if (r0 + u * kWave + lane < r1) atomicAdd(&place[wave][held[u]], 1);
+  for (int64_t a = r0 + kHeld * kWave + lane; a < r1; a += kWave)
+    atomicAdd(&place[wave][bucket_of(idx, a, E)], 1);
+  __syncthreads();
+  // per bucket: the wavefronts' counts become prefixes
+  const bool on = tid < B;
+  int total = 0, before = 0;
+  if (on) {
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int c = place[w][tid];
+      place[w][tid] = sum;
+      sum += c;
+    }
+    if (kOne) total = sum;
+  }
+  if constexpr (!kOne)
     if (on)
       for (int g = 0; g < groups; ++g) {
         total += shared_sum[g * width + tid];
         before += shared_pre[g * width + tid];
       }
-  }
   // exclusive prefix over the buckets (1024 of them here, the last one by
   // itself where there are 1025)
   const int incl = wave_inclusive_scan(total);
@@ -138,14 +166,12 @@ __global__ __launch_bounds__(1024) void sort_place_kernel(
     for (int b = tid; b <= E; b += 1024) offsets[b] = start[b];
   // (bucket 1024, of no expert: its prefixes are found here)
   if (B > 1024 && tid == 0) {
-    int sum = 0, more = 0;
+    int sum = 0;
     for (int w = 0; w < kSortWaves; ++w) {
       const int c = place[w][1024];
       place[w][1024] = sum;
       sum += c;
     }
-    if constexpr (!kOne)
-      for (int c = 0; c < (int)blockIdx.x; ++c) more += counts[(int64_t)c * B + 1024];
     start[1024] += more;
   }
   __syncthreads();
@@ -157,10 +183,9 @@ __global__ __launch_bounds__(1024) void sort_place_kernel(
   if (B > 1024 && tid < kSortWaves) place[tid][1024] += start[1024];
   __syncthreads();
   const uint64_t below = ~(~0ull << lane);
-  for (int64_t a0 = r0; a0 < r1; a0 += kWave) {
+  auto put = [&](int64_t a0, int b) {
     const int64_t a = a0 + lane;
     const bool live = a < r1;
-    const int b = live ? bucket_of(idx, a, E) : 0;
     uint64_t same = __builtin_amdgcn_ballot_w64(live);
     for (int bit = 0; bit < bits; ++bit) {
       const bool set = (b >> bit) & 1;
@@ -179,7 +204,12 @@ __global__ __launch_bounds__(1024) void sort_place_kernel(
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-  }
+  };
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u)
+    if (r0 + u * kWave < r1) put(r0 + u * kWave, held[u]);
+  for (int64_t a0 = r0 + kHeld * kWave; a0 < r1; a0 += kWave)
+    put(a0, a0 + lane < r1 ? bucket_of(idx, a0 + lane, E) : 0);
 }
 
 __global__ __launch_bounds__(256) void sort_nothing_kernel(int E, int32_t* offsets) {

@@ -723,10 +723,11 @@ hipError_t route_lanes(RouterParams p, hipStream_t st) {
   const size_t lds = p.groups > 1 ? sizeof(float) * kTokens * choice_at(kLanes * M) : 0;
   const bool scored = kScored && (p.bias || p.groups > 1);
   return in_grids(p, kTokens, [&](const RouterParams& p, dim3 grid) {
+// (few choices of few experts without either are 8 lanes')
 #define MOE_ROUTE(K)                                                                         \
   if (scored)                                                                                \
     hipLaunchKernelGGL((router_kernel<kLanes, M, K, kScored>), grid, dim3(256), lds, st, p); \
-  else                                                                                       \
+  else if constexpr (K > 8 || kLanes == 8 || M >= 16)                                        \
     hipLaunchKernelGGL((router_kernel<kLanes, M, K, false>), grid, dim3(256), lds, st, p)
     if (p.k <= 4) {
       MOE_ROUTE(4);

@@ -45,17 +45,15 @@ struct Vec {
   };
 };
 
-template <typename T, bool kVec>
+// From any address, values past K zero.
+template <typename T>
 __device__ __forceinline__ Vec<T> load_row(const T* row, int64_t c, int64_t K, bool real) {
   constexpr int V = Vec<T>::V;
   Vec<T> r;
   r.v = u32x4{0, 0, 0, 0};
   if (!real) return r;
   if (c + V <= K) {
-    if constexpr (kVec)
-      r.v = *reinterpret_cast<const u32x4*>(row + c);
-    else
-      __builtin_memcpy(&r.v, row + c, 16);
+    __builtin_memcpy(&r.v, row + c, 16);
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -177,7 +175,7 @@ struct Row {
       r.v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(src, v * 16, 0, 0));
       return r;
     } else {
-      return load_row<T, false>(in, (int64_t)v * Vec<T>::V, K, real && v < per);
+      return load_row(in, (int64_t)v * Vec<T>::V, K, real && v < per);
     }
   }
   __device__ __forceinline__ void store(const uint32_t (&w)[Vec<T>::V / 4], int v) const {

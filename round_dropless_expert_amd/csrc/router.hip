@@ -165,8 +165,8 @@ __device__ __forceinline__ void load_wave(const RouterParams& p, int64_t t, int 
 // A token's choice in fp64, by one wavefront. Lane l holds experts l + 64 m.
 // `c` is the wavefront's share of LDS, E doubles (used with groups). `least`: a
 // bound below the k-th choice, -inf if none is known; where few experts reach it,
-// each is placed by the number of them before it (k loops over the wavefront are
-// three times as long).
+// each is placed by the number of them before it, which costs a few instructions
+// an expert; otherwise the wavefront finds its largest k times.
 template <int M>
 __device__ __forceinline__ void route_exact(const RouterParams& p, int64_t t, double* c,
                                             double least) {

@@ -778,45 +778,92 @@ hipError_t route(const RouterParams& p, hipStream_t st) {
 //   sigmoid, renormalised   dl_j = w_j (g_j - sum w g) (1 - s_j)
 //   sigmoid                 dl_j = s_j (1 - s_j) g_j
 //   softmax                 dl_e = s_e (g_e - sum s g)      for every expert
-// kLanes lanes a token. What the chosen experts get is left in LDS, one value
-// each; then every lane writes its experts' gradients, whole rows at once. 16384
-// tokens of 64 experts, 6 chosen, full softmax, fp32: 6.7 us for 9.2 MB (1.8 us at
-// a copy's rate, 2.5 the launch).
+// kLanes lanes a token, all of one wavefront. What the chosen experts get is added to
+// a row of zeros in LDS; then every lane writes its experts' gradients, whole rows at
+// once. With the softmax over all experts (kHeld > 0) a lane keeps its first kHeld
+// vectors of the row, and of their exponentials. 16384 tokens of 64 experts, 6 chosen, full softmax,
+// fp32: 4.3 us for 9.2 MB (1.8 us at a copy's rate, 2.5 the launch; 6.2 with the row
+// read three times and the choices compared with every expert).
 constexpr int kGradTokens = 32;  // of a workgroup at most
 
-template <typename T, int kLanes, bool kVec>
+template <typename T, int kLanes, bool kVec, int kHeld>
 __global__ __launch_bounds__(256) void router_grad_kernel(RouterGradParams p) {
   constexpr int V = kVec ? 16 / sizeof(T) : 1;
   constexpr int kTokens = 256 / kLanes;
+  constexpr bool kFull = kHeld > 0;
   static_assert(kTokens <= kGradTokens, "share of LDS");
   __shared__ float val[kTokens][kRouterMaxTopK];
-  __shared__ int32_t at[kTokens][kRouterMaxTopK];
+  extern __shared__ float rows[];  // [kTokens][E]
   const int q = threadIdx.x % kLanes, seg = threadIdx.x / kLanes;
-  const bool full = !p.sigmoid && !p.renormalize;
   const int64_t steps = (p.T + kTokens - 1) / kTokens;
   for (int64_t step = blockIdx.x; step < steps; step += gridDim.x) {
     const int64_t t = step * kTokens + seg;
     const bool live = t < p.T;
     const T* row = static_cast<const T*>(p.logits) + (live ? t : 0) * p.ld;
     T* out = static_cast<T*>(p.dlogits) + (live ? t : 0) * p.ld;
-    // the softmax over all experts
+    // what comes from memory first, all at once: this lane's choice and its values
+    // of the row (experts own(h, i))
+    int own_e = -1;
+    float own_g = 0.f;
+    if (live && q < p.k) {
+      own_e = p.idx[t * p.k + q];
+      own_g = p.scale * p.dweight[t * p.k + q];
+    }
+    auto order = [] {  // (a token's lanes are of one wavefront)
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    };
+    auto choice = [&](int j) { return j == q ? own_e : p.idx[t * p.k + j]; };
+    auto gradient = [&](int j) { return j == q ? own_g : p.scale * p.dweight[t * p.k + j]; };
+    auto own = [&](int h, int i) { return (h * kLanes + q) * V + i; };
+    float s[kHeld > 0 ? kHeld : 1][V];
     float top = -INFINITY, inv = 0.f;
-    if (full) {
+    // the softmax over all experts
+    if constexpr (kFull) {
+#pragma unroll
+      for (int h = 0; h < kHeld; ++h) {
+        if (kVec && live && own(h, V) <= p.E) {
+          union {
+            T e[V];
+            u32x4 v;
+          } r;
+          r.v = *reinterpret_cast<const u32x4*>(row + own(h, 0));
+#pragma unroll
+          for (int i = 0; i < V; ++i) s[h][i] = to_f32(r.e[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            s[h][i] = live && own(h, i) < p.E ? load_f32(row + own(h, i)) : -INFINITY;
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < kHeld; ++h)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (!no_number(s[h][i])) top = fmaxf(top, s[h][i]);
       if (live)
-        for (int e = q; e < p.E; e += kLanes) {
+        for (int e = kHeld * kLanes * V + q; e < p.E; e += kLanes) {
           const float l = load_f32(row + e);
           if (!no_number(l)) top = fmaxf(top, l);
         }
       top = seg_max<kLanes>(top);
       float sum = 0.f;
+#pragma unroll
+      for (int h = 0; h < kHeld; ++h)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          s[h][i] = exp_below(s[h][i], top);
+          sum += s[h][i];
+        }
       if (live)
-        for (int e = q; e < p.E; e += kLanes) sum += exp_below(load_f32(row + e), top);
+        for (int e = kHeld * kLanes * V + q; e < p.E; e += kLanes)
+          sum += exp_below(load_f32(row + e), top);
       sum = seg_sum<kLanes>(sum);
       inv = sum > 0.f ? 1.f / sum : 0.f;
     } else if (p.renormalize) {
       if (live)
         for (int j = q; j < p.k; j += kLanes) {
-          const int e = p.idx[t * p.k + j];
+          const int e = choice(j);
           if (e >= 0 && e < p.E) {
             const float l = load_f32(row + e);
             if (!no_number(l)) top = fmaxf(top, l);
@@ -828,91 +875,110 @@ __global__ __launch_bounds__(256) void router_grad_kernel(RouterGradParams p) {
     float sum = 0.f, dot = 0.f;
     if (live)
       for (int j = q; j < p.k; j += kLanes) {
-        const int e = p.idx[t * p.k + j];
+        const int e = choice(j);
         const bool in = e >= 0 && e < p.E;
         const float l = in ? load_f32(row + e) : -INFINITY;
-        const float g = p.scale * p.dweight[t * p.k + j];
-        float s;
-        if (full) s = exp_below(l, top) * inv;
-        else if (!p.sigmoid) s = exp_below(l, top);
-        else s = sigmoid_above(l, p.renormalize ? top : 0.f);
-        sum += s;
-        dot += s > 0.f ? s * g : 0.f;
-        at[seg][j] = in ? e : -1;
-        val[seg][j] = s;
+        const float g = gradient(j);
+        float c;
+        if (kFull) c = exp_below(l, top) * inv;
+        else if (!p.sigmoid) c = exp_below(l, top);
+        else c = sigmoid_above(l, p.renormalize ? top : 0.f);
+        sum += c;
+        dot += c > 0.f ? c * g : 0.f;
+        val[seg][j] = c;
       }
+    float* mine = rows + seg * p.E;
+    for (int e = q; e < p.E; e += kLanes) mine[e] = 0.f;
+    order();
     sum = seg_sum<kLanes>(sum);
     dot = seg_sum<kLanes>(dot);
     if (p.renormalize) dot = sum > 0.f ? dot / sum : 0.f;
     if (live)
       for (int j = q; j < p.k; j += kLanes) {
-        const float s = val[seg][j];
-        const float g = p.scale * p.dweight[t * p.k + j];
-        const int e = at[seg][j];
+        const float c = val[seg][j];
+        const float g = gradient(j);
+        const int e = choice(j);
+        const bool in = e >= 0 && e < p.E;
         float v = g;
-        if (!full) {
-          const float l = e >= 0 ? load_f32(row + e) : -INFINITY;
-          v = p.renormalize ? s / sum * (g - dot) : s * g;
+        if (!kFull) {
+          const float l = in ? load_f32(row + e) : -INFINITY;
+          v = p.renormalize ? c / sum * (g - dot) : c * g;
           // 1 - 1 / (1 + e^-l)
           if (p.sigmoid)
             v *= l >= 0.f ? expf(-l) / (1.f + expf(-l)) : 1.f / (1.f + expf(l));
-          if (!(s > 0.f)) v = 0.f;
+          if (!(c > 0.f)) v = 0.f;
         }
-        val[seg][j] = v;
+        if (in) atomicAdd(&mine[e], v);
       }
-    __syncthreads();
+    order();
+    // V experts from e0 on, whose shares before the division are c
+    auto write = [&](int e0, const float (&c)[V]) {
+      const int n = p.E - e0 < V ? p.E - e0 : V;
+      float d[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) d[i] = mine[i < n ? e0 + i : e0];
+      if (kFull)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float share = c[i] * inv;
+          d[i] = share > 0.f ? share * (d[i] - dot) : 0.f;
+        }
+      union {
+        T e[V];
+        u32x4 v;
+      } o;
+#pragma unroll
+      for (int i = 0; i < V; ++i) o.e[i] = from_f32<T>(d[i]);
+      if (kVec && n == V) {
+        *reinterpret_cast<u32x4*>(out + e0) = o.v;
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (i < n) out[e0 + i] = o.e[i];
+      }
+    };
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h)
+      if (live && own(h, 0) < p.E) write(own(h, 0), s[h]);
     if (live)
-      for (int e0 = q * V; e0 < p.E; e0 += kLanes * V) {
-        const int n = p.E - e0 < V ? p.E - e0 : V;
-        float d[V] = {};
-        for (int j = 0; j < p.k; ++j) {
-          const int e = at[seg][j] - e0;
-          const float v = val[seg][j];
+      for (int e0 = own(kHeld, 0); e0 < p.E; e0 += kLanes * V) {
+        float c[V];
 #pragma unroll
-          for (int i = 0; i < V; ++i) d[i] += e == i ? v : 0.f;
-        }
-        if (full)
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float s = i < n ? exp_below(load_f32(row + e0 + i), top) * inv : 0.f;
-            d[i] = s > 0.f ? s * (d[i] - dot) : 0.f;
-          }
-        union {
-          T e[V];
-          u32x4 v;
-        } o;
-#pragma unroll
-        for (int i = 0; i < V; ++i) o.e[i] = from_f32<T>(d[i]);
-        if (kVec && n == V) {
-          *reinterpret_cast<u32x4*>(out + e0) = o.v;
-        } else {
-#pragma unroll
-          for (int i = 0; i < V; ++i)
-            if (i < n) out[e0 + i] = o.e[i];
-        }
+        for (int i = 0; i < V; ++i)
+          c[i] = kFull && e0 + i < p.E ? exp_below(load_f32(row + e0 + i), top) : 0.f;
+        write(e0, c);
       }
-    __syncthreads();
+    order();
   }
 }
 
-template <typename T, int kLanes>
+template <typename T, int kLanes, int kVectors>
 hipError_t grad_lanes(const RouterGradParams& p, int num_cus, hipStream_t st) {
   const int64_t steps = (p.T * kLanes + 255) / 256, most = (int64_t)num_cus * 16;
   const dim3 grid((unsigned)(steps < most ? steps : most));
-  if (p.vec)
-    hipLaunchKernelGGL((router_grad_kernel<T, kLanes, true>), grid, dim3(256), 0, st, p);
-  else
-    hipLaunchKernelGGL((router_grad_kernel<T, kLanes, false>), grid, dim3(256), 0, st, p);
+  const bool full = !p.sigmoid && !p.renormalize;
+  const size_t lds = sizeof(float) * (256 / kLanes) * p.E;
+#define MOE_GRAD(V, H) \
+  hipLaunchKernelGGL((router_grad_kernel<T, kLanes, V, H>), grid, dim3(256), lds, st, p)
+  if (p.vec && full) MOE_GRAD(true, kVectors);
+  else if (p.vec) MOE_GRAD(true, 0);
+  else if (full) MOE_GRAD(false, 4 * kVectors);
+  else MOE_GRAD(false, 0);
+#undef MOE_GRAD
   return hipGetLastError();
 }
 
+// A vector a lane, or four scalars, up to 16 lanes; two of them above (us, by one and
+// two: 16384 tokens of 64 experts in fp32 4.4 and 4.8, of 256 10.1 and 7.4, 65536 of
+// 1024 in bf16 167 and 92).
 template <typename T>
 hipError_t grad(const RouterGradParams& p, int num_cus, hipStream_t st) {
-  const int per = p.vec ? p.E / (int)(16 / sizeof(T)) : p.E;
-  if (per <= 8) return grad_lanes<T, 8>(p, num_cus, st);
-  if (per <= 16) return grad_lanes<T, 16>(p, num_cus, st);
-  if (per <= 32) return grad_lanes<T, 32>(p, num_cus, st);
-  return grad_lanes<T, 64>(p, num_cus, st);
+  const int per = p.vec ? p.E / (int)(16 / sizeof(T)) : (p.E + 3) / 4;
+  if (per <= 8) return grad_lanes<T, 8, 1>(p, num_cus, st);
+  if (per <= 16) return grad_lanes<T, 16, 1>(p, num_cus, st);
+  if (per <= 32) return grad_lanes<T, 16, 2>(p, num_cus, st);
+  if (per <= 64) return grad_lanes<T, 32, 2>(p, num_cus, st);
+  return grad_lanes<T, 64, 2>(p, num_cus, st);
 }
 
 }  // namespace

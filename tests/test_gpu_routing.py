@@ -304,6 +304,38 @@ def test_route_backward_masked(B):
                 assert (err <= 2.0 ** -23 * 700 * g.abs().max()).all()
 
 
+# E with 1 and 2 vectors a lane, rows that are read on past what a lane keeps, and
+# rows of no whole vectors
+@pytest.mark.parametrize("E,pad", [(64, 0), (128, 0), (256, 0), (512, 0), (1024, 0), (62, 5),
+                                   (130, 1), (250, 3), (1000, 5), (1021, 0)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_route_backward_rows(B, E, pad, dt):
+    T, k = 77, min(E, 20)
+    logits = randn((T, E), DT[dt], E, pad, 1.5)
+    for score in ("softmax", "sigmoid"):
+        for ren in (False, True):
+            r, idx, _ = route(B, logits, k, score, renormalize=ren)
+            dw = randn((T, k), torch.float32, 25)
+            g, bound = grad_bound(logits, idx, dw, score, ren, 1.0, DT[dt])
+            check(backward(B, r, logits, idx, dw).double().cpu().numpy(), g.numpy(),
+                  bound.numpy(), f"{score} {ren}")
+
+
+@pytest.mark.parametrize("score,renormalize", [("softmax", True), ("softmax", False),
+                                               ("sigmoid", True), ("sigmoid", False)])
+def test_route_backward_subnormal(B, score, renormalize):
+    """Gradients below fp32's normal numbers are kept: each product and sum of them
+    (one for each choice and four of an expert's own) is off by 2^-150 at most, and
+    what multiplies it afterwards is at most 1."""
+    T, E, k = 9, 64, 6
+    logits = randn((T, E), torch.float32, 26)
+    r, idx, _ = route(B, logits, k, score, renormalize=renormalize)
+    dw = 3e-39 * torch.arange(1, k + 1, device="cuda").float().expand(T, k).contiguous()
+    g, bound = grad_bound(logits, idx, dw, score, renormalize, 1.0, torch.float32)
+    check(backward(B, r, logits, idx, dw).double().cpu().numpy(), g.numpy(),
+          bound.numpy() + (k + 4) * 2.0 ** -150, "dlogits")
+
+
 @pytest.mark.parametrize("n,E", [(1, 1), (5, 8), (64, 64), (63, 1024), (1000, 7), (4096, 256),
                                  (4097, 256), (4096, 1024), (30000, 1024), (131072, 64),
                                  (600001, 300), (2100, 1023)])

@@ -744,12 +744,17 @@ moe_status_t moe_int8_grouped_gemm(const moe_grouped_t *g,
  * by a X + b (X X^T) X + c (X X^T)^2 X; y = scale times the result, bfloat16
  * [E][N][K] (may not overlap g). coefficients: host memory, steps x {a, b, c},
  * or NULL for {3.4445, -4.7750, 2.0315} in every step. The products run on the
- * matrix cores on fp16 values (11 bits), scaled where they are small, with fp32
- * accumulation: each element's error stays below the rounding of y for
- * gradients of usual spectra. A matrix of zeros gives zeros; one with an
- * infinity or a NaN gives NaN throughout. Limits: steps <= 32, N, K <= 16384,
- * E <= 1024; coefficients that let the singular values grow past 32 can leave
- * fp16's range. ws: moe_orthogonalize_workspace_size bytes, 16-byte aligned. */
+ * matrix cores on fp16 values, scaled where they are small, with fp32
+ * accumulation, and X itself is carried in 22 bits: with the usual five steps y is
+ * within bf16's half step, 2^-8, of the exact result's norm, its own rounding
+ * included, for gradients of any rank. More steps multiply what a rounding of X by
+ * 2^-23 leaves in the null spaces of a gradient of low rank by |a| each (485 in
+ * five, 70000 in nine). A
+ * matrix of zeros gives zeros; one with an infinity or a NaN gives NaN throughout.
+ * Limits: steps <= 32, N, K <= 16384, E <= 1024. fp16's range ends where
+ * coefficients let a singular value s of X pass 32, or |b| s^2 + |c| s^4 65504 (s
+ * stays below 1.3 with the usual ones): such matrices can become NaN. ws:
+ * moe_orthogonalize_workspace_size bytes, 16-byte aligned. */
 moe_status_t moe_orthogonalize_workspace_size(int32_t E, int32_t N, int32_t K,
                                               size_t *bytes);
 moe_status_t moe_orthogonalize(int32_t dtype, int32_t E, int32_t N, int32_t K,

@@ -48,3 +48,39 @@ def test_sort_long_runs(B, n, E, mode):
     for got, ref, name in zip((perm[:n], pos[:n], off[: E + 1]), want, ("perm", "pos", "offsets")):
         assert np.array_equal(got.cpu().numpy(), ref), name
     assert perm[n] == -9 and pos[n] == -9 and off[E + 1] == -9
+
+
+def test_gradient_past_4_gib(B):
+    """Each row against its closed form: with sigmoids s of the chosen two, weights w =
+    s / sum s and dweight g, dl_j = w_j (1 - s_j) (g_j - sum w g), zeros elsewhere. Some
+    ten fp32 roundings of values up to 1 and of g up to 2: 20 2^-24."""
+    T, E = 4_300_000, 256  # 4.4 GB of fp32
+    logits = torch.zeros(T, E, device="cuda")
+    logits[-1, 200], logits[-1, 7], logits[-2, 3] = 3.0, 2.0, 1.0
+    idx = torch.tensor([0, 1], dtype=torch.int32, device="cuda").repeat(T, 1)
+    idx[-1] = torch.tensor([200, 7], dtype=torch.int32)
+    idx[-2] = torch.tensor([3, 0], dtype=torch.int32)
+    dweight = torch.tensor([1.0, -2.0], device="cuda").repeat(T, 1)
+    dweight[-1, 0] = 0.5
+    dl = torch.full((T + 1, E), 7.0, device="cuda")
+    B.moe_route_backward(B.router(T, E, 2, "f32", "sigmoid"), logits, idx, dweight, dl[:T])
+
+    def want(l, g):
+        s = torch.sigmoid(torch.tensor(l, dtype=torch.float64))
+        g = torch.tensor(g, dtype=torch.float64)
+        w = s / s.sum()
+        return (w * (1 - s) * (g - (w * g).sum())).tolist()
+
+    near = lambda got, ref: abs(float(got) - ref) <= 20 * 2.0 ** -24
+    for row, experts, l, g in ((-1, (200, 7), (3.0, 2.0), (0.5, -2.0)),
+                               (-2, (3, 0), (1.0, 0.0), (1.0, -2.0))):
+        got = dl[:T][row]
+        for e, v in zip(experts, want(l, g)):
+            assert abs(v) > 0.01 and near(got[e], v), (row, e, float(got[e]), v)
+        assert int((got != 0).sum()) == 2
+    first, second = want((0.0, 0.0), (1.0, -2.0))
+    for part in dl[: T - 2].split(500_000):
+        assert near(part[:, 0].min(), first) and near(part[:, 0].max(), first)
+        assert near(part[:, 1].min(), second) and near(part[:, 1].max(), second)
+        assert int((part[:, 2:] != 0).sum()) == 0
+    assert (dl[T] == 7.0).all()

@@ -84,3 +84,75 @@ def test_gradient_past_4_gib(B):
         assert near(part[:, 1].min(), second) and near(part[:, 1].max(), second)
         assert int((part[:, 2:] != 0).sum()) == 0
     assert (dl[T] == 7.0).all()
+
+
+# kernels of 8 and 16 lanes a token, of few and many choices, and the exact one
+@pytest.mark.parametrize("E,k", [(8, 4), (64, 6), (128, 8), (256, 8), (256, 12), (512, 16), (40, 20),
+                                 (1024, 8), (1024, 33)])
+@pytest.mark.parametrize("biased", [False, True])
+def test_weights_of_extreme_logits(B, E, k, biased):
+    """Rows whose weights are known: equal shares, all of it, or nothing. A share is a
+    sum of ones (exact), a division and a product with the scale: 2^-22 of it covers
+    their three roundings."""
+    inf, nan, scale = float("inf"), float("nan"), 2.5
+    rows = []  # logits, and sigmoids of the chosen ones in the order of the choice
+
+    def row(base, s, *changes):
+        l = torch.full((E,), base)
+        for at, v in changes:
+            l[at] = v
+        rows.append((l, s))
+
+    row(MOST, [1.0] * k)
+    row(-MOST, [0.0] * k)
+    row(inf, [1.0] * k)
+    row(0.0, [0.5] * k)
+    row(-MOST, [1.0] + [0.0] * (k - 1), (E - 1, MOST))
+    row(-inf, [1.0] + [0.0] * (k - 1), (E // 2, MOST))
+    row(nan, [0.0] * k)
+    row(-inf, [1.0, 1.0] + [0.0] * (k - 2), (1, inf), (E - 2, inf))
+    logits = torch.stack([l for l, _ in rows])
+    if biased:  # it is added to scores, and the same for all: no choice changes
+        bias = torch.full((E,), 0.25, device="cuda")
+    T = len(rows)
+    for score in ("softmax", "sigmoid"):
+        for renormalize in (True, False):
+            r = B.router(T, E, k, "f32", score, renormalize=renormalize, scale=scale)
+            idx = torch.empty(T, k, dtype=torch.int32, device="cuda")
+            w = torch.full((T, k), nan, device="cuda")
+            B.moe_route(r, logits.cuda(), idx, w, bias=bias if biased else None)
+            for t, (l, s) in enumerate(rows):
+                what = (score, renormalize, t)
+                chosen = l[idx[t].cpu().long()]
+                live = chosen > -inf
+                top = (chosen == chosen[live].max()) if live.any() else torch.zeros(k).bool()
+                if score == "sigmoid" and not renormalize:
+                    want = torch.tensor(s, dtype=torch.float64)
+                elif renormalize:
+                    want = top.double() / max(int(top.sum()), 1)
+                else:  # the softmax's share of every expert with the largest logit
+                    want = top.double() / max(int((l == chosen[0]).sum()), 1)
+                want = scale * want
+                err = (w[t].double().cpu() - want).abs()
+                assert (err <= 2.0 ** -22 * want).all(), (what, w[t].tolist(), want.tolist())
+
+
+@pytest.mark.parametrize("dt", [torch.float32])
+@pytest.mark.parametrize("E,k", [(64, 6), (256, 8), (700, 17)])
+def test_softmax_of_shifted_logits(B, E, k, dt):
+    """A large number added to all of a token's logits (exactly: all are multiples of
+    1/4 below 2^22) changes no weight by more than the rounding of differences of at most
+    20: an exponent is off by 20 2^-24, a sum of E terms by E 2^-24, and a few steps."""
+    T = 50
+    l = torch.randint(-40, 41, (T, E), generator=gen(E), device="cuda").to(dt) / 4
+    ref = torch.softmax(l.double(), dim=1)
+    for shift in (-3e6, 3e6):
+        for renormalize in (True, False):
+            r = B.router(T, E, k, dt, renormalize=renormalize)
+            idx = torch.empty(T, k, dtype=torch.int32, device="cuda")
+            w = torch.empty(T, k, device="cuda")
+            B.moe_route(r, l + shift, idx, w)
+            want = ref.gather(1, idx.long())
+            if renormalize:
+                want = want / want.sum(dim=1, keepdim=True)
+            assert ((w.double() - want).abs() <= (20 + E + 8) * 2.0 ** -24 * want).all()

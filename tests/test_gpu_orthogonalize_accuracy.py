@@ -123,3 +123,53 @@ def test_one_step_and_other_coefficients(B, N, K):
     own = [(3.0, -3.2, 1.2), (2.5, -2.0, 0.5), (1.875, -1.25, 0.375)]
     assert max(error(B, g, own, steps=3, scale=-0.2)) <= LIMIT
     assert max(error(B, g, [(1.5, -0.5, 0.0)] * 12, steps=12)) <= LIMIT
+
+
+# the longest sides that fit in LDS (half of it, all of it) by blocks of 32 rows, and
+# one more column, which does not
+@pytest.mark.parametrize("m,n", [(32, 960), (30, 2496), (32, 2497), (64, 416), (61, 1184), (64, 1185),
+                                 (96, 224), (90, 736), (96, 737), (128, 480), (120, 481),
+                                 (160, 320), (155, 321), (192, 192), (192, 193)])
+def test_longest_in_lds(B, m, n):
+    g = torch.cat([torch.randn(2, m, n, generator=gen(m)), low_rank((2, m, n), 2, n)])
+    wide = error(B, g)
+    tall = error(B, g.transpose(1, 2).contiguous())
+    assert max(wide + tall) <= LIMIT, (wide, tall)
+
+
+@pytest.mark.parametrize("N,K", [(77, 201), (260, 512)])
+def test_graph_and_repeats(B, N, K):
+    """Captured and replayed with other gradients between eager updates, on one
+    workspace: the bits of the eager call each time."""
+    g = low_rank((3, N, K), 2, 11).cuda()
+    ws = torch.empty(B.orthogonalize_workspace_size(3, N, K), dtype=torch.uint8, device="cuda")
+    y, z = (torch.empty(3, N, K, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    B.moe_orthogonalize(g, y, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.moe_orthogonalize(g, y, ws)
+    for seed in range(4):
+        g.copy_(low_rank((3, N, K), 1 + seed, 20 + seed))
+        B.moe_orthogonalize(g, z, ws)
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, z) and bool(torch.isfinite(y).all())
+
+
+def test_past_4_gib(B):
+    """Matrices whose X^T and its rest lie past 4 GiB of the workspace."""
+    E, N, K = 520, 2048, 2048
+    g = torch.zeros(E, N, K, dtype=torch.bfloat16, device="cuda")
+    few = torch.cat([low_rank((1, N, K), 2, 1), torch.randn(1, N, K, generator=gen(2))])
+    for e in (0, 1):
+        g[e] = g[E - 2 + e] = few[e].cuda()
+    y = torch.full((E, N, K), 3.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.full((B.orthogonalize_workspace_size(E, N, K),), 255, dtype=torch.uint8,
+                    device="cuda")
+    B.moe_orthogonalize(g, y, ws)
+    assert torch.equal(y[0], y[E - 2]) and torch.equal(y[1], y[E - 1])
+    assert (y[2:E - 2] == 0).all()
+    want = exact(g[0].float().cpu(), [U.USUAL] * 5)
+    assert torch.linalg.matrix_norm(y[0].double().cpu() - want) <= LIMIT * torch.linalg.matrix_norm(want)

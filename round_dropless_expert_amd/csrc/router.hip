@@ -6,16 +6,23 @@
 //   idx = experts of the k largest c     w = scale s_idx (/ sum s_idx)
 //
 // The choice is the one that fp64 arithmetic makes. That is dear for every
-// expert and needed for few tokens: the fast kernel scores in fp32, with a
-// bound on its error, and a token in which two values that decide something
-// lie closer than the bound is chosen again by the exact routine.
+// expert and, with fp32 logits, needed for few tokens: the fast kernel scores in
+// fp32, with a bound on its error, and a token in which two values that decide
+// something lie closer than the bound is chosen again by the exact routine. Equal
+// values count as close, though the keys order them already, so the time depends on
+// the data: with 16-bit logits and a bias that is the same for all experts (normal
+// logits of deviation 1.5, 8 of 256) 37% of the tokens hold equal values in bf16, 5% in
+// fp16. 16384 tokens, us, with a bias of random values and with one of zeros: 8 of 256
+// experts in eight groups, fp32 13.7 and 13.7, bf16 14.4 and 29.7, fp16 13.0 and 18.4;
+// without groups 10.8 and 10.7, 10.9 and 24.5, 11.0 and 16.4; 6 of 64 in bf16 5.9 and
+// 13.2.
 //
 // The weights are fp32 functions of the chosen logits, computed so that they
 // neither overflow nor vanish together: a softmax over the chosen logits, or
 // sigmoids with a common factor where all of them are small.
 //
 // Bound by instructions, not by the 19 MB that 16384 tokens of 256 experts have
-// to move (4 us): 16384 x 256 in eight groups with a bias 13 us (44 when every token
+// to move (4 us): 16384 x 256 in eight groups with a bias 13-14 us (44 when every token
 // is chosen in fp64), without groups and bias 6; one token 4.3 and 2.7 us, of which
 // 2.4 are the launch. A workgroup takes 16 or 32 tokens and ends: with a loop over
 // more of them the compiler kept the loop's constants in 249 registers a lane, not
@@ -744,7 +751,9 @@ hipError_t route_lanes(RouterParams p, hipStream_t st) {
 // neither bias nor groups, of up to 1024); the exact one, a wavefront a token, takes
 // the rest. In us, fast and exact: 16384 tokens, 9 of 256 experts 8.2 and 38, with a
 // bias 13 and 38, and groups 17 and 44; 16 of 512 with a bias 34 and 91; 8 of 1024 26
-// and 104 (with a bias 67 and 105, but one token 14.5 and 10.4). Eight lanes a token
+// and 104. More than 512 experts with a bias go to the exact one at every number of
+// tokens, which is the slower one for many: 16384 tokens 67 and 91-105, one 14.5 and
+// 10.4 (1024 tokens by the exact one 13.6). Eight lanes a token
 // or sixteen, without groups: 65536 tokens, 6 of 64 experts 7.3 and 12, 8 of 128 9.6
 // and 13.6, 4 of 256 15.3 and 14.5.
 hipError_t route(const RouterParams& p, hipStream_t st) {
@@ -783,7 +792,10 @@ hipError_t route(const RouterParams& p, hipStream_t st) {
 // once. With the softmax over all experts (kHeld > 0) a lane keeps its first kHeld
 // vectors of the row, and of their exponentials. 16384 tokens of 64 experts, 6 chosen, full softmax,
 // fp32: 4.3 us for 9.2 MB (1.8 us at a copy's rate, 2.5 the launch; 6.2 with the row
-// read three times and the choices compared with every expert).
+// read three times and the choices compared with every expert). Wide rows are bound by
+// instructions: 65536 of 1024 in bf16, full softmax, 91 us for 268 MB (53 at a copy's
+// rate), 711 vector instructions a token, the exponentials and the row in LDS, which
+// keep the vector units busy 98% of the cycles.
 constexpr int kGradTokens = 32;  // of a workgroup at most
 
 template <typename T, int kLanes, bool kVec, int kHeld>
